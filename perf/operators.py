@@ -157,7 +157,8 @@ def prepare(case, seed):
         if op == "ckpt" or case.get("ckpt"):
             s["codes"] = _empty(rows, cols, torch.float8_e4m3fn)
             s["scales"] = torch.empty((rows, -(-cols // GROUP)), dtype=torch.uint8, device="cuda")
-            s["back"] = torch.empty_like(s["x"])
+            # what the norm's checkpoint stands for comes back in the matrix cores' type, which holds it exactly
+            s["back"] = torch.empty_like(s["x"], dtype=dtype if op == "ckpt" else torch.bfloat16)
         return s
     if op == "wgrad":
         tokens, topk, experts, n, k = (case[m] for m in ("tokens", "topk", "experts", "n", "k"))
@@ -263,7 +264,7 @@ def _plain(s):
         y = (xc * rstd * s["weight"].float() + s["bias"].float()).to(s["x"].dtype)
         out = {"y": y, "mean": mean[:, 0], "rstd": rstd[:, 0]}
         if case["ckpt"]:
-            out["kept"] = _values(*_quantize(y)).to(y.dtype)
+            out["kept"] = _values(*_quantize(y)).to(torch.bfloat16)
         return out
     if op == "norm_bwd":
         dy = s["dy"].float()
@@ -357,7 +358,7 @@ def work(case):
         n, kept = case["rows"] * case["cols"], case["rows"] * (case["cols"] + -(-case["cols"] // GROUP))
         if op == "norm_fwd":
             # with a checkpoint: written, read again and returned as values
-            return {"bytes": 2 * n * es + 2 * case["cols"] * es + 8 * case["rows"] + (2 * kept + n * es if case["ckpt"] else 0),
+            return {"bytes": 2 * n * es + 2 * case["cols"] * es + 8 * case["rows"] + (2 * kept + 2 * n if case["ckpt"] else 0),
                     "flops": 8 * n}
         if op == "norm_bwd":
             return {"bytes": 3 * n * es + 3 * case["cols"] * es + 8 * case["rows"], "flops": 14 * n}
