@@ -210,6 +210,9 @@ muon_status muon_workspace_min_size(const muon_mat *descs, int32_t n_mats, uint3
  * such a call returns MUON_ERR_ALIAS. */
 muon_status muon_set_workspace(void *device_ptr, size_t bytes);
 
+/* The workspace set on this thread ((NULL, 0) if none). */
+muon_status muon_get_workspace(void **device_ptr, size_t *bytes);
+
 /* Options used by muon_step (and eps by muon_ns_batched) on this thread.
  * Defaults: iters 5, coeffs {3.4445, -4.7750, 2.0315}, eps 1e-7,
  * mode MUON_NS_FULL | MUON_PACK_COST | MUON_AA_PLAIN. coeffs NULL keeps the
@@ -298,6 +301,141 @@ muon_status muon_adamw_step(const muon_mat *params, const muon_mat *grads, const
 #define MUON_PLACE_LPT 1u
 muon_status muon_place(const double *costs, int32_t n_mats, int32_t ranks, uint32_t policy,
                        int32_t *owner, double *load, double *imbalance);
+
+/* ---------------------------------------------------------------------------
+ * Training operators: what stands between the activations of an expert layer
+ * and the gradients that muon_step consumes. Layer norm with its backward
+ * pass, activation checkpoints in 8 bits and the weight gradients read from
+ * them, expert routing with its balance loss and backward pass.
+ *
+ * The conventions above hold, with these additions:
+ *   - Matrices may have no rows (their data may then be NULL); outputs that
+ *     sum over rows are then written as zeros.
+ *   - Any pitch and any alignment to the element size run the same kernels.
+ *   - Sums, statistics and softmax are float32; each result is rounded once.
+ *     The order of every sum is fixed: the same inputs give the same bits.
+ *   - An operand named NULL-able may be NULL where its comment says so.
+ *   - Their launches are not recorded by muon_set_phase_timing.
+ *   - Scratch is the thread's workspace, of the size that the matching
+ *     *_workspace_size function gives (0 bytes: none needs to be set).
+ *     MUON_ERR_HIP also reports that the host ran out of memory.
+ */
+
+/* An activation checkpoint: rows x cols values as e4m3 codes (one byte, OCP
+ * FP8: largest 448, no infinities), row pitch ld_codes, and for each 128
+ * columns of a row (the last group may be shorter) one scale byte b, row
+ * pitch ld_scales >= ceil(cols / 128). A value is code * 2^(b - 127). */
+typedef struct muon_ckpt {
+  void *codes;
+  void *scales;
+  int64_t rows;
+  int64_t cols;
+  int64_t ld_codes;
+  int64_t ld_scales;
+} muon_ckpt;
+
+/*
+ * Layer norm over the columns of x: per row mean = sum x / cols,
+ * rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ * y = (x - mean) rstd weight + bias.
+ *   x, y          same shape and dtype, cols <= 32768; y may not overlap x.
+ *   mean, rstd    float32 vectors of rows entries (NULL-able).
+ *   weight, bias  1 x cols, one dtype, which may differ from x's (NULL-able:
+ *                 1 and 0).
+ *   eps           finite, >= 0.
+ *   ckpt          NULL, or receives the checkpoint of y as stored (what
+ *                 muon_ckpt_save(y) writes), in the same pass.
+ */
+muon_status muon_layernorm_forward(const muon_mat *x, const muon_mat *y, float *mean, float *rstd,
+                                   const muon_mat *weight, const muon_mat *bias, float eps,
+                                   const muon_ckpt *ckpt);
+
+/*
+ * Its backward pass: with xh = (x - mean) rstd and h = dy weight,
+ *   dx = rstd (h - mean(h) - xh mean(h xh)) (row means),
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy.
+ *   dy, x, dx       same shape and dtype; dx overlaps neither.
+ *   mean, rstd      as the forward pass wrote them.
+ *   weight          NULL-able (1);  dweight, dbias  1 x cols, overwritten, in
+ *                   weight's dtype (NULL-able: not computed).
+ * Workspace: muon_layernorm_workspace_size (none when dweight and dbias are
+ * NULL).
+ */
+muon_status muon_layernorm_backward(const muon_mat *dy, const muon_mat *x, const float *mean,
+                                    const float *rstd, const muon_mat *dx, const muon_mat *weight,
+                                    const muon_mat *dweight, const muon_mat *dbias);
+muon_status muon_layernorm_workspace_size(int64_t rows, int64_t cols, size_t *bytes);
+
+/*
+ * Saves x as a checkpoint: per group of 128 columns the smallest power of two
+ * 2^(b - 127) >= 2^-127 with max |x| <= 448 * 2^(b - 127) over the group's
+ * finite values, and the values over it, rounded to the nearest code (ties to
+ * even). NaN and infinities become NaN codes and leave the scale alone.
+ */
+muon_status muon_ckpt_save(const muon_mat *x, const muon_ckpt *ckpt);
+
+/* Loads a checkpoint's values into out. Exact, with these ends: bf16 rounds
+ * below 2^-133, and a value of 2^128 (which the largest floats round to) is an
+ * infinity. */
+muon_status muon_ckpt_load(const muon_ckpt *ckpt, const muon_mat *out);
+
+/*
+ * Weight gradients of a group of expert layers, from the checkpoint of their
+ * input:  grad_g[n, k] = sum over offsets[g] <= s < offsets[g + 1] of
+ *   dy[s, n] * x[rows[s] / rows_per_token, k].
+ *   dy        slots x n, in slot order; bf16 (products of bf16 values with
+ *             float32 sums) or float32 (products exact in float32).
+ *   x         tokens x k.
+ *   grads     descriptor of the first group's n x k gradient, dy's dtype;
+ *             group g's lies g * group_stride elements further. Overwritten;
+ *             zeros for an empty group.
+ *   offsets   device, n_groups + 1 ascending int32 (NULL with one group: every
+ *             slot). Values outside [0, slots] count as the nearest bound.
+ *   rows      device, int32 per slot (NULL: rows[s] = s). A slot whose token
+ *             lies outside x contributes nothing.
+ * offsets and rows are what muon_route_forward writes, with rows_per_token =
+ * topk. Workspace: muon_ckpt_weight_grad_workspace_size.
+ */
+muon_status muon_ckpt_weight_grad(const muon_mat *dy, const muon_ckpt *x, const muon_mat *grads,
+                                  int64_t group_stride, int32_t n_groups, const int32_t *offsets,
+                                  const int32_t *rows, int32_t rows_per_token);
+muon_status muon_ckpt_weight_grad_workspace_size(int32_t dtype, int64_t slots, int64_t n, int64_t k,
+                                                 int64_t groups, size_t *bytes);
+
+/*
+ * Routing of tokens to experts. Per token (row of logits) p = softmax over
+ * the experts; the choice is the topk largest logits, the lower index first
+ * among equals; -inf and NaN are never chosen, so that a token may have
+ * fewer choices, or (masked wholly) none.
+ *   logits   tokens x experts, experts <= 1024, topk <= min(experts, 32).
+ *   indices  tokens x topk int32, by falling logit; -1 where nothing is left.
+ *   weights  tokens x topk float32: p of the choice, with renormalize != 0
+ *            over the sum of the token's chosen p; 0 where nothing is left.
+ *   counts   experts + 1 int32: how many slots chose each expert, then n, the
+ *            number of tokens with a logit above -inf.
+ *   offsets  experts + 1 int32: exclusive sums of the counts.
+ *   rows     tokens * topk int32: the slots (token * topk + choice) in expert
+ *            order, ascending within an expert; -1 behind the last.
+ *   loss     one float32: alpha experts / (topk n) * sum over experts of
+ *            counts_e * (sum over tokens of p_te) / n  (n at least 1).
+ * All contiguous. Workspace: muon_route_workspace_size.
+ */
+muon_status muon_route_forward(const muon_mat *logits, int32_t topk, int32_t renormalize, float alpha,
+                               int32_t *indices, float *weights, int32_t *counts, int32_t *offsets,
+                               int32_t *rows, float *loss);
+muon_status muon_route_workspace_size(int64_t tokens, int64_t experts, int32_t topk, size_t *bytes);
+
+/*
+ * Its backward pass: the gradient of loss * dloss + sum(weights * dweights)
+ * with respect to the logits, the choice and the counts held fixed.
+ *   indices, counts  as the forward pass wrote them.
+ *   dweights         tokens x topk float32 (NULL-able: 0).
+ *   dloss            one float32 (NULL-able: 0).
+ *   dlogits          the shape and dtype of logits, overwritten.
+ */
+muon_status muon_route_backward(const muon_mat *logits, int32_t topk, int32_t renormalize, float alpha,
+                                const int32_t *indices, const int32_t *counts, const float *dweights,
+                                const float *dloss, const muon_mat *dlogits);
 
 #ifdef __cplusplus
 }

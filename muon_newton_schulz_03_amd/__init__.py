@@ -45,8 +45,12 @@ EXPORTED = (
     "muon_ns_batched", "muon_step", "muon_set_stream", "muon_workspace_size",
     "muon_workspace_min_size", "muon_set_workspace", "muon_set_step_options",
     "muon_last_error", "muon_plan_info", "muon_set_phase_timing", "muon_phase_times",
-    "muon_place", "muon_adamw_step", "muon_step_noalloc",
+    "muon_place", "muon_adamw_step", "muon_step_noalloc", "muon_get_workspace",
+    "muon_layernorm_forward", "muon_layernorm_backward", "muon_layernorm_workspace_size",
+    "muon_ckpt_save", "muon_ckpt_load", "muon_ckpt_weight_grad", "muon_ckpt_weight_grad_workspace_size",
+    "muon_route_forward", "muon_route_backward", "muon_route_workspace_size",
 )
+MUON_CKPT_GROUP = 128  # columns that share one scale byte of a checkpoint
 MUON_NOALLOC_SCRATCH_BYTES = 256 << 20
 PHASES = ("prep", "norm", "gram", "aa", "bx", "finish", "adamw", "reduce")
 
@@ -65,6 +69,17 @@ class muon_mat(ctypes.Structure):
         ("ld", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
         ("col_blocks", ctypes.c_int32),
+    ]
+
+
+class muon_ckpt(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld_codes", ctypes.c_int64),
+        ("ld_scales", ctypes.c_int64),
     ]
 
 
@@ -103,7 +118,23 @@ def load_library(path=LIB_PATH):
         "muon_place": ([ctypes.POINTER(ctypes.c_double), ctypes.c_int32, ctypes.c_int32, ctypes.c_uint32,
                         ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double),
                         ctypes.POINTER(ctypes.c_double)], ctypes.c_int),
+        "muon_get_workspace": ([ctypes.POINTER(ctypes.c_void_p), sz], ctypes.c_int),
     }
+    # the training operators take packed descriptors (bytes) where the header has struct pointers
+    p, i32, i64, f = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    for name, args in {
+        "muon_layernorm_forward": [p, p, p, p, p, p, f, p],
+        "muon_layernorm_backward": [p] * 8,
+        "muon_layernorm_workspace_size": [i64, i64, sz],
+        "muon_ckpt_save": [p, p],
+        "muon_ckpt_load": [p, p],
+        "muon_ckpt_weight_grad": [p, p, p, i64, i32, p, p, i32],
+        "muon_ckpt_weight_grad_workspace_size": [i32, i64, i64, i64, i64, sz],
+        "muon_route_forward": [p, i32, i32, f, p, p, p, p, p, p],
+        "muon_route_workspace_size": [i64, i64, i32, sz],
+        "muon_route_backward": [p, i32, i32, f, p, p, p, p, p],
+    }.items():
+        sigs[name] = (args, ctypes.c_int)
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -328,3 +359,272 @@ def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr=1e-3, beta1=0.9, beta
     muon_set_stream(None)
     _check(lib().muon_adamw_step(mats(W), mats(G), mats(Mo), mats(V), len(W), lr, beta1, beta2, eps,
                                  weight_decay, step))
+
+
+# ---------------------------------------------------------------------------
+# training operators
+# ---------------------------------------------------------------------------
+
+import struct as _struct  # noqa: E402
+
+_MAT = _struct.Struct("=Qqqqii").pack   # muon_mat: data, rows, cols, ld, dtype, col_blocks
+_CKPT = _struct.Struct("=QQqqqq").pack  # muon_ckpt
+_codes = None
+
+
+def _on_gpu(name, t, device):
+    """The device of a tensor that a kernel will touch, which has to be the others'."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a GPU tensor")
+    d = t.get_device()
+    if device is not None and d != device:
+        raise ValueError(f"{name}: on another device than the other tensors")
+    return d
+
+
+def _mat(name, t, device):
+    """Packed muon_mat of a 2-D tensor with unit column stride (NULL for None)."""
+    global _codes
+    if t is None:
+        return None
+    _on_gpu(name, t, device)
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor")
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if cols > 1 and unit != 1:
+        raise ValueError(f"{name}: expected unit column stride")
+    if rows <= 1 or ld < cols:
+        if rows > 1:
+            raise ValueError(f"{name}: rows overlap")
+        ld = cols
+    if _codes is None:
+        import torch
+        _codes = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return _MAT(t.data_ptr(), rows, cols, ld, code, 1)
+
+
+def _vec(name, t, dtype, shape, device):
+    """Address of a contiguous tensor of the given dtype and shape (None for None)."""
+    if t is None:
+        return None
+    _on_gpu(name, t, device)
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+class Checkpoint:
+    """An activation checkpoint in 8 bits (see muon_ckpt in muon.h): `codes`,
+    rows x cols float8_e4m3fn, and `scales`, rows x ceil(cols / 128) uint8,
+    both with unit column stride."""
+
+    __slots__ = ("codes", "scales", "_packed")
+
+    def __init__(self, codes, scales):
+        import torch
+        if codes.dtype != torch.float8_e4m3fn or scales.dtype != torch.uint8:
+            raise TypeError("a checkpoint holds float8_e4m3fn codes and uint8 scales")
+        if codes.dim() != 2 or scales.dim() != 2:
+            raise ValueError("a checkpoint's codes and scales are 2-D")
+        rows, cols = codes.shape
+        groups = -(-cols // MUON_CKPT_GROUP)
+        if scales.shape != (rows, groups):
+            raise ValueError(f"scales: expected shape {(rows, groups)}, got {tuple(scales.shape)}")
+        ld_c, unit_c = codes.stride()
+        ld_s, unit_s = scales.stride()
+        if (cols > 1 and unit_c != 1) or (groups > 1 and unit_s != 1):
+            raise ValueError("a checkpoint's codes and scales have unit column stride")
+        if rows <= 1:
+            ld_c, ld_s = cols, groups
+        if ld_c < cols or ld_s < groups:
+            raise ValueError("a checkpoint's rows overlap")
+        _on_gpu("scales", scales, _on_gpu("codes", codes, None))
+        self.codes, self.scales = codes, scales
+        self._packed = _CKPT(codes.data_ptr(), scales.data_ptr(), rows, cols, ld_c, ld_s)
+
+    @classmethod
+    def empty(cls, rows, cols, device="cuda"):
+        """Room for the checkpoint of a rows x cols matrix (rows on 16-byte boundaries)."""
+        import torch
+        codes = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.float8_e4m3fn, device=device)[:, :cols]
+        return cls(codes, torch.empty((rows, -(-cols // MUON_CKPT_GROUP)), dtype=torch.uint8, device=device))
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+
+def _enter(t):
+    """The device index of a call's first tensor; its current stream becomes the call's."""
+    import torch
+    device = _on_gpu("argument", t, None)
+    if device != torch.cuda.current_device():
+        raise ValueError("the tensors are not on the current device")
+    _check(lib().muon_set_stream(torch.cuda.current_stream(device).cuda_stream))
+    return device
+
+
+class _Scratch:
+    """The workspace of one call: the caller's (a uint8 tensor), or a temporary
+    one from torch's allocator, whose memory is reused in stream order only.
+    What the thread had set before is set again afterwards."""
+
+    def __init__(self, nbytes, workspace, device):
+        self.nbytes, self.buf = nbytes, workspace
+        if nbytes:
+            import torch
+            if workspace is None:
+                self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            else:
+                _on_gpu("workspace", workspace, device)
+                if not workspace.is_contiguous():
+                    raise ValueError("workspace: expected a contiguous tensor")
+
+    def __enter__(self):
+        if self.nbytes:
+            self.old, self.old_bytes = ctypes.c_void_p(), ctypes.c_size_t()
+            _check(_lib.muon_get_workspace(ctypes.byref(self.old), ctypes.byref(self.old_bytes)))
+            _check(_lib.muon_set_workspace(self.buf.data_ptr(), self.buf.numel() * self.buf.element_size()))
+
+    def __exit__(self, *exc):
+        if self.nbytes:
+            err = exc[0] is None
+            st = _lib.muon_set_workspace(self.old, self.old_bytes)
+            if err:
+                _check(st)
+
+
+def _size(fn, *args):
+    out = ctypes.c_size_t()
+    _check(fn(*args, ctypes.byref(out)))
+    return out.value
+
+
+def muon_layernorm_workspace_size(rows, cols):
+    return _size(lib().muon_layernorm_workspace_size, rows, cols)
+
+
+def muon_ckpt_weight_grad_workspace_size(dtype, slots, n, k, groups=1):
+    return _size(lib().muon_ckpt_weight_grad_workspace_size, dtype, slots, n, k, groups)
+
+
+def muon_route_workspace_size(tokens, experts, topk):
+    return _size(lib().muon_route_workspace_size, tokens, experts, topk)
+
+
+def muon_layernorm_forward(x, y, mean=None, rstd=None, weight=None, bias=None, eps=1e-5, ckpt=None):
+    """y = layer norm of x's rows (see muon.h). mean, rstd: float32 vectors
+    that the backward pass reads; weight, bias: 1 x cols; ckpt: a Checkpoint
+    that receives y in 8 bits in the same pass."""
+    import torch
+    d = _enter(x)
+    f32, rows = torch.float32, x.shape[:1]
+    if ckpt is not None:
+        _on_gpu("ckpt", ckpt.codes, d)
+    _check(_lib.muon_layernorm_forward(
+        _mat("x", x, d), _mat("y", y, d), _vec("mean", mean, f32, rows, d), _vec("rstd", rstd, f32, rows, d),
+        _mat("weight", weight, d), _mat("bias", bias, d), eps, None if ckpt is None else ckpt._packed))
+
+
+def muon_layernorm_backward(dy, x, mean, rstd, dx, weight=None, dweight=None, dbias=None, workspace=None):
+    """dx, and where given dweight and dbias (1 x cols), of the layer norm (see
+    muon.h). workspace: a uint8 tensor of muon_layernorm_workspace_size bytes
+    (default: a temporary one)."""
+    import torch
+    d = _enter(dy)
+    f32, rows = torch.float32, dy.shape[:1]
+    args = (_mat("dy", dy, d), _mat("x", x, d), _vec("mean", mean, f32, rows, d), _vec("rstd", rstd, f32, rows, d),
+            _mat("dx", dx, d), _mat("weight", weight, d), _mat("dweight", dweight, d), _mat("dbias", dbias, d))
+    need = muon_layernorm_workspace_size(*dy.shape) if dweight is not None or dbias is not None else 0
+    with _Scratch(need, workspace, d):
+        _check(_lib.muon_layernorm_backward(*args))
+
+
+def muon_ckpt_save(x, ckpt):
+    """Save the matrix x as an 8-bit checkpoint (see muon.h)."""
+    d = _enter(x)
+    _on_gpu("ckpt", ckpt.codes, d)
+    _check(_lib.muon_ckpt_save(_mat("x", x, d), ckpt._packed))
+
+
+def muon_ckpt_load(ckpt, out):
+    """Load a checkpoint's values into the matrix out (see muon.h)."""
+    d = _enter(out)
+    _on_gpu("ckpt", ckpt.codes, d)
+    _check(_lib.muon_ckpt_load(ckpt._packed, _mat("out", out, d)))
+
+
+def muon_ckpt_weight_grad(dy, ckpt, grads, offsets=None, rows=None, rows_per_token=1, workspace=None):
+    """Weight gradients of a group of layers from their input's checkpoint (see
+    muon.h): grads[g] = sum over the slots of group g of dy[s]^T x[token(s)].
+    dy: slots x n; grads: groups x n x k (its matrices are what muon_step
+    takes); offsets (groups + 1) and rows (slots): int32, as
+    muon_route_forward writes them with rows_per_token = topk."""
+    import torch
+    d = _enter(dy)
+    if grads.dim() != 3:
+        raise ValueError("grads: expected a 3-D tensor (groups x n x k)")
+    _on_gpu("grads", grads, d)
+    groups, n, k = grads.shape
+    stride, ld, unit = grads.stride()
+    if (k > 1 and unit != 1) or (n > 1 and ld < k):
+        raise ValueError("grads: expected unit column stride")
+    if n <= 1:
+        ld = k
+    _on_gpu("ckpt", ckpt.codes, d)
+    dy_mat = _mat("dy", dy, d)
+    if grads.dtype != dy.dtype:
+        raise TypeError("dy and grads differ in dtype")
+    code = _codes[dy.dtype]
+    if groups > 1 and offsets is None:
+        raise ValueError("offsets: needed with more than one group")
+    args = (dy_mat, ckpt._packed, _MAT(grads.data_ptr(), n, k, ld, code, 1), stride, groups,
+            _vec("offsets", offsets, torch.int32, (groups + 1,), d), _vec("rows", rows, torch.int32, dy.shape[:1], d),
+            rows_per_token)
+    with _Scratch(muon_ckpt_weight_grad_workspace_size(code, dy.shape[0], n, k, groups), workspace, d):
+        _check(_lib.muon_ckpt_weight_grad(*args))
+
+
+def muon_route_forward(logits, indices, weights, counts, offsets, rows, loss, alpha=1e-2, renormalize=True,
+                       workspace=None):
+    """Route tokens to their topk experts (see muon.h). logits: tokens x
+    experts; indices (int32) and weights (float32): tokens x topk, which sets
+    topk; counts and offsets: experts + 1, rows: tokens * topk, all int32;
+    loss: one float32. All outputs are overwritten."""
+    import torch
+    d = _enter(logits)
+    m = _mat("logits", logits, d)
+    tokens, experts = logits.shape
+    if indices.dim() != 2:
+        raise ValueError("indices: expected a 2-D tensor (tokens x topk)")
+    topk = indices.shape[1]
+    i32, pair, table = torch.int32, (tokens, topk), (experts + 1,)
+    args = (m, topk, int(renormalize), alpha, _vec("indices", indices, i32, pair, d),
+            _vec("weights", weights, torch.float32, pair, d), _vec("counts", counts, i32, table, d),
+            _vec("offsets", offsets, i32, table, d), _vec("rows", rows, i32, (tokens * topk,), d),
+            _vec("loss", loss, torch.float32, (1,), d))
+    with _Scratch(muon_route_workspace_size(tokens, experts, topk), workspace, d):
+        _check(_lib.muon_route_forward(*args))
+
+
+def muon_route_backward(logits, indices, counts, dlogits, dweights=None, dloss=None, alpha=1e-2, renormalize=True):
+    """Gradient of loss * dloss + (weights * dweights).sum() with respect to
+    the logits (see muon.h)."""
+    import torch
+    d = _enter(logits)
+    if indices.dim() != 2:
+        raise ValueError("indices: expected a 2-D tensor (tokens x topk)")
+    pair = (logits.shape[0], indices.shape[1])
+    f32 = torch.float32
+    _check(_lib.muon_route_backward(
+        _mat("logits", logits, d), pair[1], int(renormalize), alpha, _vec("indices", indices, torch.int32, pair, d),
+        _vec("counts", counts, torch.int32, (logits.shape[1] + 1,), d), _vec("dweights", dweights, f32, pair, d),
+        _vec("dloss", dloss, f32, (1,), d), _mat("dlogits", dlogits, d)))

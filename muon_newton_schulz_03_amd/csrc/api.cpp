@@ -7,21 +7,11 @@
 #include "kernels.h"
 #include "muon.h"
 #include "plan.h"
+#include "state.h"
 
 namespace {
 
 using namespace muon;
-
-struct State {
-  hipStream_t stream = nullptr;
-  void *ws = nullptr;
-  size_t ws_bytes = 0;
-  int32_t iters = 5;
-  float coeffs[3] = {3.4445f, -4.7750f, 2.0315f};
-  float eps = 1e-7f;
-  uint32_t mode = MUON_NS_FULL | MUON_PACK_COST | MUON_AA_PLAIN;
-  std::string err;
-};
 
 thread_local State g_state;
 
@@ -385,6 +375,10 @@ muon_status step_impl(const muon_mat *params, const muon_mat *grads, const muon_
 
 }  // namespace
 
+namespace muon {
+State &thread_state() { return g_state; }
+}  // namespace muon
+
 extern "C" {
 
 muon_status muon_ns_batched(const muon_mat *descs, int32_t n_mats, int32_t iters, const float coeffs[3],
@@ -451,6 +445,13 @@ muon_status muon_set_workspace(void *device_ptr, size_t bytes) {
   if (reinterpret_cast<uintptr_t>(device_ptr) % 256) return fail(MUON_ERR_ALIGN, "workspace not 256-byte aligned");
   g_state.ws = device_ptr;
   g_state.ws_bytes = bytes;
+  return ok();
+}
+
+muon_status muon_get_workspace(void **device_ptr, size_t *bytes) {
+  if (!device_ptr || !bytes) return fail(MUON_ERR_INVALID_ARG, "device_ptr and bytes must not be NULL");
+  *device_ptr = g_state.ws;
+  *bytes = g_state.ws_bytes;
   return ok();
 }
 

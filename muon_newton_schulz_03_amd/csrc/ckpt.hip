@@ -1,0 +1,149 @@
+// Activation checkpoints in 8 bits (gfx950): e4m3 codes and one power-of-two
+// scale byte for each 128 columns of a row, saved from and loaded to bf16 or
+// float32 matrices. Both directions are bound by memory: each element is read
+// once and written once.
+#include <hip/hip_runtime.h>
+
+#include "lanes.h"
+#include "train.h"
+
+namespace muon {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // units a thread, their loads in flight together
+
+// Units of a row are numbered through: unit u lies in row u / per_row. The
+// quotient from 2^32 / per_row, one too few at most.
+struct RowSplit {
+  uint32_t per_row, magic;
+};
+__device__ inline void split(uint32_t u, const RowSplit &d, uint32_t &row, uint32_t &rest) {
+  row = __umulhi(u, d.magic);
+  rest = u - row * d.per_row;
+  if (rest >= d.per_row) {
+    ++row;
+    rest -= d.per_row;
+  }
+}
+
+// A unit is 8 columns; 16 lanes hold a group of 128.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void ckpt_save_kernel(const CkptArgs a, const RowSplit d, uint32_t units) {
+  uint32_t row[kUnroll], at[kUnroll];
+  Raw8<T> x[kUnroll];
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const uint32_t u = (blockIdx.x * kUnroll + j) * kThreads + threadIdx.x;
+    split(u, d, row[j], at[j]);
+    const int c = int(at[j]) * 8;
+    x[j] = load8(static_cast<const T *>(a.in) + int64_t(row[j]) * a.ld + c, u < units ? a.cols - c : 0);
+  }
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const uint32_t u = (blockIdx.x * kUnroll + j) * kThreads + threadIdx.x;
+    float f[8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[i] = x[j].get(i);
+      m = max(m, finite_mag(f[i]));
+    }
+    const uint32_t sb = scale_byte(row16_max(m));
+    const u32x2 codes = encode8(f, scale_inverse(sb));
+    const int c = int(at[j]) * 8;
+    if (u < units && c < a.cols) {
+      store_codes8(a.ck.codes + int64_t(row[j]) * a.ck.ld_codes + c, codes, a.cols - c);
+      if ((at[j] & 15) == 0) a.ck.scales[int64_t(row[j]) * a.ck.ld_scales + (c >> 7)] = uint8_t(sb);
+    }
+  }
+}
+
+// Eight values as T. The scaled conversion gives bf16, which holds a value
+// exactly (but below 2^-133); float32 takes values of the same codes at
+// scale 1 and multiplies, exact throughout.
+__device__ inline Raw8<__bf16> values8(const u32x2 c, uint32_t sb, __bf16) {
+  const float s = scale_value(sb);
+  Raw8<__bf16> r;
+  r.v[0] = decode2<0>(c[0], s);
+  r.v[1] = decode2<1>(c[0], s);
+  r.v[2] = decode2<0>(c[1], s);
+  r.v[3] = decode2<1>(c[1], s);
+  return r;
+}
+__device__ inline Raw8<float> values8(const u32x2 c, uint32_t sb, float) {
+  const Raw8<__bf16> one = values8(c, 127, __bf16());
+  const float s = scale_value(sb);
+  Raw8<float> r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.v[i >> 2][i & 3] = f32_bits(one.get(i) * s);
+  return r;
+}
+
+__device__ inline u32x2 load_codes8(const uint8_t *p, int n) {
+  u32x2 c = {0u, 0u};
+  if (n >= 8) {
+    c = *reinterpret_cast<const u32x2_any *>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) c[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
+  }
+  return c;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void ckpt_load_kernel(const CkptArgs a, const RowSplit d, uint32_t units) {
+  uint32_t row[kUnroll], at[kUnroll], sb[kUnroll];
+  u32x2 codes[kUnroll];
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const uint32_t u = (blockIdx.x * kUnroll + j) * kThreads + threadIdx.x;
+    split(u, d, row[j], at[j]);
+    const int c = int(at[j]) * 8;
+    const int n = u < units ? a.cols - c : 0;
+    codes[j] = load_codes8(a.ck.codes + int64_t(row[j]) * a.ck.ld_codes + c, n);
+    sb[j] = n > 0 ? a.ck.scales[int64_t(row[j]) * a.ck.ld_scales + (c >> 7)] : 127u;
+  }
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const uint32_t u = (blockIdx.x * kUnroll + j) * kThreads + threadIdx.x;
+    const int c = int(at[j]) * 8;
+    if (u < units && c < a.cols)
+      store8(static_cast<T *>(a.out) + int64_t(row[j]) * a.ld + c, values8(codes[j], sb[j], T()), a.cols - c);
+  }
+}
+
+// Launches over at most 2^31 units at a time.
+template <typename K>
+hipError_t by_rows(const CkptArgs &all, K kernel, size_t es, hipStream_t s) {
+  const uint32_t per_row = uint32_t((all.cols + kCkptGroup - 1) / kCkptGroup) * 16;
+  const RowSplit d{per_row, uint32_t((uint64_t(1) << 32) / per_row)};
+  const int64_t most = (int64_t(1) << 31) / per_row;
+  for (int64_t r = 0; r < all.rows; r += most) {
+    CkptArgs a = all;
+    a.rows = all.rows - r < most ? all.rows - r : most;
+    if (a.in) a.in = static_cast<const char *>(all.in) + r * all.ld * int64_t(es);
+    if (a.out) a.out = static_cast<char *>(all.out) + r * all.ld * int64_t(es);
+    a.ck.codes += r * all.ck.ld_codes;
+    a.ck.scales += r * all.ck.ld_scales;
+    const uint32_t units = uint32_t(a.rows) * per_row;
+    hipLaunchKernelGGL(kernel, dim3((units + kUnroll * kThreads - 1) / (kUnroll * kThreads)), dim3(kThreads), 0, s, a, d,
+                       units);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_ckpt_save(const CkptArgs &a, bool bf16, hipStream_t s) {
+  return bf16 ? by_rows(a, ckpt_save_kernel<__bf16>, 2, s) : by_rows(a, ckpt_save_kernel<float>, 4, s);
+}
+
+hipError_t launch_ckpt_load(const CkptArgs &a, bool bf16, hipStream_t s) {
+  return bf16 ? by_rows(a, ckpt_load_kernel<__bf16>, 2, s) : by_rows(a, ckpt_load_kernel<float>, 4, s);
+}
+
+}  // namespace muon

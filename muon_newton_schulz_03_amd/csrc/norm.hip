@@ -1,0 +1,340 @@
+// Layer norm, forward and backward (gfx950).
+//
+//   mu = sum x / C,  r = 1 / sqrt(sum (x - mu)^2 / C + eps),
+//   y = (x - mu) r w + b;
+//   xh = (x - mu) r,  h = dy w,  dx = r (h - mean(h) - xh mean(h xh)),
+//   dw = sum over rows of dy xh,  db = sum over rows of dy.
+//
+// Both passes are bound by memory: each element is read once into registers,
+// where a row's sums are taken (centred, in float32), and written once. A
+// row belongs to one wave (up to 1024 columns) or one workgroup.
+#include <hip/hip_runtime.h>
+
+#include "lanes.h"
+#include "train.h"
+
+namespace muon {
+namespace {
+
+template <bool kF32>
+__device__ inline void load_vec8(const void *p, int col, int n, float (&f)[8]) {
+  if constexpr (kF32) {
+    const Raw8<float> r = load8(static_cast<const float *>(p) + col, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = r.get(i);
+  } else {
+    const Raw8<__bf16> r = load8(static_cast<const __bf16 *>(p) + col, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = r.get(i);
+  }
+}
+
+// Sums of one or two values over the kTpr threads of a row; `slot` toggles
+// between two LDS areas, so one barrier a call is enough.
+template <int kTpr, int kN>
+__device__ inline void row_sum(float (&v)[kN], float *lds, int &slot) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (kTpr > 64) {
+    constexpr int kWaves = kTpr / 64;
+    float *area = lds + slot * kWaves * kN;
+    slot ^= 1;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) area[(threadIdx.x >> 6) * kN + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      v[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) v[i] += area[w * kN + i];
+    }
+  }
+}
+
+// kTpr threads a row, kNv runs of 8 columns a thread.
+template <typename T, bool kWf32, bool kCkpt, int kTpr, int kNv>
+__global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const NormFwdArgs a) {
+  constexpr int kBlock = kTpr < 256 ? 256 : kTpr;
+  __shared__ float lds[2 * (kTpr / 64)];
+  int slot = 0;
+  const int t = int(threadIdx.x) % kTpr;
+  const int64_t row = int64_t(blockIdx.x) * (kBlock / kTpr) + int(threadIdx.x) / kTpr;
+  if (row >= a.rows) return;  // whole rows leave (one row a workgroup, or one a wave)
+  const T *x = static_cast<const T *>(a.x) + row * a.ld_x;
+  T *y = static_cast<T *>(a.y) + row * a.ld_y;
+  Raw8<T> xr[kNv];
+  float s[1] = {0.f};
+#pragma unroll
+  for (int v = 0; v < kNv; ++v) {
+    const int c = (v * kTpr + t) * 8;
+    xr[v] = load8(x + c, a.cols - c);
+  }
+#pragma unroll
+  for (int v = 0; v < kNv; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[0] += xr[v].get(i);
+  row_sum<kTpr, 1>(s, lds, slot);
+  const float inv_c = 1.f / float(a.cols);
+  const float mean = s[0] * inv_c;
+  s[0] = 0.f;
+#pragma unroll
+  for (int v = 0; v < kNv; ++v) {
+    const int n = a.cols - (v * kTpr + t) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = xr[v].get(i) - mean;
+      if (i < n) s[0] = fmaf(d, d, s[0]);
+    }
+  }
+  row_sum<kTpr, 1>(s, lds, slot);
+  const float rstd = 1.f / sqrtf(s[0] * inv_c + a.eps);
+  if (t == 0) {
+    if (a.mean) a.mean[row] = mean;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+#pragma unroll
+  for (int v = 0; v < kNv; ++v) {
+    const int c = (v * kTpr + t) * 8, n = a.cols - c;
+    if (!kCkpt && n <= 0) break;
+    float f[8], w[8], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.f, b[i] = 0.f;
+    if (a.w) load_vec8<kWf32>(a.w, c, n, w);
+    if (a.b) load_vec8<kWf32>(a.b, c, n, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = fmaf((xr[v].get(i) - mean) * rstd, w[i], b[i]);
+    const Raw8<T> r = pack8(f, T());
+    if (n > 0) store8(y + c, r, n);
+    if constexpr (kCkpt) {
+      // the checkpoint of y as stored; its groups of 128 columns are 16 lanes
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[i] = i < n ? r.get(i) : 0.f;
+        m = max(m, finite_mag(f[i]));
+      }
+      const uint32_t sb = scale_byte(row16_max(m));
+      const u32x2 codes = encode8(f, scale_inverse(sb));
+      if (n > 0) {
+        store_codes8(a.ck.codes + row * a.ck.ld_codes + c, codes, n);
+        if ((t & 15) == 0) a.ck.scales[row * a.ck.ld_scales + (c >> 7)] = uint8_t(sb);
+      }
+    }
+  }
+}
+
+template <typename T, bool kWf32, bool kCkpt>
+hipError_t fwd(const NormFwdArgs &a, hipStream_t s) {
+  auto go = [&](auto kernel, int tpr) {
+    const int per = tpr < 256 ? 256 / tpr : 1;
+    hipLaunchKernelGGL(kernel, dim3(unsigned((a.rows + per - 1) / per)), dim3(tpr < 256 ? 256 : tpr), 0, s, a);
+    return hipGetLastError();
+  };
+  if (a.cols <= 512) return go(norm_fwd_kernel<T, kWf32, kCkpt, 64, 1>, 64);
+  if (a.cols <= 1024) return go(norm_fwd_kernel<T, kWf32, kCkpt, 64, 2>, 64);
+  if (a.cols <= 2048) return go(norm_fwd_kernel<T, kWf32, kCkpt, 256, 1>, 256);
+  if (a.cols <= 4096) return go(norm_fwd_kernel<T, kWf32, kCkpt, 256, 2>, 256);
+  if (a.cols <= 8192) return go(norm_fwd_kernel<T, kWf32, kCkpt, 256, 4>, 256);
+  if (a.cols <= 16384) return go(norm_fwd_kernel<T, kWf32, kCkpt, 1024, 2>, 1024);
+  return go(norm_fwd_kernel<T, kWf32, kCkpt, 1024, 4>, 1024);
+}
+
+// Each workgroup takes rows b, b + blocks, ... (kBlock / kTpr at a time) and
+// keeps its columns' sums of dy xh and dy in registers; the next rows' loads
+// are in flight while the current ones are reduced.
+template <typename T, bool kWf32, int kTpr, int kNv>
+__global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_bwd_kernel(const NormBwdArgs a) {
+  constexpr int kBlock = kTpr < 256 ? 256 : kTpr;
+  constexpr int kPer = kBlock / kTpr;
+  __shared__ float lds[2 * (kTpr / 64) * 2];
+  __shared__ float comb[kPer > 1 ? kTpr * kNv * 8 : 1];
+  int slot = 0;
+  const int t = int(threadIdx.x) % kTpr, sub = int(threadIdx.x) / kTpr;
+  const float inv_c = 1.f / float(a.cols);
+  Raw8<T> xr[kNv], dr[kNv], xn[kNv], dn[kNv];
+  float aw[kNv][8], ab[kNv][8];
+#pragma unroll
+  for (int v = 0; v < kNv; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) aw[v][i] = ab[v][i] = 0.f;
+  float mn = 0.f, rn = 0.f;
+  auto fetch = [&](int64_t row) {
+    if (row >= a.rows) {
+#pragma unroll
+      for (int v = 0; v < kNv; ++v) xn[v] = Raw8<T>{}, dn[v] = Raw8<T>{};
+      mn = rn = 0.f;
+      return;
+    }
+    const T *x = static_cast<const T *>(a.x) + row * a.ld_x;
+    const T *d = static_cast<const T *>(a.dy) + row * a.ld_dy;
+#pragma unroll
+    for (int v = 0; v < kNv; ++v) {
+      const int c = (v * kTpr + t) * 8;
+      xn[v] = load8(x + c, a.cols - c);
+      dn[v] = load8(d + c, a.cols - c);
+    }
+    mn = a.mean[row];
+    rn = a.rstd[row];
+  };
+  const int64_t step = int64_t(a.blocks) * kPer;
+  int64_t base = int64_t(blockIdx.x) * kPer;
+  fetch(base + sub);
+  for (; base < a.rows; base += step) {
+    const int64_t row = base + sub;
+    const float mean = mn, rstd = rn;
+#pragma unroll
+    for (int v = 0; v < kNv; ++v) xr[v] = xn[v], dr[v] = dn[v];
+    fetch(row + step);
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < kNv; ++v) {
+      const int c = (v * kTpr + t) * 8, n = a.cols - c;
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+      if (a.w) load_vec8<kWf32>(a.w, c, n, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = dr[v].get(i), xh = (xr[v].get(i) - mean) * rstd, h = d * w[i];
+        s[0] += h;
+        s[1] = fmaf(h, xh, s[1]);
+        aw[v][i] = fmaf(d, xh, aw[v][i]);
+        ab[v][i] += d;
+      }
+    }
+    row_sum<kTpr, 2>(s, lds, slot);
+    if (row < a.rows) {
+      const float m0 = s[0] * inv_c, m1 = s[1] * inv_c;
+      T *dx = static_cast<T *>(a.dx) + row * a.ld_dx;
+#pragma unroll
+      for (int v = 0; v < kNv; ++v) {
+        const int c = (v * kTpr + t) * 8, n = a.cols - c;
+        if (n <= 0) break;
+        float w[8], f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 1.f;
+        if (a.w) load_vec8<kWf32>(a.w, c, n, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float xh = (xr[v].get(i) - mean) * rstd;
+          f[i] = rstd * (dr[v].get(i) * w[i] - m0 - xh * m1);
+        }
+        store8(dx + c, pack8(f, T()), n);
+      }
+    }
+  }
+  if (!a.sums) return;
+  float *part = a.part + int64_t(blockIdx.x) * 2 * a.cols;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float(&acc)[kNv][8] = which ? ab : aw;
+    if constexpr (kPer > 1) {  // the workgroup's rows, added wave by wave
+      for (int p = kPer - 1; p > 0; --p) {
+        __syncthreads();
+        if (sub == p)
+#pragma unroll
+          for (int v = 0; v < kNv; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) comb[(v * 8 + i) * kTpr + t] = acc[v][i];
+        __syncthreads();
+        if (sub == 0)
+#pragma unroll
+          for (int v = 0; v < kNv; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[v][i] += comb[(v * 8 + i) * kTpr + t];
+      }
+    }
+    if (sub == 0)
+#pragma unroll
+      for (int v = 0; v < kNv; ++v) {
+        const int c = (v * kTpr + t) * 8, n = a.cols - c;
+        if (n > 0) store8(part + which * a.cols + c, pack8(acc[v], float()), n);
+      }
+  }
+}
+
+// Sums the workgroups' partials: 32 columns a workgroup, 8 threads a column,
+// each over every eighth partial, joined in a fixed order.
+constexpr int kRedCols = 32, kRedSlices = 8;
+__global__ __launch_bounds__(kRedCols * kRedSlices) void norm_grad_kernel(const NormBwdArgs a) {
+  __shared__ float lds[kRedSlices][kRedCols];
+  const int lc = int(threadIdx.x) % kRedCols, sl = int(threadIdx.x) / kRedCols;
+  const int c = int(blockIdx.x) * kRedCols + lc;  // of 2 * cols: dw, then db
+  float s = 0.f;
+  if (c < 2 * a.cols) {
+    const float *p = a.part + c;
+    int b = sl;
+    for (; b + 7 * kRedSlices < a.blocks; b += 8 * kRedSlices) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = p[int64_t(b + j * kRedSlices) * 2 * a.cols];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[j];
+    }
+    for (; b < a.blocks; b += kRedSlices) s += p[int64_t(b) * 2 * a.cols];
+  }
+  lds[sl][lc] = s;
+  __syncthreads();
+  if (sl || c >= 2 * a.cols) return;
+  s = 0.f;
+#pragma unroll
+  for (int j = 0; j < kRedSlices; ++j) s += lds[j][lc];
+  void *out = c < a.cols ? a.dw : a.db;
+  const int oc = c < a.cols ? c : c - a.cols;
+  if (!out) return;
+  if (a.w_f32)
+    static_cast<float *>(out)[oc] = s;
+  else
+    static_cast<__bf16 *>(out)[oc] = __bf16(s);
+}
+
+int bwd_tpr(int64_t cols) { return cols <= 1024 ? 64 : cols <= 8192 ? 256 : 1024; }
+
+template <typename T, bool kWf32>
+hipError_t bwd(const NormBwdArgs &a, hipStream_t s) {
+  auto go = [&](auto kernel, int tpr) {
+    if (a.blocks > 0) hipLaunchKernelGGL(kernel, dim3(unsigned(a.blocks)), dim3(tpr < 256 ? 256 : tpr), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.sums) return e;
+    hipLaunchKernelGGL(norm_grad_kernel, dim3((2 * a.cols + kRedCols - 1) / kRedCols), dim3(kRedCols * kRedSlices), 0, s,
+                       a);
+    return hipGetLastError();
+  };
+  if (a.cols <= 512) return go(norm_bwd_kernel<T, kWf32, 64, 1>, 64);
+  if (a.cols <= 1024) return go(norm_bwd_kernel<T, kWf32, 64, 2>, 64);
+  if (a.cols <= 2048) return go(norm_bwd_kernel<T, kWf32, 256, 1>, 256);
+  if (a.cols <= 4096) return go(norm_bwd_kernel<T, kWf32, 256, 2>, 256);
+  if (a.cols <= 8192) return go(norm_bwd_kernel<T, kWf32, 256, 4>, 256);
+  if (a.cols <= 16384) return go(norm_bwd_kernel<T, kWf32, 1024, 2>, 1024);
+  return go(norm_bwd_kernel<T, kWf32, 1024, 4>, 1024);
+}
+
+}  // namespace
+
+// Workgroups of the backward pass: enough to fill the chip, but each with
+// several rows, since each leaves 8 bytes a column of partial sums.
+int norm_bwd_blocks(int64_t rows, int64_t cols) {
+  const int per = bwd_tpr(cols) < 256 ? 256 / bwd_tpr(cols) : 1;
+  const int64_t want = (rows + 4 * per - 1) / (4 * per);
+  return int(want < 512 ? want : 512);
+}
+
+hipError_t launch_norm_fwd(const NormFwdArgs &a, bool bf16, hipStream_t s) {
+  if (a.rows <= 0) return hipSuccess;
+  const bool ck = a.ck.codes != nullptr;
+  if (bf16) {
+    if (a.w_f32) return ck ? fwd<__bf16, true, true>(a, s) : fwd<__bf16, true, false>(a, s);
+    return ck ? fwd<__bf16, false, true>(a, s) : fwd<__bf16, false, false>(a, s);
+  }
+  if (a.w_f32) return ck ? fwd<float, true, true>(a, s) : fwd<float, true, false>(a, s);
+  return ck ? fwd<float, false, true>(a, s) : fwd<float, false, false>(a, s);
+}
+
+hipError_t launch_norm_bwd(const NormBwdArgs &a, bool bf16, hipStream_t s) {
+  if (bf16) return a.w_f32 ? bwd<__bf16, true>(a, s) : bwd<__bf16, false>(a, s);
+  return a.w_f32 ? bwd<float, true>(a, s) : bwd<float, false>(a, s);
+}
+
+}  // namespace muon

@@ -19,3 +19,4 @@ from .muon_oracle import (  # noqa: F401
     newton_schulz_iteration_rows,
 )
 from .adamw_oracle import adamw_step  # noqa: F401,E402
+from . import train_oracle  # noqa: F401,E402

@@ -1,0 +1,491 @@
+"""GPU parity of the training operators against their float64 oracles, through
+the public binding, with guard rows around every matrix output.
+
+Tolerances: half a step of the output's type relative to the value, plus a
+float32 bound on the sums behind it: u = 2^-24 times the length of the longest
+chain of additions (and the few roundings of each term) times the sum of the
+terms' magnitudes. Codes, scales, indices, counts and lists are exact."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import padded
+from oracle import train_oracle as T
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF, F32 = torch.bfloat16, torch.float32
+HALF = {BF: 2.0 ** -8, F32: U}
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape, scale=1.0):
+    return torch.randn(shape, generator=g, device="cuda") * scale
+
+
+def n64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def mat(v, dtype, extra=0):
+    """v in a guarded buffer of its own, rows `extra` elements longer."""
+    _, t = padded(v.shape[0], v.shape[1], dtype, v.shape[1] + extra)
+    t.copy_(v)
+    return t
+
+
+def out_mat(rows, cols, dtype, extra=0):
+    return padded(rows, cols, dtype, cols + extra)[1]
+
+
+class Codes:
+    """A checkpoint whose codes and scales lie inside larger buffers of a known fill."""
+
+    def __init__(self, mu, rows, cols, extra=0):
+        groups = -(-cols // 128)
+        self.c = torch.full((rows + 2, cols + extra), 0x55, dtype=torch.uint8, device="cuda")
+        self.s = torch.full((rows + 2, groups + extra), 0x55, dtype=torch.uint8, device="cuda")
+        self.rows, self.cols, self.groups = rows, cols, groups
+        self.ck = mu.Checkpoint(self.c.view(torch.float8_e4m3fn)[1:1 + rows, :cols], self.s[1:1 + rows, :groups])
+
+    def check(self):
+        for t, cols in ((self.c, self.cols), (self.s, self.groups)):
+            assert bool((t[0] == 0x55).all() and (t[self.rows + 1:] == 0x55).all() and (t[:, cols:] == 0x55).all())
+
+    def read(self):
+        v = T.code_values()[self.c[1:1 + self.rows, :self.cols].cpu().numpy()]
+        return v, self.s[1:1 + self.rows, :self.groups].cpu().numpy().astype(np.int64)
+
+
+def close(got, ref, tol, what):
+    got, ref = np.asarray(got, np.float64), np.asarray(ref, np.float64)
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), f"{what}: {bad.sum()} off, worst {np.max(np.abs(got - ref) / np.maximum(tol, 1e-300)):.3g} of the tolerance"
+
+
+# rows, cols, pitch beyond cols: each width class of the kernels, odd widths and pitches, one row and one column
+NORM = [(1, 1, 0), (3, 7, 0), (5, 129, 3), (37, 512, 0), (9, 513, 0), (64, 1024, 8), (13, 1025, 1), (4, 2048, 0),
+        (33, 2047, 0), (21, 4096, 0), (7, 4097, 5), (130, 7168, 0), (3, 8193, 0), (2, 16385, 1), (2, 32768, 0)]
+
+
+@pytest.mark.parametrize("dtype,wdtype", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("rows,cols,extra", NORM)
+def test_layernorm(gpu_lib, rows, cols, extra, dtype, wdtype):
+    mu, g = gpu_lib, gen(rows * 40000 + cols)
+    x = mat(randn(g, rows, cols) * 2 + 0.7, dtype, extra)
+    w, b = mat(1 + randn(g, 1, cols, scale=0.3), wdtype), mat(randn(g, 1, cols, scale=0.3), wdtype)
+    dy = mat(randn(g, rows, cols, scale=1e-2), dtype, extra)
+    y, dx = out_mat(rows, cols, dtype, extra), out_mat(rows, cols, dtype, extra)
+    dw, db = out_mat(1, cols, wdtype), out_mat(1, cols, wdtype)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    codes = Codes(mu, rows, cols, extra)
+    mu.muon_layernorm_forward(x, y, mean, rstd, w, b, eps=1e-5, ckpt=codes.ck)
+    X, W, B = n64(x), n64(w)[0], n64(b)[0]
+    ry, rm, rr = T.layernorm(X, W, B)
+    big = np.abs(X).max(1)
+    # the mean: tree sums of at most 32 terms a thread, then 6 + 4 levels
+    close(n64(mean), rm, 48 * U * np.abs(X).mean(1), "mean")
+    close(n64(rstd), rr, 48 * U * rr * (1 + rr * big), "rstd")
+    scale = ((big + np.abs(rm)) * rr)[:, None] * np.abs(W)
+    close(n64(y), ry, HALF[dtype] * np.abs(ry) + 48 * U * (scale * (1 + (rr * big)[:, None]) + np.abs(B)), "y")
+    # the checkpoint of y as stored, bit for bit
+    unit, sb = T.checkpoint(n64(y))
+    got, gb = codes.read()
+    codes.check()
+    assert np.array_equal(gb, sb) and np.array_equal(got, unit)
+    # backward, from the statistics as stored
+    mu.muon_layernorm_backward(dy, x, mean, rstd, dx, w, dw, db)
+    D, M, R = n64(dy), n64(mean), n64(rstd)
+    rdx, rdw, rdb = T.layernorm_grad(D, X, M, R, W)
+    xh, h = (X - M[:, None]) * R[:, None], D * W
+    mag = R[:, None] * (np.abs(h) + np.abs(h).mean(1, keepdims=True) + np.abs(xh) * np.abs(h * xh).mean(1, keepdims=True))
+    slack = (1 + (R * big)[:, None])  # x - mean is rounded against x
+    close(n64(dx), rdx, HALF[dtype] * np.abs(rdx) + 64 * U * mag * slack, "dx")
+    # at most 32 rows a chain here, 4 waves, 64 partials in 8 slices
+    close(n64(dw)[0], rdw, HALF[wdtype] * np.abs(rdw) + 128 * U * (np.abs(D * xh) * slack).sum(0), "dweight")
+    close(n64(db)[0], rdb, HALF[wdtype] * np.abs(rdb) + 128 * U * np.abs(D).sum(0), "dbias")
+
+
+def test_layernorm_many_rows_and_optional_operands(gpu_lib):
+    """More rows than workgroups; no weight, no bias, no statistics, one gradient alone; no rows at all."""
+    mu, g = gpu_lib, gen(5)
+    rows, cols = 9001, 96
+    x, dy = mat(randn(g, rows, cols), BF), mat(randn(g, rows, cols), BF)
+    y, dx = out_mat(rows, cols, BF), out_mat(rows, cols, BF)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    mu.muon_layernorm_forward(x, y, mean, rstd)
+    y2 = out_mat(rows, cols, BF)
+    mu.muon_layernorm_forward(x, y2)
+    assert torch.equal(y, y2)
+    ry, _, _ = T.layernorm(n64(x))
+    close(n64(y), ry, 2.0 ** -8 * np.abs(ry) + 64 * U * (1 + np.abs(ry)) ** 2, "y")
+    db, dw = out_mat(1, cols, F32), out_mat(1, cols, F32)
+    mu.muon_layernorm_backward(dy, x, mean, rstd, dx, dbias=db)
+    mu.muon_layernorm_backward(dy, x, mean, rstd, dx, dweight=dw)
+    M, R = n64(mean), n64(rstd)
+    _, rdw, rdb = T.layernorm_grad(n64(dy), n64(x), M, R)
+    xh = (n64(x) - M[:, None]) * R[:, None]
+    close(n64(db)[0], rdb, 128 * U * np.abs(n64(dy)).sum(0), "dbias")
+    close(n64(dw)[0], rdw, 128 * U * (np.abs(n64(dy) * xh) + np.abs(n64(dy))).sum(0), "dweight")
+    only = out_mat(rows, cols, BF)
+    mu.muon_layernorm_backward(dy, x, mean, rstd, only)
+    assert torch.equal(only, dx)
+    none = torch.empty((0, cols), dtype=BF, device="cuda")
+    stat = torch.empty(0, device="cuda")
+    mu.muon_layernorm_forward(none, none.clone(), stat, stat.clone())
+    mu.muon_layernorm_backward(none, none.clone(), stat, stat.clone(), none.clone(), dweight=dw, dbias=db)
+    assert not n64(dw).any() and not n64(db).any()
+
+
+def test_layernorm_infinities_stay_in_their_row(gpu_lib):
+    x = mat(randn(gen(6), 4, 300), F32)
+    x[1, 7], x[2, 3] = float("inf"), float("nan")
+    y = out_mat(4, 300, F32, 0)
+    codes = Codes(gpu_lib, 4, 300)
+    gpu_lib.muon_layernorm_forward(x, y, ckpt=codes.ck)
+    assert bool(torch.isnan(y[1]).all() and torch.isnan(y[2]).all() and torch.isfinite(y[0]).all() and torch.isfinite(y[3]).all())
+    got, _ = codes.read()
+    assert np.isnan(got[1]).all() and np.isfinite(got[0]).all()
+
+
+CKPT = [(1, 1, 0), (2, 5, 0), (3, 128, 0), (5, 129, 1), (17, 255, 7), (100, 768, 0), (31, 2047, 0), (9, 7168, 0), (300, 40, 0)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols,extra", CKPT)
+def test_checkpoint(gpu_lib, rows, cols, extra, dtype):
+    mu, g = gpu_lib, gen(rows * 40000 + cols)
+    v = randn(g, rows, cols) * torch.exp(2 * randn(g, 1, cols))
+    v[torch.rand(v.shape, generator=g, device="cuda") < 0.02] = 0
+    x = mat(v, dtype, extra)
+    codes = Codes(mu, rows, cols, extra)
+    mu.muon_ckpt_save(x, codes.ck)
+    unit, sb = T.checkpoint(n64(x))
+    got, gb = codes.read()
+    codes.check()
+    assert np.array_equal(gb, sb) and np.array_equal(got, unit)
+    for to in (BF, F32):
+        back = out_mat(rows, cols, to, extra)
+        mu.muon_ckpt_load(codes.ck, back)
+        assert np.array_equal(n64(back), T.values(unit, sb)), to
+
+
+def test_checkpoint_of_special_values(gpu_lib):
+    """Zeros, denormals, the largest values, infinities and NaN, ties and both sides of a scale's border."""
+    rows = torch.zeros((8, 256), device="cuda")
+    rows[1, :4] = torch.tensor([float("inf"), 1.0, -float("inf"), float("nan")], device="cuda")
+    rows[2, 0], rows[2, 128] = 3.4028234e38, 1e-45
+    rows[3, 0], rows[3, 128] = 1.75, 1.7500001
+    rows[4, :16] = torch.arange(16, device="cuda") / 16 + 16  # ties between codes
+    rows[4, 16] = 448
+    rows[5, :] = 2.0 ** -130
+    rows[6, 0], rows[6, 1] = -448 * 2.0 ** 100, 2.0 ** 90
+    rows[7, :] = float("nan")
+    codes = Codes(gpu_lib, 8, 256)
+    gpu_lib.muon_ckpt_save(mat(rows, F32), codes.ck)
+    unit, sb = T.checkpoint(n64(rows))
+    got, gb = codes.read()
+    assert np.array_equal(gb, sb) and np.array_equal(got, unit, equal_nan=True)
+    back = out_mat(8, 256, F32)
+    gpu_lib.muon_ckpt_load(codes.ck, back)
+    with np.errstate(over="ignore"):  # the largest floats round up to the code of 2^128, an infinity in float32
+        assert np.array_equal(n64(back), T.values(unit, sb).astype(np.float32), equal_nan=True)
+    _, bf = padded(8, 256, BF)
+    gpu_lib.muon_ckpt_load(codes.ck, bf)
+    assert torch.equal(torch.nan_to_num(bf, nan=7.0), torch.nan_to_num(back.to(BF), nan=7.0))
+    none = gpu_lib.Checkpoint.empty(0, 70)
+    gpu_lib.muon_ckpt_save(torch.empty((0, 70), device="cuda"), none)
+
+
+def saved(mu, x):
+    ck = mu.Checkpoint.empty(*x.shape)
+    mu.muon_ckpt_save(x, ck)
+    back = torch.empty(x.shape, device="cuda")
+    mu.muon_ckpt_load(ck, back)
+    return ck, n64(back)
+
+
+def wgrad_tol(dtype, ref, mag, length):
+    # sums of 16 products in the matrix core, one after another; three parts of a float32 gradient
+    return HALF[dtype] * np.abs(ref) + (length / 4 + 40) * U * mag
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("slots,n,k,extra", [(1, 1, 1, 0), (1, 3, 5, 0), (31, 64, 64, 0), (32, 128, 256, 0), (33, 130, 260, 0),
+                                             (65, 127, 255, 1), (200, 7, 513, 0), (97, 300, 129, 3), (1500, 136, 272, 0),
+                                             (4000, 64, 70, 0)])
+def test_weight_grad_dense(gpu_lib, slots, n, k, extra, dtype):
+    mu, g = gpu_lib, gen(slots * 7 + n)
+    ck, X = saved(mu, randn(g, slots, k) * torch.exp(randn(g, 1, k)))
+    dy = mat(randn(g, slots, n, scale=1e-3), dtype, extra)
+    out = out_mat(n, k, dtype, extra)
+    mu.muon_ckpt_weight_grad(dy, ck, out[None])
+    ref, mag = T.weight_grad(n64(dy), X)
+    close(n64(out), ref[0], wgrad_tol(dtype, ref[0], mag[0], slots), "gradient")
+
+
+def lists(g, tokens, topk, experts, seed_popular=1.0):
+    want = randn(g, experts) * seed_popular + randn(g, tokens, experts)
+    picked = want.topk(topk, 1).indices.reshape(-1)
+    rows = torch.argsort(picked, stable=True).to(torch.int32)
+    counts = torch.bincount(picked, minlength=experts)
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
+    return rows, offsets
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tokens,topk,experts,n,k", [(1, 1, 2, 5, 9), (3, 3, 7, 66, 131), (100, 8, 16, 64, 260),
+                                                     (333, 5, 40, 129, 64), (700, 2, 3, 768, 300)])
+def test_weight_grad_groups(gpu_lib, tokens, topk, experts, n, k, dtype):
+    mu, g = gpu_lib, gen(tokens + experts)
+    ck, X = saved(mu, randn(g, tokens, k))
+    rows, offsets = lists(g, tokens, topk, experts, 2.0)
+    dy = mat(randn(g, tokens * topk, n, scale=1e-3), dtype)
+    out = out_mat(experts * n, k, dtype)
+    mu.muon_ckpt_weight_grad(dy, ck, out.view(experts, n, k), offsets, rows, topk)
+    ref, mag = T.weight_grad(n64(dy), X, offsets.tolist(), rows.cpu().numpy(), topk)
+    length = int((offsets[1:] - offsets[:-1]).max())
+    close(n64(out).reshape(ref.shape), ref, wgrad_tol(dtype, ref, mag, length), "gradients")
+
+
+def test_weight_grad_odd_lists(gpu_lib):
+    """Empty groups, slots of no token, offsets beyond the slots, no slots at all; a float32 gradient's infinities."""
+    mu, g = gpu_lib, gen(3)
+    ck, X = saved(mu, randn(g, 10, 40))
+    dy = mat(randn(g, 12, 20), F32)
+    rows = torch.tensor([0, 3, -1, 7, 9, 10, 400, 2, 2, 1, 5, 6], dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([-5, 0, 4, 4, 9, 70], dtype=torch.int32, device="cuda")
+    out = out_mat(5 * 20, 40, F32).view(5, 20, 40)
+    mu.muon_ckpt_weight_grad(dy, ck, out, offsets, rows, 1)
+    there = (rows >= 0) & (rows < 10)
+    D = n64(dy) * there.cpu().numpy()[:, None]
+    ref, mag = T.weight_grad(D, X, [0, 0, 4, 4, 9, 12], rows.clamp(0, 9).cpu().numpy(), 1)
+    close(n64(out), ref, wgrad_tol(F32, ref, mag, 12), "gradients")
+    empty = torch.empty((0, 20), device="cuda")
+    mu.muon_ckpt_weight_grad(empty, ck, out, torch.zeros(6, dtype=torch.int32, device="cuda"),
+                             torch.empty(0, dtype=torch.int32, device="cuda"), 1)
+    assert not n64(out).any()
+    dy[3, 2], dy[4, 5] = float("inf"), float("nan")
+    one = out_mat(20, 40, F32)
+    mu.muon_ckpt_weight_grad(dy, ck, one[None], rows=rows)
+    assert bool(torch.isnan(one[5]).all()) and not bool(torch.isfinite(one[2]).any())
+    assert bool(torch.isfinite(one[[0, 1, 3, 4]]).all()) and bool(torch.isfinite(one[6:]).all())
+    assert bool((one[2][torch.from_numpy(X[7] > 0).cuda()] == float("inf")).all())
+
+
+def test_weight_grad_keeps_float32(gpu_lib):
+    """A float32 gradient reaches the sum whole: one slot, x a power of two."""
+    ck, _ = saved(gpu_lib, torch.full((1, 8), 4.0, device="cuda"))
+    dy = mat(randn(gen(8), 1, 500) * torch.exp(5 * randn(gen(9), 1, 500)), F32)
+    out = out_mat(500, 8, F32)
+    gpu_lib.muon_ckpt_weight_grad(dy, ck, out[None])
+    assert torch.equal(out, (4 * dy).t().expand(500, 8))
+
+
+def route_all(mu, logits, topk, **kw):
+    tokens, experts = logits.shape
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = (torch.full((tokens, topk), 77, **i32), torch.full((tokens, topk), 7.0, device="cuda"),
+           torch.full((experts + 1,), 77, **i32), torch.full((experts + 1,), 77, **i32),
+           torch.full((tokens * topk,), 77, **i32), torch.full((1,), 7.0, device="cuda"))
+    mu.muon_route_forward(logits, *out, **kw)
+    return out
+
+
+ROUTE = [(1, 1, 1), (1, 5, 2), (7, 64, 8), (128, 128, 8), (129, 65, 3), (1000, 384, 8), (300, 385, 1), (65, 1024, 32),
+         (2500, 7, 7), (66000, 3, 1)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("tokens,experts,topk", ROUTE)
+def test_route(gpu_lib, tokens, experts, topk, renorm, dtype):
+    mu, g = gpu_lib, gen(tokens + experts)
+    v = randn(g, tokens, experts) * 1.5
+    if tokens > 4:
+        v[tokens - tokens // 5:] = -float("inf")   # padding
+        v[1, experts // 2:] = -float("inf")
+        v[2] = 0.25                                 # ties
+    logits = mat(v, dtype, 3)
+    idx, w, counts, offs, rows, loss = route_all(mu, logits, topk, alpha=0.3, renormalize=renorm)
+    L = n64(logits)
+    ri, rw, rc, ro, rr, rl = T.route(L, topk, 0.3, renorm)
+    for got, ref in ((idx, ri), (counts, rc), (offs, ro), (rows, rr)):
+        assert np.array_equal(got.cpu().numpy(), ref)
+    spread = np.nanmax(np.where(np.isfinite(L), L, np.nan)) - np.nanmin(np.where(np.isfinite(L), L, np.nan))
+    # the exponent's argument is rounded, sums of 16 registers over 64 lanes
+    rel = (24 + spread) * 2 * U
+    close(n64(w), rw, rel * rw, "weights")
+    close(n64(loss)[0], rl, (rel + 128 * U) * abs(rl), "loss")
+    dw = randn(g, tokens, topk)
+    dloss = torch.full((1,), 0.7, device="cuda")
+    dl = out_mat(tokens, experts, dtype, 3)
+    mu.muon_route_backward(logits, idx, counts, dl, dweights=dw, dloss=dloss, alpha=0.3, renormalize=renorm)
+    a, dl7 = float(np.float32(0.3)), float(np.float32(0.7))
+    ref = T.route_grad(L, ri, rc, topk, n64(dw), dl7, a, renorm)
+    p = T.softmax(L)
+    d = np.tile(dl7 * a * experts / (topk * max(1, int(rc[-1])) ** 2) * rc[:-1], (tokens, 1))
+    extra = np.zeros_like(p)
+    safe = np.maximum(ri, 0)
+    gw = np.where(ri >= 0, np.abs(n64(dw)), 0)
+    if renorm:
+        q = np.where(ri >= 0, np.take_along_axis(p, safe, 1), 0)
+        q = q / np.maximum(q.sum(1, keepdims=True), 1e-300)
+        gw = q * (gw + (q * gw).sum(1, keepdims=True))
+        np.put_along_axis(extra, safe, np.maximum(gw, np.take_along_axis(extra, safe, 1)), 1)
+    else:
+        np.put_along_axis(extra, safe, np.maximum(gw, np.take_along_axis(extra, safe, 1)), 1)
+        d, extra = d + extra, 0 * extra
+    mag = p * (d + (d * p).sum(1, keepdims=True)) + extra
+    tiny = 2.0 ** -133 if dtype == BF else 2.0 ** -149  # below the normal range a step is absolute
+    close(n64(dl), ref, HALF[dtype] * np.abs(ref) + 3 * rel * mag + tiny, "dlogits")
+
+
+def test_route_backward_is_the_slope(gpu_lib):
+    """The gradient against differences of the forward pass's own weights and loss, in float32: steps of 2^-6 leave
+    truncation near h^2 / 6 of third derivatives (at most 1) and rounding near 8 u / h."""
+    mu, g = gpu_lib, gen(12)
+    tokens, experts, topk, h = 4, 9, 3, 2.0 ** -6
+    v = torch.sort(randn(g, tokens, experts), 1).values + torch.arange(experts, device="cuda") * 0.2  # no choice changes
+    logits = mat(v, F32)
+    dw = randn(g, tokens, topk)
+    for renorm in (True, False):
+        idx, w, counts, _, _, _ = route_all(mu, logits, topk, alpha=0.5, renormalize=renorm)
+        dl = out_mat(tokens, experts, F32)
+        mu.muon_route_backward(logits, idx, counts, dl, dweights=dw, dloss=torch.ones(1, device="cuda"), alpha=0.5,
+                               renormalize=renorm)
+        for t in range(tokens):
+            for e in range(experts):
+                f = []
+                for s in (h, -h):
+                    moved = logits.clone()
+                    moved[t, e] += s
+                    i2, w2, _, _, _, l2 = route_all(mu, moved, topk, alpha=0.5, renormalize=renorm)
+                    assert torch.equal(i2, idx)
+                    f.append(float(l2.double() + (w2.double() * dw.double()).sum()))
+                slope = (f[0] - f[1]) / (2 * h)
+                assert abs(float(dl[t, e]) - slope) <= 10 * (h * h / 6 + 8 * U / h), (renorm, t, e)
+
+
+def test_route_masked_everywhere_and_empty(gpu_lib):
+    mu = gpu_lib
+    logits = mat(torch.full((200, 10), -float("inf"), device="cuda"), BF)
+    idx, w, counts, offs, rows, loss = route_all(mu, logits, 4)
+    assert bool((idx == -1).all() and (w == 0).all() and (counts == 0).all() and (offs == 0).all() and (rows == -1).all())
+    assert float(loss) == 0
+    dl = out_mat(200, 10, BF)
+    mu.muon_route_backward(logits, idx, counts, dl, dweights=torch.ones((200, 4), device="cuda"), dloss=torch.ones(1, device="cuda"))
+    assert not n64(dl).any()
+    none = torch.empty((0, 10), device="cuda")
+    idx, w, counts, offs, rows, loss = route_all(mu, none, 4)
+    assert not n64(counts).any() and not n64(offs).any() and float(loss) == 0
+    # the lowest finite value is a logit like any other; NaN and infinities end nothing and stay in range
+    low = torch.full((3, 6), torch.finfo(F32).min, device="cuda")
+    low[1, 2], low[2, 4] = float("nan"), float("inf")
+    idx, w, counts, offs, rows, loss = route_all(mu, low, 2)
+    assert idx.tolist() == [[0, 1], [0, 1], [4, 0]] and int(counts[6]) == 3
+    assert bool(torch.isnan(w[1]).all()) and np.allclose(n64(w[0]), 0.5)
+
+
+def test_same_bits_every_time_and_on_other_streams(gpu_lib):
+    """Two runs of every operator on different streams give the same bits, and what the thread had set stays set."""
+    import ctypes
+    mu, g = gpu_lib, gen(21)
+    keep = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    mu.muon_set_workspace(keep.data_ptr(), 4096)
+    tokens, experts, topk, n, k = 700, 12, 3, 96, 640
+    x = randn(g, tokens, k).to(BF)
+    dy = randn(g, tokens * topk, n).to(BF)
+    dn = randn(g, tokens, k).to(BF)
+    logits = randn(g, tokens, experts)
+    w, b = randn(g, 1, k).to(BF), randn(g, 1, k).to(BF)
+    dw = randn(g, tokens, topk)
+    torch.cuda.synchronize()
+
+    def all_of_it():
+        y, dx, ck = torch.empty_like(x), torch.empty_like(x), mu.Checkpoint.empty(tokens, k)
+        mean, rstd = torch.empty(tokens, device="cuda"), torch.empty(tokens, device="cuda")
+        mu.muon_layernorm_forward(x, y, mean, rstd, w, b, ckpt=ck)
+        r = route_all(mu, logits, topk)
+        grads = torch.empty((experts, n, k), dtype=BF, device="cuda")
+        mu.muon_ckpt_weight_grad(dy, ck, grads, r[3], r[4], topk)
+        dl, gw, gb = torch.empty_like(logits), torch.empty_like(w), torch.empty_like(b)
+        mu.muon_route_backward(logits, r[0], r[2], dl, dweights=dw, dloss=r[5])
+        mu.muon_layernorm_backward(dn, x, mean, rstd, dx, w, gw, gb)
+        return [y, mean, rstd, ck.codes.view(torch.uint8).clone(), ck.scales, grads, dl, dx, gw, gb, *r]
+
+    first = all_of_it()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = all_of_it()
+    torch.cuda.synchronize()
+    for p, q in zip(first, second):
+        assert torch.equal(p, q)
+    ptr, size = ctypes.c_void_p(), ctypes.c_size_t()
+    assert mu.lib().muon_get_workspace(ctypes.byref(ptr), ctypes.byref(size)) == 0
+    assert ptr.value == keep.data_ptr() and size.value == 4096
+    mu.muon_set_workspace(None, 0)
+    mu.muon_set_stream(None)
+
+
+def test_graph_replays(gpu_lib):
+    """Captured once with the caller's workspace, replayed on new inputs with eager work between, equal to eager calls."""
+    mu, g = gpu_lib, gen(22)
+    tokens, experts, topk, n, k = 300, 8, 2, 80, 384
+    x, dn = torch.empty((tokens, k), dtype=BF, device="cuda"), torch.empty((tokens, k), dtype=BF, device="cuda")
+    dy, logits = torch.empty((tokens * topk, n), device="cuda"), torch.empty((tokens, experts), device="cuda")
+    w = randn(g, 1, k).to(BF)
+    size = max(mu.muon_layernorm_workspace_size(tokens, k), mu.muon_route_workspace_size(tokens, experts, topk),
+               mu.muon_ckpt_weight_grad_workspace_size(mu.MUON_F32, tokens * topk, n, k, experts), 256)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def make():
+        return dict(y=torch.empty_like(x), dx=torch.empty_like(x), mean=torch.empty(tokens, device="cuda"),
+                    rstd=torch.empty(tokens, device="cuda"), ck=mu.Checkpoint.empty(tokens, k),
+                    idx=torch.empty((tokens, topk), **i32), wt=torch.empty((tokens, topk), device="cuda"),
+                    counts=torch.empty(experts + 1, **i32), offs=torch.empty(experts + 1, **i32),
+                    rows=torch.empty(tokens * topk, **i32), loss=torch.empty(1, device="cuda"),
+                    grads=torch.empty((experts, n, k), device="cuda"), dl=torch.empty_like(logits), gw=torch.empty_like(w))
+
+    def step(o):
+        mu.muon_layernorm_forward(x, o["y"], o["mean"], o["rstd"], w, ckpt=o["ck"])
+        mu.muon_route_forward(logits, o["idx"], o["wt"], o["counts"], o["offs"], o["rows"], o["loss"], workspace=ws)
+        mu.muon_ckpt_weight_grad(dy, o["ck"], o["grads"], o["offs"], o["rows"], topk, workspace=ws)
+        mu.muon_route_backward(logits, o["idx"], o["counts"], o["dl"], dloss=o["loss"])
+        mu.muon_layernorm_backward(dn, x, o["mean"], o["rstd"], o["dx"], w, o["gw"], workspace=ws)
+
+    def fill(seed):
+        h = gen(seed)
+        for t in (x, dn, dy, logits):
+            t.copy_(randn(h, *t.shape))
+
+    captured, eager = make(), make()
+    fill(1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(captured)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(captured)
+    torch.cuda.synchronize()
+    for seed in (1, 2, 3):
+        fill(seed)
+        step(eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in eager:
+            if name != "ck":
+                assert torch.equal(captured[name], eager[name]), (seed, name)
+    mu.muon_set_stream(None)
