@@ -371,6 +371,7 @@ muon_status muon_ckpt_weight_grad(const muon_mat *dy, const muon_ckpt *x, const 
     if (n_groups > 1 && group_stride < (grads->rows - 1) * grads->ld + grads->cols)
       refuse(MUON_ERR_SHAPE, "group_stride: gradients overlap");
     if (n_groups > 1 && !offsets) refuse(MUON_ERR_INVALID_ARG, "offsets must not be NULL with more than one group");
+    if (x->ld_codes > kMaxIndex || x->ld_scales > kMaxIndex) refuse(MUON_ERR_SHAPE, "x: pitches must lie below 2^31");
     if (rows_per_token < 1) refuse(MUON_ERR_INVALID_ARG, "rows_per_token must be >= 1");
     if (!rows && dy->rows > x->rows * int64_t(rows_per_token))
       refuse(MUON_ERR_SHAPE, "without rows, dy has at most rows_per_token rows for each row of x");

@@ -36,6 +36,11 @@ constexpr int kBK = 32;        // slots a step
 constexpr int kThreads = 256;  // 4 waves, each 128 x 64 of the tile
 constexpr int kABytes = kBK * kBM * 2;
 constexpr int kXBytes = kBK * kBN * 2;
+// slot / per_token for slots below 2^31, as the high half of 2 slot * mul
+// shifted down; `end`: the first slot whose token lies outside x.
+struct TokenOf {
+  uint32_t mul, shift, end;
+};
 constexpr int kOutPitch = 64 + 4;  // floats; epilogue rows of a wave
 
 template <bool kF32>
@@ -73,25 +78,30 @@ __device__ inline Split3 split3(float a, float b) {
   return {h0 >> 16 | h1, m0 >> 16 | m1, l0 >> 16 | (l1 & 0xffff0000u)};
 }
 
-constexpr uint32_t kNoToken = 0xffffffffu;
-
-// 16 bytes from p, zeros from `end` on (the buffer's end is all that stops it).
-__device__ inline u32x4 load16(const char *p, const char *end) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (p + 16 <= end) {
-    v = *reinterpret_cast<const u32x4_any *>(p);
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t b = p + i < end ? uint8_t(p[i]) : 0u;
-      v[0] = v[0] >> 8 | v[1] << 24;
-      v[1] = v[1] >> 8 | v[2] << 24;
-      v[2] = v[2] >> 8 | v[3] << 24;
-      v[3] = v[3] >> 8 | b << 24;
-    }
-  }
-  return v;
+// Global memory, said so: the compiler then counts these loads apart from LDS
+// traffic.
+typedef const __attribute__((address_space(1))) char *GlobalPtr;
+__device__ inline u32x4 load16(GlobalPtr p) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) u32x4_any *>(p);
 }
+
+// Moves a run down by `bytes` (zeros behind it).
+template <int kDwords>
+__device__ inline void shift_down(uint32_t (&v)[kDwords], uint32_t bytes) {
+#pragma unroll
+  for (int d = kDwords / 2; d >= 1; d /= 2)
+    if (bytes & (4 * d)) {
+#pragma unroll
+      for (int i = 0; i < kDwords; ++i) v[i] = i + d < kDwords ? v[i + d] : 0u;
+    }
+#pragma unroll
+  for (int i = 0; i < kDwords; ++i) v[i] = __builtin_amdgcn_alignbyte(i + 1 < kDwords ? v[i + 1] : 0u, v[i], bytes & 3);
+}
+
+__device__ inline uint32_t raw_word(const Raw8<__bf16> &r, int i) { return r.v[i]; }
+__device__ inline uint32_t raw_word(const Raw8<float> &r, int i) { return r.v[i >> 2][i & 3]; }
+__device__ inline void raw_word(Raw8<__bf16> &r, int i, uint32_t w) { r.v[i] = w; }
+__device__ inline void raw_word(Raw8<float> &r, int i, uint32_t w) { r.v[i >> 2][i & 3] = w; }
 
 // What a thread holds of a step on its way to LDS: two rows' runs of 8
 // gradients, and two rows' runs of 16 codes with their scales.
@@ -100,21 +110,21 @@ struct Staged {
   Raw8<T> dy[2];
   u32x4 codes[2];
   uint32_t scale[2];
+  // bit r: row r adds nothing (past the group's end, or no such token); from
+  // bit 4 + 4 r and 16 + 8 r: by how many bytes the run of row r was read too
+  // early (codes, gradients), so as not to pass the buffer's end
+  uint32_t fix;
 };
 
-template <typename T, bool kPartial>
-__global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, uint32_t token_magic) {
+template <typename T, bool kRows, bool kPartial>
+__global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, const TokenOf div) {
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kPlanes = kF32 ? 3 : 1;
   constexpr int kStage = stage_bytes<kF32>();
   extern __shared__ __align__(256) char lds[];
 
-  // consecutive work (the tiles of one group) on one XCD, which shares an L2
-  const uint32_t per_xcd = (gridDim.x + 7) / 8;
-  uint32_t id = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  uint32_t id = blockIdx.x;
   const uint32_t tiles = uint32_t(a.tiles_n) * a.tiles_k;
-  const uint32_t work = tiles * a.splits * a.groups;
-  if (id >= work) return;
   const uint32_t tile = id % tiles;
   id /= tiles;
   const int split = int(id % uint32_t(a.splits)), group = int(id / uint32_t(a.splits));
@@ -132,61 +142,116 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, u
     lo += split * each;
     hi = lo + each < hi ? lo + each : hi;
   }
-  const int len = hi > lo ? int(hi - lo) : 0;
+  const int len = hi > lo && a.tokens > 0 ? int(hi - lo) : 0;
   const int steps = (len + kBK - 1) / kBK;
 
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
   const int srow = tid >> 4;               // staged rows srow and srow + 16 of a step
   const int dcol = n0 + (tid & 15) * 8;    // 8 gradients
   const int xcol = k0 + (tid & 15) * 16;   // 16 codes
-  // this run's first slot; a lane's place in a step's rows
-  const char *dy = static_cast<const char *>(a.dy) + lo * a.ld_dy * int64_t(sizeof(T));
-  const int64_t dyoff = (srow * a.ld_dy + dcol) * int64_t(sizeof(T));
-  const char *dy_end = static_cast<const char *>(a.dy) + ((a.slots - 1) * a.ld_dy + a.n) * int64_t(sizeof(T));
-  const char *codes_end = reinterpret_cast<const char *>(a.x.codes) + (a.tokens - 1) * a.x.ld_codes + a.k;
+  // this run's first slot, and where the buffers' last runs start (bytes)
+  const GlobalPtr dy = GlobalPtr(a.dy) + lo * a.ld_dy * int64_t(sizeof(T));
+  const int64_t dy_last = ((a.slots - 1 - lo) * a.ld_dy + a.n - 8) * int64_t(sizeof(T));
+  const int64_t dy_step = a.ld_dy * kBK * int64_t(sizeof(T));
   const int32_t *rows = a.rows + lo;
+  // runs that lie wholly past the tile's matrix read its first column instead
+  const int dc = dcol < a.n ? dcol : 0, xc = xcol < a.k ? xcol : 0;
+  const int64_t dy_at[2] = {(srow * a.ld_dy + dc) * int64_t(sizeof(T)),
+                            ((srow + 16) * a.ld_dy + dc) * int64_t(sizeof(T))};
+  const GlobalPtr codes = GlobalPtr(static_cast<const void *>(a.x.codes)) + xc;
+  const GlobalPtr scales = GlobalPtr(static_cast<const void *>(a.x.scales)) + (xc >> 7);
+  const uint32_t ld_codes = uint32_t(a.x.ld_codes), ld_scales = uint32_t(a.x.ld_scales);
+  // a token's run of codes stays in the buffer up to this one
+  const int64_t spare = (a.tokens - 1) * a.x.ld_codes + a.k - 16 - xc;
+  const int32_t safe = spare < 0 ? -1 : int32_t(spare / a.x.ld_codes);
 
-  // the tokens of a step's rows, one step ahead of their codes
-  auto token_of = [&](int step, uint32_t (&token)[2]) {
+  // the slots of a step's rows (a row past the end repeats the last)
+  auto slots_of = [&](int step, uint32_t (&slot)[2]) {
+    const int st = step < steps ? step : steps - 1;
+    const int most = len - 1 - st * kBK;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int at = step * kBK + srow + 16 * r;
-      token[r] = kNoToken;
-      if (at < len) {
-        const uint32_t v = uint32_t(a.rows ? rows[at] : int32_t(lo) + at);
-        uint32_t q = __umulhi(v, token_magic);  // v / per_token, one too few at most
-        if (v - q * uint32_t(a.per_token) >= uint32_t(a.per_token)) ++q;
-        if (q < uint32_t(a.tokens)) token[r] = q;
-      }
+      const int at = srow + 16 * r < most ? srow + 16 * r : most;
+      slot[r] = kRows ? uint32_t(rows[st * kBK + at]) : uint32_t(int32_t(lo) + st * kBK + at);
     }
   };
-  // Runs that reach past a row's end read what lies behind it in the buffer:
-  // those columns' sums are not stored. Nothing past the buffer is read.
-  auto fetch = [&](int step, const uint32_t (&token)[2], Staged<T> &st) {
-    const char *base = dy + int64_t(step) * (kBK * int64_t(sizeof(T))) * a.ld_dy;
+  // A step's loads are issued whatever their rows, and what does not count is
+  // mended on the way to LDS: a load that may be skipped would make every
+  // later wait one for all loads in flight. A run that reaches past its row's
+  // end reads what lies behind it in the buffer (those columns' sums are not
+  // stored), and one that would pass the buffer starts that much earlier.
+  auto fetch = [&](int step, uint32_t (&slot)[2], Staged<T> &st) {
+    st.fix = 0;
+    const int near = step < steps ? step : steps - 1;
+    const GlobalPtr base = dy + near * dy_step;
+    int64_t p[2] = {dy_at[0], dy_at[1]};
+    if (step * kBK + kBK > len || dy_last - near * dy_step < dy_step) {  // the last steps
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      st.dy[r] = Raw8<T>{};
-      st.codes[r] = u32x4{0u, 0u, 0u, 0u};
-      st.scale[r] = 127;
-      if (token[r] == kNoToken) continue;
-      if (dcol < a.n) {
-        const char *p = base + dyoff + r * 16 * int(sizeof(T)) * a.ld_dy;
-        if constexpr (kF32) {
-          st.dy[r].v[0] = load16(p, dy_end);
-          st.dy[r].v[1] = load16(p + 16, dy_end);
-        } else {
-          st.dy[r].v = load16(p, dy_end);
+      for (int r = 0; r < 2; ++r) {
+        if (step * kBK + srow + 16 * r >= len) st.fix |= 1u << r;
+        const int most = len - 1 - near * kBK;
+        const int at = srow + 16 * r < most ? srow + 16 * r : most;
+        p[r] = (at * a.ld_dy + dc) * int64_t(sizeof(T));
+        const int64_t over = p[r] - (dy_last - near * dy_step);
+        if (over > 0) {
+          st.fix |= uint32_t(over) << (16 + 8 * r);
+          p[r] -= over;
         }
       }
-      if (xcol < a.k) {
-        st.codes[r] = load16(reinterpret_cast<const char *>(a.x.codes) + int64_t(token[r]) * a.x.ld_codes + xcol, codes_end);
-        st.scale[r] = a.x.scales[int64_t(token[r]) * a.x.ld_scales + (xcol >> 7)];
+    }
+    uint32_t q[2], early[2] = {0, 0};
+    bool odd = false;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      q[r] = __umulhi(slot[r] << 1, div.mul) >> div.shift;  // slot / per_token
+      odd |= slot[r] >= div.end || int32_t(q[r]) > safe;
+    }
+    if (__any(odd)) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (slot[r] >= div.end) {  // no such token
+          st.fix |= 1u << r;
+          q[r] = 0;
+        }
+        if (int32_t(q[r]) > safe) {
+          early[r] = uint32_t(int64_t(q[r]) * a.x.ld_codes - spare);
+          st.fix |= early[r] << (4 + 4 * r);
+        }
       }
     }
+    slots_of(step + 2, slot);  // before the codes: waiting for it is not waiting for them
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if constexpr (kF32) {
+        st.dy[r].v[0] = load16(base + p[r]);
+        st.dy[r].v[1] = load16(base + p[r] + 16);
+      } else {
+        st.dy[r].v = load16(base + p[r]);
+      }
+      st.codes[r] = load16(codes + uint64_t(q[r]) * ld_codes - early[r]);
+      st.scale[r] = uint8_t(scales[uint64_t(q[r]) * ld_scales]);
+    }
   };
-  auto to_lds = [&](const Staged<T> &st, char *stage) {
+  auto to_lds = [&](Staged<T> &st, char *stage) {
     char *xs = stage + kPlanes * kABytes;
+    if (__any(st.fix != 0)) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        constexpr int kDwords = int(sizeof(T)) * 2;
+        uint32_t d[kDwords], c[4];
+#pragma unroll
+        for (int i = 0; i < kDwords; ++i) d[i] = raw_word(st.dy[r], i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = st.codes[r][i];
+        shift_down(c, st.fix >> (4 + 4 * r) & 15);
+        shift_down(d, st.fix >> (16 + 8 * r) & 31);
+        const bool none = st.fix >> r & 1;
+#pragma unroll
+        for (int i = 0; i < kDwords; ++i) raw_word(st.dy[r], i, none ? 0u : d[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.codes[r][i] = none ? 0u : c[i];
+      }
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = srow + 16 * r;
@@ -244,45 +309,74 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, u
     const s16x4 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)((lds_char)base + off + 4 * pitch));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(p, q, 0, 1, 2, 3, 4, 5, 6, 7));
   };
+  // The fragments of a group (16 slots of one part of dy) are read while the
+  // products of the group before run.
+  bf16x8 af[2][4], bf[2][2];
+  auto read_x = [&](const char *stage, int kk) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) bf[kk & 1][j] = frag(stage + kPlanes * kABytes + kk * 16 * kBN * 2, xoff[j], kBN * 2);
+  };
+  auto read_dy = [&](const char *stage, int g) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      af[g & 1][i] = frag(stage + (g % kPlanes) * kABytes + (g / kPlanes) * 16 * kBM * 2, aoff[i], kBM * 2);
+  };
+  constexpr int kGroups = kBK / 16 * kPlanes;
   auto compute = [&](const char *stage) {
-    const char *xs = stage + kPlanes * kABytes;
 #pragma unroll
-    for (int kk = 0; kk < kBK / 16; ++kk) {
-      bf16x8 bf[2];
+    for (int g = 0; g < kGroups; ++g) {
+      if (g + 1 < kGroups) {
+        if ((g + 1) % kPlanes == 0) read_x(stage, (g + 1) / kPlanes);
+        read_dy(stage, g + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) bf[j] = frag(xs + kk * 16 * kBN * 2, xoff[j], kBN * 2);
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int pl = 0; pl < kPlanes; ++pl)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bf16x8 af = frag(stage + pl * kABytes + kk * 16 * kBM * 2, aoff[i], kBM * 2);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af, bf[j], acc[i][j], 0, 0, 0);
-        }
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[g & 1][i], bf[g / kPlanes & 1][j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  if (steps > 0) {
-    Staged<T> st;
-    uint32_t tok[2];
-    token_of(0, tok);
-    fetch(0, tok, st);
-    token_of(1, tok);
-    to_lds(st, lds);
-    fetch(1, tok, st);
-    token_of(2, tok);
+  // Step s is in LDS; step s + 1, loaded earlier, goes to the other stage, and
+  // one further on is fetched into its registers.
+  auto pass = [&](int s, int fetched, Staged<T> &st, uint32_t (&slot)[2], char *now, char *next) {
+    read_x(now, 0);
+    read_dy(now, 0);
+    to_lds(st, next);
+    fetch(fetched, slot, st);
+    __builtin_amdgcn_sched_barrier(0);
+    if (s < steps) compute(now);
     __syncthreads();
-    // step s: LDS holds it; s + 1 goes to the other stage, s + 2 is fetched
-    int at = 0;
-#pragma unroll 1
-    for (int s = 0; s < steps; ++s) {
-      to_lds(st, lds + (kStage - at));
-      fetch(s + 2, tok, st);
-      token_of(s + 3, tok);
-      __builtin_amdgcn_sched_barrier(0);
-      compute(lds + at);
+  };
+  if (steps > 0) {
+    uint32_t t0[2], t1[2];
+    slots_of(0, t0);
+    slots_of(1, t1);
+    if constexpr (kF32) {  // three products a step hide a load by themselves
+      Staged<T> st;
+      fetch(0, t0, st);
+      to_lds(st, lds);
+      fetch(1, t1, st);
       __syncthreads();
-      at = kStage - at;
+#pragma unroll 1
+      for (int s = 0; s < steps; s += 2) {
+        pass(s, s + 2, st, t0, lds, lds + kStage);
+        pass(s + 1, s + 3, st, t1, lds + kStage, lds);
+      }
+    } else {
+      Staged<T> s0, s1;
+      fetch(0, t0, s0);
+      fetch(1, t1, s1);
+      to_lds(s0, lds);
+      fetch(2, t0, s0);
+      __syncthreads();
+#pragma unroll 1
+      for (int s = 0; s < steps; s += 2) {
+        pass(s, s + 3, s1, t1, lds, lds + kStage);
+        pass(s + 1, s + 4, s0, t0, lds + kStage, lds);
+      }
     }
   }
 
@@ -321,6 +415,30 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, u
   }
 }
 
+// Buffers that hold less than one run of the tiled kernel (gradients of fewer
+// than 8 elements, codes of fewer than 16): a thread per element of the
+// result.
+template <typename T>
+__global__ __launch_bounds__(256) void wgrad_tiny_kernel(const WgradArgs a) {
+  const int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (u >= int64_t(a.groups) * a.n * a.k) return;
+  const int k = int(u % a.k), n = int(u / a.k % a.n), group = int(u / (int64_t(a.n) * a.k));
+  int64_t lo = 0, hi = a.slots;
+  if (a.offsets) {
+    lo = a.offsets[group] < 0 ? 0 : a.offsets[group];
+    hi = a.offsets[group + 1] > a.slots ? a.slots : a.offsets[group + 1];
+  }
+  float s = 0.f;
+  for (int64_t i = lo; i < hi; ++i) {
+    const uint32_t token = uint32_t(a.rows ? a.rows[i] : int32_t(i)) / uint32_t(a.per_token);
+    if (token >= uint32_t(a.tokens)) continue;
+    const float x = bits_f32(decode2<0>(a.x.codes[token * a.x.ld_codes + k], 1.f) << 16) *
+                    scale_value(a.x.scales[token * a.x.ld_scales + (k >> 7)]);
+    s = fmaf(float(static_cast<const T *>(a.dy)[i * a.ld_dy + n]), x, s);
+  }
+  static_cast<T *>(a.out)[group * a.stride + n * a.ld_out + k] = T(s);
+}
+
 // Adds the partials in split order; a thread takes eight columns of a row.
 template <typename T>
 __global__ __launch_bounds__(256) void wgrad_join_kernel(const WgradArgs a) {
@@ -348,14 +466,23 @@ hipError_t wgrad(const WgradArgs &a, hipStream_t s) {
   constexpr int kEpilogue = 4 * 32 * kOutPitch * 4;
   constexpr int kLds = 2 * kStage > kEpilogue ? 2 * kStage : kEpilogue;
   const uint32_t work = uint32_t(a.tiles_n) * a.tiles_k * a.splits * a.groups;
-  const uint32_t magic =
-      uint32_t(std::min<uint64_t>((uint64_t(1) << 32) / uint32_t(a.per_token), 0xffffffffu));
-  const dim3 grid((work + 7) / 8 * 8);
-  if (a.splits == 1) {
-    hipLaunchKernelGGL((wgrad_kernel<T, false>), grid, dim3(kThreads), kLds, s, a, magic);
+  // mul = ceil(2^(31 + shift) / d) with 2^(shift - 1) < d <= 2^shift: exact up
+  // to 2^31 (the excess mul d - 2^(31 + shift) < d adds less than 1 / d there)
+  const uint64_t d = uint64_t(a.per_token);
+  TokenOf div{0, 0, uint32_t(std::min<uint64_t>(uint64_t(a.tokens) * d, uint64_t(1) << 31))};
+  while ((uint64_t(1) << div.shift) < d) ++div.shift;
+  div.mul = uint32_t(((uint64_t(1) << (31 + div.shift)) + d - 1) / d);
+  if (a.slots > 0 && a.tokens > 0 &&
+      ((a.slots - 1) * a.ld_dy + a.n < 8 || (a.tokens - 1) * a.x.ld_codes + a.k < 16)) {
+    const int64_t total = int64_t(a.groups) * a.n * a.k;
+    hipLaunchKernelGGL(wgrad_tiny_kernel<T>, dim3(unsigned((total + 255) / 256)), dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((wgrad_kernel<T, true>), grid, dim3(kThreads), kLds, s, a, magic);
+  const dim3 grid(work);
+  auto kernel = a.splits == 1 ? (a.rows ? wgrad_kernel<T, true, false> : wgrad_kernel<T, false, false>)
+                              : (a.rows ? wgrad_kernel<T, true, true> : wgrad_kernel<T, false, true>);
+  hipLaunchKernelGGL(kernel, grid, dim3(kThreads), kLds, s, a, div);
+  if (a.splits == 1) return hipGetLastError();
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t total = int64_t(a.groups) * a.n * ((a.k + 7) / 8);
