@@ -213,6 +213,11 @@ muon_status muon_set_workspace(void *device_ptr, size_t bytes);
 /* The workspace set on this thread ((NULL, 0) if none). */
 muon_status muon_get_workspace(void **device_ptr, size_t *bytes);
 
+/* muon_get_workspace and muon_set_workspace in one: the workspace set before
+ * goes to *old_ptr and *old_bytes (NULL: not wanted). A call that fails
+ * changes nothing. */
+muon_status muon_exchange_workspace(void *device_ptr, size_t bytes, void **old_ptr, size_t *old_bytes);
+
 /* Options used by muon_step (and eps by muon_ns_batched) on this thread.
  * Defaults: iters 5, coeffs {3.4445, -4.7750, 2.0315}, eps 1e-7,
  * mode MUON_NS_FULL | MUON_PACK_COST | MUON_AA_PLAIN. coeffs NULL keeps the

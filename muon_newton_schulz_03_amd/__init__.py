@@ -7,8 +7,10 @@ stream. There is no CPU fallback: if the library is missing, every call
 raises.
 """
 import ctypes
+import functools
 import json
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmuon.so")
@@ -45,7 +47,7 @@ EXPORTED = (
     "muon_ns_batched", "muon_step", "muon_set_stream", "muon_workspace_size",
     "muon_workspace_min_size", "muon_set_workspace", "muon_set_step_options",
     "muon_last_error", "muon_plan_info", "muon_set_phase_timing", "muon_phase_times",
-    "muon_place", "muon_adamw_step", "muon_step_noalloc", "muon_get_workspace",
+    "muon_place", "muon_adamw_step", "muon_step_noalloc", "muon_get_workspace", "muon_exchange_workspace",
     "muon_layernorm_forward", "muon_layernorm_backward", "muon_layernorm_workspace_size",
     "muon_ckpt_save", "muon_ckpt_load", "muon_ckpt_weight_grad", "muon_ckpt_weight_grad_workspace_size",
     "muon_route_forward", "muon_route_backward", "muon_route_workspace_size",
@@ -119,6 +121,7 @@ def load_library(path=LIB_PATH):
                         ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double),
                         ctypes.POINTER(ctypes.c_double)], ctypes.c_int),
         "muon_get_workspace": ([ctypes.POINTER(ctypes.c_void_p), sz], ctypes.c_int),
+        "muon_exchange_workspace": ([ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(ctypes.c_void_p), sz], ctypes.c_int),
     }
     # the training operators take packed descriptors (bytes) where the header has struct pointers
     p, i32, i64, f = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
@@ -365,42 +368,42 @@ def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr=1e-3, beta1=0.9, beta
 # training operators
 # ---------------------------------------------------------------------------
 
-import struct as _struct  # noqa: E402
+_MAT = struct.Struct("=Qqqqii").pack   # muon_mat: data, rows, cols, ld, dtype, col_blocks
+_CKPT = struct.Struct("=QQqqqq").pack  # muon_ckpt
+_torch = _codes = None
 
-_MAT = _struct.Struct("=Qqqqii").pack   # muon_mat: data, rows, cols, ld, dtype, col_blocks
-_CKPT = _struct.Struct("=QQqqqq").pack  # muon_ckpt
-_codes = None
 
+# The smallest calls take about as long here as on the GPU, so these helpers ask
+# a tensor for each fact once.
 
 def _on_gpu(name, t, device):
     """The device of a tensor that a kernel will touch, which has to be the others'."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a GPU tensor")
     d = t.get_device()
-    if device is not None and d != device:
-        raise ValueError(f"{name}: on another device than the other tensors")
+    if d != device or d < 0:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a GPU tensor")
+        if device is not None:
+            raise ValueError(f"{name}: on another device than the other tensors")
     return d
 
 
 def _mat(name, t, device):
     """Packed muon_mat of a 2-D tensor with unit column stride (NULL for None)."""
-    global _codes
     if t is None:
         return None
-    _on_gpu(name, t, device)
-    if t.dim() != 2:
+    if t.get_device() != device:
+        _on_gpu(name, t, device)
+    strides = t.stride()
+    if len(strides) != 2:
         raise ValueError(f"{name}: expected a 2-D tensor")
+    ld, unit = strides
     rows, cols = t.shape
-    ld, unit = t.stride()
     if cols > 1 and unit != 1:
         raise ValueError(f"{name}: expected unit column stride")
     if rows <= 1 or ld < cols:
         if rows > 1:
             raise ValueError(f"{name}: rows overlap")
         ld = cols
-    if _codes is None:
-        import torch
-        _codes = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
     code = _codes.get(t.dtype)
     if code is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
@@ -411,7 +414,8 @@ def _vec(name, t, dtype, shape, device):
     """Address of a contiguous tensor of the given dtype and shape (None for None)."""
     if t is None:
         return None
-    _on_gpu(name, t, device)
+    if t.get_device() != device:
+        _on_gpu(name, t, device)
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -464,42 +468,36 @@ class Checkpoint:
 
 def _enter(t):
     """The device index of a call's first tensor; its current stream becomes the call's."""
-    import torch
+    global _torch, _codes
+    if _codes is None:
+        import torch
+        _torch, _codes = torch, {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
     device = _on_gpu("argument", t, None)
-    if device != torch.cuda.current_device():
+    if device != _torch.cuda.current_device():
         raise ValueError("the tensors are not on the current device")
-    _check(lib().muon_set_stream(torch.cuda.current_stream(device).cuda_stream))
+    # the raw handle of torch.cuda.current_stream, without an object around it
+    _check((_lib or lib()).muon_set_stream(_torch._C._cuda_getCurrentRawStream(device)))
     return device
 
 
-class _Scratch:
-    """The workspace of one call: the caller's (a uint8 tensor), or a temporary
-    one from torch's allocator, whose memory is reused in stream order only.
-    What the thread had set before is set again afterwards."""
-
-    def __init__(self, nbytes, workspace, device):
-        self.nbytes, self.buf = nbytes, workspace
-        if nbytes:
-            import torch
-            if workspace is None:
-                self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            else:
-                _on_gpu("workspace", workspace, device)
-                if not workspace.is_contiguous():
-                    raise ValueError("workspace: expected a contiguous tensor")
-
-    def __enter__(self):
-        if self.nbytes:
-            self.old, self.old_bytes = ctypes.c_void_p(), ctypes.c_size_t()
-            _check(_lib.muon_get_workspace(ctypes.byref(self.old), ctypes.byref(self.old_bytes)))
-            _check(_lib.muon_set_workspace(self.buf.data_ptr(), self.buf.numel() * self.buf.element_size()))
-
-    def __exit__(self, *exc):
-        if self.nbytes:
-            err = exc[0] is None
-            st = _lib.muon_set_workspace(self.old, self.old_bytes)
-            if err:
-                _check(st)
+def _with_scratch(nbytes, workspace, device, fn, *args):
+    """Calls fn with a workspace of nbytes: the caller's (a uint8 tensor), or a
+    temporary one from torch's allocator, whose memory is reused in stream order
+    only. What the thread had set before is set again afterwards."""
+    if not nbytes:
+        return _check(fn(*args))
+    if workspace is None:
+        workspace = _torch.empty(nbytes, dtype=_torch.uint8, device="cuda")
+    else:
+        _on_gpu("workspace", workspace, device)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous tensor")
+    old, old_bytes = ctypes.c_void_p(), ctypes.c_size_t()
+    _check(_lib.muon_exchange_workspace(workspace.data_ptr(), workspace.nbytes, old, old_bytes))
+    try:
+        _check(fn(*args))
+    finally:
+        _lib.muon_exchange_workspace(old, old_bytes, None, None)
 
 
 def _size(fn, *args):
@@ -508,14 +506,18 @@ def _size(fn, *args):
     return out.value
 
 
+# the sizes depend on these numbers alone
+@functools.lru_cache(256)
 def muon_layernorm_workspace_size(rows, cols):
     return _size(lib().muon_layernorm_workspace_size, rows, cols)
 
 
+@functools.lru_cache(256)
 def muon_ckpt_weight_grad_workspace_size(dtype, slots, n, k, groups=1):
     return _size(lib().muon_ckpt_weight_grad_workspace_size, dtype, slots, n, k, groups)
 
 
+@functools.lru_cache(256)
 def muon_route_workspace_size(tokens, experts, topk):
     return _size(lib().muon_route_workspace_size, tokens, experts, topk)
 
@@ -524,9 +526,8 @@ def muon_layernorm_forward(x, y, mean=None, rstd=None, weight=None, bias=None, e
     """y = layer norm of x's rows (see muon.h). mean, rstd: float32 vectors
     that the backward pass reads; weight, bias: 1 x cols; ckpt: a Checkpoint
     that receives y in 8 bits in the same pass."""
-    import torch
     d = _enter(x)
-    f32, rows = torch.float32, x.shape[:1]
+    f32, rows = _torch.float32, x.shape[:1]
     if ckpt is not None:
         _on_gpu("ckpt", ckpt.codes, d)
     _check(_lib.muon_layernorm_forward(
@@ -538,14 +539,12 @@ def muon_layernorm_backward(dy, x, mean, rstd, dx, weight=None, dweight=None, db
     """dx, and where given dweight and dbias (1 x cols), of the layer norm (see
     muon.h). workspace: a uint8 tensor of muon_layernorm_workspace_size bytes
     (default: a temporary one)."""
-    import torch
     d = _enter(dy)
-    f32, rows = torch.float32, dy.shape[:1]
+    f32, rows = _torch.float32, dy.shape[:1]
     args = (_mat("dy", dy, d), _mat("x", x, d), _vec("mean", mean, f32, rows, d), _vec("rstd", rstd, f32, rows, d),
             _mat("dx", dx, d), _mat("weight", weight, d), _mat("dweight", dweight, d), _mat("dbias", dbias, d))
     need = muon_layernorm_workspace_size(*dy.shape) if dweight is not None or dbias is not None else 0
-    with _Scratch(need, workspace, d):
-        _check(_lib.muon_layernorm_backward(*args))
+    _with_scratch(need, workspace, d, _lib.muon_layernorm_backward, *args)
 
 
 def muon_ckpt_save(x, ckpt):
@@ -568,7 +567,6 @@ def muon_ckpt_weight_grad(dy, ckpt, grads, offsets=None, rows=None, rows_per_tok
     dy: slots x n; grads: groups x n x k (its matrices are what muon_step
     takes); offsets (groups + 1) and rows (slots): int32, as
     muon_route_forward writes them with rows_per_token = topk."""
-    import torch
     d = _enter(dy)
     if grads.dim() != 3:
         raise ValueError("grads: expected a 3-D tensor (groups x n x k)")
@@ -587,10 +585,10 @@ def muon_ckpt_weight_grad(dy, ckpt, grads, offsets=None, rows=None, rows_per_tok
     if groups > 1 and offsets is None:
         raise ValueError("offsets: needed with more than one group")
     args = (dy_mat, ckpt._packed, _MAT(grads.data_ptr(), n, k, ld, code, 1), stride, groups,
-            _vec("offsets", offsets, torch.int32, (groups + 1,), d), _vec("rows", rows, torch.int32, dy.shape[:1], d),
+            _vec("offsets", offsets, _torch.int32, (groups + 1,), d), _vec("rows", rows, _torch.int32, dy.shape[:1], d),
             rows_per_token)
-    with _Scratch(muon_ckpt_weight_grad_workspace_size(code, dy.shape[0], n, k, groups), workspace, d):
-        _check(_lib.muon_ckpt_weight_grad(*args))
+    _with_scratch(muon_ckpt_weight_grad_workspace_size(code, dy.shape[0], n, k, groups), workspace, d,
+                  _lib.muon_ckpt_weight_grad, *args)
 
 
 def muon_route_forward(logits, indices, weights, counts, offsets, rows, loss, alpha=1e-2, renormalize=True,
@@ -599,32 +597,29 @@ def muon_route_forward(logits, indices, weights, counts, offsets, rows, loss, al
     experts; indices (int32) and weights (float32): tokens x topk, which sets
     topk; counts and offsets: experts + 1, rows: tokens * topk, all int32;
     loss: one float32. All outputs are overwritten."""
-    import torch
     d = _enter(logits)
     m = _mat("logits", logits, d)
     tokens, experts = logits.shape
     if indices.dim() != 2:
         raise ValueError("indices: expected a 2-D tensor (tokens x topk)")
     topk = indices.shape[1]
-    i32, pair, table = torch.int32, (tokens, topk), (experts + 1,)
+    i32, pair, table = _torch.int32, (tokens, topk), (experts + 1,)
     args = (m, topk, int(renormalize), alpha, _vec("indices", indices, i32, pair, d),
-            _vec("weights", weights, torch.float32, pair, d), _vec("counts", counts, i32, table, d),
+            _vec("weights", weights, _torch.float32, pair, d), _vec("counts", counts, i32, table, d),
             _vec("offsets", offsets, i32, table, d), _vec("rows", rows, i32, (tokens * topk,), d),
-            _vec("loss", loss, torch.float32, (1,), d))
-    with _Scratch(muon_route_workspace_size(tokens, experts, topk), workspace, d):
-        _check(_lib.muon_route_forward(*args))
+            _vec("loss", loss, _torch.float32, (1,), d))
+    _with_scratch(muon_route_workspace_size(tokens, experts, topk), workspace, d, _lib.muon_route_forward, *args)
 
 
 def muon_route_backward(logits, indices, counts, dlogits, dweights=None, dloss=None, alpha=1e-2, renormalize=True):
     """Gradient of loss * dloss + (weights * dweights).sum() with respect to
     the logits (see muon.h)."""
-    import torch
     d = _enter(logits)
     if indices.dim() != 2:
         raise ValueError("indices: expected a 2-D tensor (tokens x topk)")
     pair = (logits.shape[0], indices.shape[1])
-    f32 = torch.float32
+    f32 = _torch.float32
     _check(_lib.muon_route_backward(
-        _mat("logits", logits, d), pair[1], int(renormalize), alpha, _vec("indices", indices, torch.int32, pair, d),
-        _vec("counts", counts, torch.int32, (logits.shape[1] + 1,), d), _vec("dweights", dweights, f32, pair, d),
+        _mat("logits", logits, d), pair[1], int(renormalize), alpha, _vec("indices", indices, _torch.int32, pair, d),
+        _vec("counts", counts, _torch.int32, (logits.shape[1] + 1,), d), _vec("dweights", dweights, f32, pair, d),
         _vec("dloss", dloss, f32, (1,), d), _mat("dlogits", dlogits, d)))

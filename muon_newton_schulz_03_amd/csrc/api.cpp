@@ -455,6 +455,16 @@ muon_status muon_get_workspace(void **device_ptr, size_t *bytes) {
   return ok();
 }
 
+muon_status muon_exchange_workspace(void *device_ptr, size_t bytes, void **old_ptr, size_t *old_bytes) {
+  void *const was = g_state.ws;
+  const size_t had = g_state.ws_bytes;
+  const muon_status st = muon_set_workspace(device_ptr, bytes);
+  if (st != MUON_OK) return st;
+  if (old_ptr) *old_ptr = was;
+  if (old_bytes) *old_bytes = had;
+  return st;
+}
+
 muon_status muon_set_step_options(int32_t iters, const float coeffs[3], float eps, uint32_t mode) {
   Error err;
   if (!check_iters(iters, &err) || !validate_mode(mode, &err)) return fail(err);

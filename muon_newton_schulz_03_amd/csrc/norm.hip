@@ -10,23 +10,24 @@
 // row belongs to one wave (up to 1024 columns) or one workgroup.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "lanes.h"
 #include "train.h"
 
 namespace muon {
 namespace {
 
-template <bool kF32>
-__device__ inline void load_vec8(const void *p, int col, int n, float (&f)[8]) {
-  if constexpr (kF32) {
-    const Raw8<float> r = load8(static_cast<const float *>(p) + col, n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = r.get(i);
-  } else {
-    const Raw8<__bf16> r = load8(static_cast<const __bf16 *>(p) + col, n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = r.get(i);
-  }
+// Runs of a row whose length is a whole number of runs (kWhole) are there or
+// not; else the last one may be cut. The first form has no branch but the
+// lanes' own.
+template <bool kWhole, typename T>
+__device__ inline Raw8<T> load_run(const T *p, int n) {
+  return load8(p, kWhole ? (n > 0 ? 8 : 0) : n);
+}
+template <bool kWhole, typename T>
+__device__ inline void store_run(T *p, const Raw8<T> &r, int n) {
+  store8(p, r, kWhole ? 8 : n);
 }
 
 // Sums of one or two values over the kTpr threads of a row; `slot` toggles
@@ -54,10 +55,11 @@ __device__ inline void row_sum(float (&v)[kN], float *lds, int &slot) {
 }
 
 // kTpr threads a row, kNv runs of 8 columns a thread.
-template <typename T, bool kWf32, bool kCkpt, int kTpr, int kNv>
+template <typename T, bool kWf32, bool kCkpt, bool kWhole, int kTpr, int kNv>
 __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const NormFwdArgs a) {
   constexpr int kBlock = kTpr < 256 ? 256 : kTpr;
   __shared__ float lds[2 * (kTpr / 64)];
+  using W = std::conditional_t<kWf32, float, __bf16>;
   int slot = 0;
   const int t = int(threadIdx.x) % kTpr;
   const int64_t row = int64_t(blockIdx.x) * (kBlock / kTpr) + int(threadIdx.x) / kTpr;
@@ -69,15 +71,14 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
 #pragma unroll
   for (int v = 0; v < kNv; ++v) {
     const int c = (v * kTpr + t) * 8;
-    xr[v] = load8(x + c, a.cols - c);
+    xr[v] = load_run<kWhole>(x + c, a.cols - c);
   }
 #pragma unroll
   for (int v = 0; v < kNv; ++v)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[0] += xr[v].get(i);
+    s[0] += ((xr[v].get(0) + xr[v].get(1)) + (xr[v].get(2) + xr[v].get(3))) +
+            ((xr[v].get(4) + xr[v].get(5)) + (xr[v].get(6) + xr[v].get(7)));
   row_sum<kTpr, 1>(s, lds, slot);
-  const float inv_c = 1.f / float(a.cols);
-  const float mean = s[0] * inv_c;
+  const float mean = s[0] / float(a.cols);
   s[0] = 0.f;
 #pragma unroll
   for (int v = 0; v < kNv; ++v) {
@@ -89,7 +90,7 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
     }
   }
   row_sum<kTpr, 1>(s, lds, slot);
-  const float rstd = 1.f / sqrtf(s[0] * inv_c + a.eps);
+  const float rstd = 1.f / sqrtf(s[0] / float(a.cols) + a.eps);
   if (t == 0) {
     if (a.mean) a.mean[row] = mean;
     if (a.rstd) a.rstd[row] = rstd;
@@ -98,15 +99,15 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
   for (int v = 0; v < kNv; ++v) {
     const int c = (v * kTpr + t) * 8, n = a.cols - c;
     if (!kCkpt && n <= 0) break;
-    float f[8], w[8], b[8];
+    float f[8];
+    const float one[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    Raw8<W> w = pack8(one, W()), b{};
+    if (a.w) w = load_run<kWhole>(static_cast<const W *>(a.w) + c, n);
+    if (a.b) b = load_run<kWhole>(static_cast<const W *>(a.b) + c, n);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f, b[i] = 0.f;
-    if (a.w) load_vec8<kWf32>(a.w, c, n, w);
-    if (a.b) load_vec8<kWf32>(a.b, c, n, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fmaf((xr[v].get(i) - mean) * rstd, w[i], b[i]);
+    for (int i = 0; i < 8; ++i) f[i] = fmaf((xr[v].get(i) - mean) * rstd, w.get(i), b.get(i));
     const Raw8<T> r = pack8(f, T());
-    if (n > 0) store8(y + c, r, n);
+    if (n > 0) store_run<kWhole>(y + c, r, n);
     if constexpr (kCkpt) {
       // the checkpoint of y as stored; its groups of 128 columns are 16 lanes
       uint32_t m = 0;
@@ -125,58 +126,69 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
   }
 }
 
-template <typename T, bool kWf32, bool kCkpt>
+template <typename T, bool kWf32, bool kCkpt, bool kWhole>
 hipError_t fwd(const NormFwdArgs &a, hipStream_t s) {
   auto go = [&](auto kernel, int tpr) {
     const int per = tpr < 256 ? 256 / tpr : 1;
     hipLaunchKernelGGL(kernel, dim3(unsigned((a.rows + per - 1) / per)), dim3(tpr < 256 ? 256 : tpr), 0, s, a);
     return hipGetLastError();
   };
-  if (a.cols <= 512) return go(norm_fwd_kernel<T, kWf32, kCkpt, 64, 1>, 64);
-  if (a.cols <= 1024) return go(norm_fwd_kernel<T, kWf32, kCkpt, 64, 2>, 64);
-  if (a.cols <= 2048) return go(norm_fwd_kernel<T, kWf32, kCkpt, 256, 1>, 256);
-  if (a.cols <= 4096) return go(norm_fwd_kernel<T, kWf32, kCkpt, 256, 2>, 256);
-  if (a.cols <= 8192) return go(norm_fwd_kernel<T, kWf32, kCkpt, 256, 4>, 256);
-  if (a.cols <= 16384) return go(norm_fwd_kernel<T, kWf32, kCkpt, 1024, 2>, 1024);
-  return go(norm_fwd_kernel<T, kWf32, kCkpt, 1024, 4>, 1024);
+  if (a.cols <= 512) return go(norm_fwd_kernel<T, kWf32, kCkpt, kWhole, 64, 1>, 64);
+  if (a.cols <= 1024) return go(norm_fwd_kernel<T, kWf32, kCkpt, kWhole, 64, 2>, 64);
+  if (a.cols <= 2048) return go(norm_fwd_kernel<T, kWf32, kCkpt, kWhole, 256, 1>, 256);
+  if (a.cols <= 4096) return go(norm_fwd_kernel<T, kWf32, kCkpt, kWhole, 256, 2>, 256);
+  if (a.cols <= 8192) return go(norm_fwd_kernel<T, kWf32, kCkpt, kWhole, 256, 4>, 256);
+  if (a.cols <= 16384) return go(norm_fwd_kernel<T, kWf32, kCkpt, kWhole, 1024, 2>, 1024);
+  return go(norm_fwd_kernel<T, kWf32, kCkpt, kWhole, 1024, 4>, 1024);
 }
 
 // Each workgroup takes rows b, b + blocks, ... (kBlock / kTpr at a time) and
-// keeps its columns' sums of dy xh and dy in registers; the next rows' loads
-// are in flight while the current ones are reduced.
-template <typename T, bool kWf32, int kTpr, int kNv>
+// keeps its columns' sums of dy xh and dy, and the weight, in registers; the
+// loads of its next rows are in flight while one is reduced.
+template <typename T, bool kWf32, bool kWhole, int kTpr, int kNv>
 __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_bwd_kernel(const NormBwdArgs a) {
   constexpr int kBlock = kTpr < 256 ? 256 : kTpr;
   constexpr int kPer = kBlock / kTpr;
+  using W = std::conditional_t<kWf32, float, __bf16>;
   __shared__ float lds[2 * (kTpr / 64) * 2];
   __shared__ float comb[kPer > 1 ? kTpr * kNv * 8 : 1];
   int slot = 0;
   const int t = int(threadIdx.x) % kTpr, sub = int(threadIdx.x) / kTpr;
   const float inv_c = 1.f / float(a.cols);
-  Raw8<T> xr[kNv], dr[kNv], xn[kNv], dn[kNv];
+  Raw8<T> xn[kNv], dn[kNv];
+  Raw8<W> w[kNv];
+  float mn, rn;
   float aw[kNv][8], ab[kNv][8];
 #pragma unroll
-  for (int v = 0; v < kNv; ++v)
+  for (int v = 0; v < kNv; ++v) {
+    const int c = (v * kTpr + t) * 8;
+    if (a.w) {
+      w[v] = load_run<kWhole>(static_cast<const W *>(a.w) + c, a.cols - c);
+    } else {
+      const float one[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+      w[v] = pack8(one, W());
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) aw[v][i] = ab[v][i] = 0.f;
-  float mn = 0.f, rn = 0.f;
+  }
+  // 0, in a vector register: a value known to be the same in every lane would
+  // be moved to a scalar one at once, which waits for all loads before it
+  int lane0 = 0;
+  asm volatile("" : "+v"(lane0));
   auto fetch = [&](int64_t row) {
-    if (row >= a.rows) {
-#pragma unroll
-      for (int v = 0; v < kNv; ++v) xn[v] = Raw8<T>{}, dn[v] = Raw8<T>{};
-      mn = rn = 0.f;
-      return;
-    }
+    const bool there = row < a.rows;
     const T *x = static_cast<const T *>(a.x) + row * a.ld_x;
     const T *d = static_cast<const T *>(a.dy) + row * a.ld_dy;
 #pragma unroll
     for (int v = 0; v < kNv; ++v) {
-      const int c = (v * kTpr + t) * 8;
-      xn[v] = load8(x + c, a.cols - c);
-      dn[v] = load8(d + c, a.cols - c);
+      const int c = (v * kTpr + t) * 8, n = there ? a.cols - c : 0;
+      xn[v] = load_run<kWhole>(x + c, n);
+      dn[v] = load_run<kWhole>(d + c, n);
     }
-    mn = a.mean[row];
-    rn = a.rstd[row];
+    const int64_t at = (there ? row : 0) + lane0;
+    const float m = a.mean[at], r = a.rstd[at];
+    mn = there ? m : 0.f;
+    rn = there ? r : 0.f;
   };
   const int64_t step = int64_t(a.blocks) * kPer;
   int64_t base = int64_t(blockIdx.x) * kPer;
@@ -184,26 +196,21 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_bwd_kernel(const
   for (; base < a.rows; base += step) {
     const int64_t row = base + sub;
     const float mean = mn, rstd = rn;
+    Raw8<T> xr[kNv], dr[kNv];
 #pragma unroll
     for (int v = 0; v < kNv; ++v) xr[v] = xn[v], dr[v] = dn[v];
     fetch(row + step);
     float s[2] = {0.f, 0.f};
 #pragma unroll
-    for (int v = 0; v < kNv; ++v) {
-      const int c = (v * kTpr + t) * 8, n = a.cols - c;
-      float w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.f;
-      if (a.w) load_vec8<kWf32>(a.w, c, n, w);
+    for (int v = 0; v < kNv; ++v)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = dr[v].get(i), xh = (xr[v].get(i) - mean) * rstd, h = d * w[i];
+        const float g = dr[v].get(i), xh = (xr[v].get(i) - mean) * rstd, h = g * w[v].get(i);
         s[0] += h;
         s[1] = fmaf(h, xh, s[1]);
-        aw[v][i] = fmaf(d, xh, aw[v][i]);
-        ab[v][i] += d;
+        aw[v][i] = fmaf(g, xh, aw[v][i]);
+        ab[v][i] += g;
       }
-    }
     row_sum<kTpr, 2>(s, lds, slot);
     if (row < a.rows) {
       const float m0 = s[0] * inv_c, m1 = s[1] * inv_c;
@@ -212,25 +219,21 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_bwd_kernel(const
       for (int v = 0; v < kNv; ++v) {
         const int c = (v * kTpr + t) * 8, n = a.cols - c;
         if (n <= 0) break;
-        float w[8], f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 1.f;
-        if (a.w) load_vec8<kWf32>(a.w, c, n, w);
+        float f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float xh = (xr[v].get(i) - mean) * rstd;
-          f[i] = rstd * (dr[v].get(i) * w[i] - m0 - xh * m1);
+          f[i] = rstd * (dr[v].get(i) * w[v].get(i) - m0 - xh * m1);
         }
-        store8(dx + c, pack8(f, T()), n);
+        store_run<kWhole>(dx + c, pack8(f, T()), n);
       }
     }
   }
   if (!a.sums) return;
   float *part = a.part + int64_t(blockIdx.x) * 2 * a.cols;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    float(&acc)[kNv][8] = which ? ab : aw;
+  auto leave = [&](float(&acc)[kNv][8], float *to) {
     if constexpr (kPer > 1) {  // the workgroup's rows, added wave by wave
+#pragma unroll
       for (int p = kPer - 1; p > 0; --p) {
         __syncthreads();
         if (sub == p)
@@ -250,9 +253,11 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_bwd_kernel(const
 #pragma unroll
       for (int v = 0; v < kNv; ++v) {
         const int c = (v * kTpr + t) * 8, n = a.cols - c;
-        if (n > 0) store8(part + which * a.cols + c, pack8(acc[v], float()), n);
+        if (n > 0) store_run<kWhole>(to + c, pack8(acc[v], float()), n);
       }
-  }
+  };
+  leave(aw, part);
+  leave(ab, part + a.cols);
 }
 
 // Sums the workgroups' partials: 32 columns a workgroup, 8 threads a column,
@@ -290,9 +295,12 @@ __global__ __launch_bounds__(kRedCols * kRedSlices) void norm_grad_kernel(const 
     static_cast<__bf16 *>(out)[oc] = __bf16(s);
 }
 
-int bwd_tpr(int64_t cols) { return cols <= 1024 ? 64 : cols <= 8192 ? 256 : 1024; }
+// Threads a row of the backward kernel. Wide rows: 512, so that 256 workgroups
+// (whose partial sums the second launch reads) fill the chip; 16384x7168 bf16
+// takes 136 us so, 165 with 256 threads and 512 workgroups.
+int bwd_tpr(int64_t cols) { return cols <= 1024 ? 64 : cols <= 2048 ? 256 : cols <= 16384 ? 512 : 1024; }
 
-template <typename T, bool kWf32>
+template <typename T, bool kWf32, bool kWhole>
 hipError_t bwd(const NormBwdArgs &a, hipStream_t s) {
   auto go = [&](auto kernel, int tpr) {
     if (a.blocks > 0) hipLaunchKernelGGL(kernel, dim3(unsigned(a.blocks)), dim3(tpr < 256 ? 256 : tpr), 0, s, a);
@@ -302,13 +310,13 @@ hipError_t bwd(const NormBwdArgs &a, hipStream_t s) {
                        a);
     return hipGetLastError();
   };
-  if (a.cols <= 512) return go(norm_bwd_kernel<T, kWf32, 64, 1>, 64);
-  if (a.cols <= 1024) return go(norm_bwd_kernel<T, kWf32, 64, 2>, 64);
-  if (a.cols <= 2048) return go(norm_bwd_kernel<T, kWf32, 256, 1>, 256);
-  if (a.cols <= 4096) return go(norm_bwd_kernel<T, kWf32, 256, 2>, 256);
-  if (a.cols <= 8192) return go(norm_bwd_kernel<T, kWf32, 256, 4>, 256);
-  if (a.cols <= 16384) return go(norm_bwd_kernel<T, kWf32, 1024, 2>, 1024);
-  return go(norm_bwd_kernel<T, kWf32, 1024, 4>, 1024);
+  if (a.cols <= 512) return go(norm_bwd_kernel<T, kWf32, kWhole, 64, 1>, 64);
+  if (a.cols <= 1024) return go(norm_bwd_kernel<T, kWf32, kWhole, 64, 2>, 64);
+  if (a.cols <= 2048) return go(norm_bwd_kernel<T, kWf32, kWhole, 256, 1>, 256);
+  if (a.cols <= 4096) return go(norm_bwd_kernel<T, kWf32, kWhole, 512, 1>, 512);
+  if (a.cols <= 8192) return go(norm_bwd_kernel<T, kWf32, kWhole, 512, 2>, 512);
+  if (a.cols <= 16384) return go(norm_bwd_kernel<T, kWf32, kWhole, 512, 4>, 512);
+  return go(norm_bwd_kernel<T, kWf32, kWhole, 1024, 4>, 1024);
 }
 
 }  // namespace
@@ -317,19 +325,27 @@ hipError_t bwd(const NormBwdArgs &a, hipStream_t s) {
 // several rows, since each leaves 8 bytes a column of partial sums.
 int norm_bwd_blocks(int64_t rows, int64_t cols) {
   const int per = bwd_tpr(cols) < 256 ? 256 / bwd_tpr(cols) : 1;
-  const int64_t want = (rows + 4 * per - 1) / (4 * per);
-  return int(want < 512 ? want : 512);
+  const int64_t want = (rows + 2 * per - 1) / (2 * per), most = bwd_tpr(cols) < 512 ? 512 : 256;
+  return int(want < most ? want : most);
 }
+
+namespace {
+template <typename T, bool kWf32>
+hipError_t fwd(const NormFwdArgs &a, hipStream_t s) {
+  const bool ck = a.ck.codes != nullptr;
+  if (a.cols % 8 == 0) return ck ? fwd<T, kWf32, true, true>(a, s) : fwd<T, kWf32, false, true>(a, s);
+  return ck ? fwd<T, kWf32, true, false>(a, s) : fwd<T, kWf32, false, false>(a, s);
+}
+template <typename T, bool kWf32>
+hipError_t bwd(const NormBwdArgs &a, hipStream_t s) {
+  return a.cols % 8 == 0 ? bwd<T, kWf32, true>(a, s) : bwd<T, kWf32, false>(a, s);
+}
+}  // namespace
 
 hipError_t launch_norm_fwd(const NormFwdArgs &a, bool bf16, hipStream_t s) {
   if (a.rows <= 0) return hipSuccess;
-  const bool ck = a.ck.codes != nullptr;
-  if (bf16) {
-    if (a.w_f32) return ck ? fwd<__bf16, true, true>(a, s) : fwd<__bf16, true, false>(a, s);
-    return ck ? fwd<__bf16, false, true>(a, s) : fwd<__bf16, false, false>(a, s);
-  }
-  if (a.w_f32) return ck ? fwd<float, true, true>(a, s) : fwd<float, true, false>(a, s);
-  return ck ? fwd<float, false, true>(a, s) : fwd<float, false, false>(a, s);
+  if (bf16) return a.w_f32 ? fwd<__bf16, true>(a, s) : fwd<__bf16, false>(a, s);
+  return a.w_f32 ? fwd<float, true>(a, s) : fwd<float, false>(a, s);
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs &a, bool bf16, hipStream_t s) {

@@ -11,8 +11,10 @@
 //   the weights' gradient g, d + g at the choice (plain weights) or
 //   w (g - sum w g) at the choice (shares).
 //
-// One wave holds a token's logits, expert j * 64 + lane in register j. The
-// slot lists are stable (expert order, then slot order) without atomics on
+// Forward, 16 lanes hold a token's logits, four tokens a wave: each of the k
+// rounds finds the maximum and its lowest index by lane permutations, and the
+// instructions of a round serve four tokens. Backward, a wave holds one token.
+// The slot lists are stable (expert order, then slot order) without atomics on
 // the result: workgroups count their tokens' choices, the counts are summed
 // over workgroups in order, and inside a workgroup a slot's rank is the
 // number of lower bits in its expert's mask of tokens.
@@ -24,8 +26,6 @@
 namespace muon {
 namespace {
 
-constexpr int kThreads = 1024;  // forward: 16 waves
-constexpr int kWaves = kThreads / 64;
 constexpr int kSub = 64;        // tokens ranked at a time (two mask words an expert)
 constexpr float kNegInf = -__builtin_inff();
 
@@ -70,84 +70,169 @@ __device__ inline float softmax(const float (&x)[kJ], float (&p)[kJ], float &bas
   return m;
 }
 
+// A token's logits over a row of 16 lanes, expert 16 j + lane in register j, and
+// the row's reductions (no traffic through LDS).
+__device__ inline float row_max(float v) {
+  v = fmaxf(v, dpp<kQuadSwap1>(v));
+  v = fmaxf(v, dpp<kQuadSwap2>(v));
+  v = fmaxf(v, dpp<kHalfMirror>(v));
+  return fmaxf(v, dpp<kMirror>(v));
+}
+__device__ inline float row_sum(float v) {
+  v += dpp<kQuadSwap1>(v);
+  v += dpp<kQuadSwap2>(v);
+  v += dpp<kHalfMirror>(v);
+  return v + dpp<kMirror>(v);
+}
+__device__ inline uint32_t row_min(uint32_t v) {
+  v = min(v, dpp<kQuadSwap1>(v));
+  v = min(v, dpp<kQuadSwap2>(v));
+  v = min(v, dpp<kHalfMirror>(v));
+  return min(v, dpp<kMirror>(v));
+}
+
+// exp(d) for d <= 0: the product with log2 e in two parts, then the hardware's
+// power of two. Ends at 2^-126, 28 decades below the smallest sum it joins.
+__device__ inline float exp_sum(float d) {
+  d = d < -200.f ? -200.f : d;  // -inf too; NaN stays
+  const float hi = d * 1.44269502f;                               // log2 e rounded
+  const float lo = fmaf(d, 1.44269502f, -hi) + d * 1.92596303e-8f;  // what the product and the constant lost
+  const float e = __builtin_amdgcn_exp2f(hi);
+  return fmaf(e, lo * 0.693147182f, e);
+}
+
+// Threads of the forward kernels: four tokens a wave; the wide forms hold 32 or
+// more logits a lane and need more registers each.
+template <int kJ>
+constexpr int route_threads() { return kJ > 24 ? 512 : 1024; }
+
+template <int kJ>
 struct RouteLds {
-  int hist[kRouteMaxExperts];           // counts, or running counts
-  float psum[kRouteMaxExperts];
-  int offs[kRouteMaxExperts + 1];
-  uint32_t mask[kRouteMaxExperts][kSub / 32];
-  int scan[kThreads / 64 + 1];
+  static constexpr int kWaves = route_threads<kJ>() / 64;
+  int hist[kJ * 16];                    // counts, or running counts
+  float psum[kJ * 16];
+  int offs[kJ * 16 + 1];
+  union {
+    uint32_t mask[kJ * 16][kSub / 32];
+    float wave_psum[kWaves][kJ * 16];
+  };
+  int scan[kWaves + 1];
   int valid;
 };
 
 // The choice, weights, counts and sums of tokens [begin, end).
 template <typename T, int kJ>
-__device__ void route_tokens(const RouteFwdArgs &a, int begin, int end, RouteLds &lds) {
-  const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
-  for (int e = int(threadIdx.x); e < a.experts; e += kThreads) {
-    lds.hist[e] = 0;
-    lds.psum[e] = 0.f;
-  }
+__device__ void route_tokens(const RouteFwdArgs &a, int begin, int end, RouteLds<kJ> &lds) {
+  constexpr int kThreads = route_threads<kJ>(), kWaves = kThreads / 64;
+  const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6, l = lane & 15;
+  for (int e = int(threadIdx.x); e < a.experts; e += kThreads) lds.hist[e] = 0;
   if (threadIdx.x == 0) lds.valid = 0;
   __syncthreads();
   float ps[kJ];
 #pragma unroll
   for (int j = 0; j < kJ; ++j) ps[j] = 0.f;
   int valid = 0;
-  for (int t = begin + wave; t < end; t += kWaves) {
-    float x[kJ], p[kJ], base, inv;
-    load_logits<T, kJ>(static_cast<const T *>(a.logits) + int64_t(t) * a.ld, a.experts, lane, x);
-    float m = softmax<kJ>(x, p, base, inv);
+  for (int first = begin + wave * 4; first < end; first += kWaves * 4) {
+    const int t = first + (lane >> 4);
+    const T *logits = static_cast<const T *>(a.logits) + int64_t(t < end ? t : end - 1) * a.ld;
+    float x[kJ], p[kJ], m = kNegInf, s = 0.f;
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) ps[j] += p[j];
+    for (int j = 0; j < kJ; ++j) {
+      const int e = j * 16 + l;
+      x[j] = e < a.experts ? float(logits[e]) : kNegInf;
+    }
+    // rows past the end count and choose nothing
+    if (t >= end) {
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) x[j] = kNegInf;
+    }
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) m = fmaxf(m, x[j]);
+    m = row_max(m);
+    const float base = m == kNegInf ? 0.f : m;  // a row of -inf: every p is 0
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      p[j] = exp_sum(x[j] - base);
+      s += p[j];
+    }
+    s = row_sum(s);
+    const float inv = s == 0.f ? 1.f : 1.f / s;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) ps[j] = fmaf(p[j], inv, ps[j]);
     valid += m > kNegInf ? 1 : 0;
-    int mine = -1;
-    float w = 0.f, share = 0.f;
+    // choice i stays with lane i % 16 of the row
+    int mine[2] = {-1, -1};
+    float top[2] = {kNegInf, kNegInf};
     for (int i = 0; i < a.topk; ++i) {
-      if (!(m > kNegInf)) break;  // nothing left to choose
-      int idx = -1;
+      if (!__any(m > kNegInf)) break;  // nothing left to choose
+      uint32_t at = 0xffffu;
+#pragma unroll
+      for (int j = kJ - 1; j >= 0; --j) at = x[j] == m ? uint32_t(j * 16) : at;
+      const uint32_t e = row_min(at + uint32_t(l));
+      const bool some = m > kNegInf;
+      if (l == (i & 15) && some) {
+        if (i < 16) {
+          mine[0] = int(e);
+          top[0] = m;
+        } else {
+          mine[1] = int(e);
+          top[1] = m;
+        }
+      }
+      const int gone = int(e) - l;  // 16 j of the register that holds it, in its lane
+      m = kNegInf;
 #pragma unroll
       for (int j = 0; j < kJ; ++j) {
-        const uint64_t b = __ballot(x[j] == m);
-        if (idx < 0 && b) idx = j * 64 + __builtin_ctzll(b);
+        x[j] = gone == j * 16 ? kNegInf : x[j];
+        m = fmaxf(m, x[j]);
       }
-      const float pw = expf(m - base) * inv;
-      share += pw;
-      if (lane == i) {
-        mine = idx;
-        w = pw;
-      }
-      float next = kNegInf;
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        x[j] = j * 64 + lane == idx ? kNegInf : x[j];
-        next = fmaxf(next, x[j]);
-      }
-      if (i + 1 < a.topk) m = wave_max(next);
+      m = row_max(m);
     }
-    if (a.renorm) w /= share == 0.f ? 1.f : share;
-    if (lane < a.topk) {
-      a.indices[int64_t(t) * a.topk + lane] = mine;
-      a.weights[int64_t(t) * a.topk + lane] = w;
-      if (mine >= 0) atomicAdd(&lds.hist[mine], 1);
+    float w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) w[h] = mine[h] >= 0 ? expf(top[h] - base) * inv : 0.f;
+    if (a.renorm) {
+      const float share = row_sum(w[0] + w[1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[h] /= share == 0.f ? 1.f : share;
+    }
+    if (t < end) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = 16 * h + l;
+        if (i >= a.topk) break;
+        a.indices[int64_t(t) * a.topk + i] = mine[h];
+        a.weights[int64_t(t) * a.topk + i] = w[h];
+        if (mine[h] >= 0) atomicAdd(&lds.hist[mine[h]], 1);
+      }
     }
   }
-  if (lane == 0 && valid) atomicAdd(&lds.valid, valid);
-  for (int v = 0; v < kWaves; ++v) {  // in wave order: the same sum in every run
-    if (wave == v) {
+  if (l == 0 && valid) atomicAdd(&lds.valid, valid);
+  // the waves' sums, added in wave order: the same result in every run
 #pragma unroll
-      for (int j = 0; j < kJ; ++j)
-        if (j * 64 + lane < a.experts) lds.psum[j * 64 + lane] += ps[j];
-    }
-    __syncthreads();
+  for (int j = 0; j < kJ; ++j) {
+    ps[j] += __shfl_xor(ps[j], 16);
+    ps[j] += __shfl_xor(ps[j], 32);
+    if (lane < 16) lds.wave_psum[wave][j * 16 + l] = ps[j];
   }
+  __syncthreads();
+  for (int e = int(threadIdx.x); e < a.experts; e += kThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) s += lds.wave_psum[w][e];
+    lds.psum[e] = s;
+  }
+  __syncthreads();
 }
 
 // Exclusive scan of counts (a.experts of them, in LDS or global memory) into
 // lds.offs.
-__device__ void scan_counts(const int *counts, int experts, RouteLds &lds) {
+template <int kJ>
+__device__ void scan_counts(const int *counts, int experts, RouteLds<kJ> &lds) {
+  // two neighbouring experts a thread: the wide forms have half the threads
   const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
-  const int e = int(threadIdx.x);
-  const int c = e < experts ? counts[e] : 0;
+  const int e = int(threadIdx.x) * 2;
+  const int c0 = e < experts ? counts[e] : 0, c = c0 + (e + 1 < experts ? counts[e + 1] : 0);
   int v = c;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -158,14 +243,18 @@ __device__ void scan_counts(const int *counts, int experts, RouteLds &lds) {
   __syncthreads();
   int before = 0;
   for (int w = 0; w < wave; ++w) before += lds.scan[w];
-  if (e < experts) lds.offs[e] = before + v - c;
-  if (e == experts - 1) lds.offs[experts] = before + v;
+  const int at = before + v - c;
+  if (e < experts) lds.offs[e] = at;
+  if (e + 1 < experts) lds.offs[e + 1] = at + c0;
+  if (e == experts - 1 || e + 1 == experts - 1) lds.offs[experts] = before + v;
   __syncthreads();
 }
 
 // Writes the slots of tokens [begin, end) to their places: lds.offs[e] plus
 // lds.hist[e], the slots of expert e that earlier tokens have.
-__device__ void place_slots(const RouteFwdArgs &a, int begin, int end, RouteLds &lds) {
+template <int kJ>
+__device__ void place_slots(const RouteFwdArgs &a, int begin, int end, RouteLds<kJ> &lds) {
+  constexpr int kThreads = route_threads<kJ>();
   for (int sub = begin; sub < end; sub += kSub) {
     for (int i = int(threadIdx.x); i < a.experts * (kSub / 32); i += kThreads) (&lds.mask[0][0])[i] = 0;
     __syncthreads();
@@ -193,7 +282,9 @@ __device__ inline int counted(const RouteFwdArgs &a) { return a.tokens * a.topk;
 
 // counts, offsets and the loss, by one workgroup: lds.offs is set, counts and
 // psum hold the totals.
-__device__ void finish(const RouteFwdArgs &a, const int *counts, const float *psum, int valid, RouteLds &lds) {
+template <int kJ>
+__device__ void finish(const RouteFwdArgs &a, const int *counts, const float *psum, int valid, RouteLds<kJ> &lds) {
+  constexpr int kThreads = route_threads<kJ>(), kWaves = kThreads / 64;
   const float n = float(valid > 0 ? valid : 1);
   float s = 0.f;
   for (int e = int(threadIdx.x); e < a.experts; e += kThreads) {
@@ -202,11 +293,11 @@ __device__ void finish(const RouteFwdArgs &a, const int *counts, const float *ps
   }
   s = wave_sum(s);
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds.psum[threadIdx.x >> 6] = s;
+  if ((threadIdx.x & 63) == 0) lds.wave_psum[0][threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x) return;
   s = 0.f;
-  for (int w = 0; w < kWaves; ++w) s += lds.psum[w];
+  for (int w = 0; w < kWaves; ++w) s += lds.wave_psum[0][w];
   a.offsets[a.experts] = lds.offs[a.experts];
   a.counts[a.experts] = valid;
   a.loss[0] = a.alpha * float(a.experts) / (float(a.topk) * n) * s;
@@ -214,8 +305,9 @@ __device__ void finish(const RouteFwdArgs &a, const int *counts, const float *ps
 
 // A few tokens: everything in one launch of one workgroup.
 template <typename T, int kJ>
-__global__ __launch_bounds__(kThreads) void route_one_kernel(const RouteFwdArgs a) {
-  __shared__ RouteLds lds;
+__global__ __launch_bounds__(route_threads<kJ>()) void route_one_kernel(const RouteFwdArgs a) {
+  constexpr int kThreads = route_threads<kJ>();
+  __shared__ RouteLds<kJ> lds;
   route_tokens<T, kJ>(a, 0, a.tokens, lds);
   scan_counts(lds.hist, a.experts, lds);
   const int total = lds.offs[a.experts];
@@ -232,8 +324,9 @@ __global__ __launch_bounds__(kThreads) void route_one_kernel(const RouteFwdArgs 
 
 // Many tokens, first launch: each workgroup's tokens, counts and sums.
 template <typename T, int kJ>
-__global__ __launch_bounds__(kThreads) void route_tokens_kernel(const RouteFwdArgs a) {
-  __shared__ RouteLds lds;
+__global__ __launch_bounds__(route_threads<kJ>()) void route_tokens_kernel(const RouteFwdArgs a) {
+  constexpr int kThreads = route_threads<kJ>();
+  __shared__ RouteLds<kJ> lds;
   const int begin = int(blockIdx.x) * a.per_block;
   const int end = begin + a.per_block < a.tokens ? begin + a.per_block : a.tokens;
   route_tokens<T, kJ>(a, begin, end, lds);
@@ -245,9 +338,9 @@ __global__ __launch_bounds__(kThreads) void route_tokens_kernel(const RouteFwdAr
 }
 
 // Second launch: over the workgroups, hist becomes its exclusive prefix sum
-// and row 0 of psum the total, 16 experts a workgroup and 16 threads an
+// and row 0 of psum the total, 16 experts a workgroup and 64 threads an
 // expert, each over a run of consecutive workgroups.
-constexpr int kScanExperts = 16, kScanSlices = 16;
+constexpr int kScanExperts = 16, kScanSlices = 64;
 __global__ __launch_bounds__(kScanExperts * kScanSlices) void route_scan_kernel(const RouteFwdArgs a) {
   __shared__ int cnt[kScanSlices][kScanExperts];
   __shared__ float sum[kScanSlices][kScanExperts];
@@ -270,6 +363,7 @@ __global__ __launch_bounds__(kScanExperts * kScanSlices) void route_scan_kernel(
   if (e < a.experts) {
     int before = 0, total = 0;
     float all = 0.f;
+#pragma unroll 8
     for (int j = 0; j < kScanSlices; ++j) {
       before += j < sl ? cnt[j][le] : 0;
       total += cnt[j][le];
@@ -286,23 +380,20 @@ __global__ __launch_bounds__(kScanExperts * kScanSlices) void route_scan_kernel(
       a.psum[e] = all;  // row 0: its own slice has read it
     }
   }
-  if (blockIdx.x == 0) {
-    __syncthreads();
+  if (blockIdx.x == 0 && threadIdx.x < 64) {
     int v = 0;
-    for (int b = int(threadIdx.x); b < a.blocks; b += kScanExperts * kScanSlices) v += a.valid[b];
-    (&cnt[0][0])[threadIdx.x] = v;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      v = 0;
-      for (int i = 0; i < kScanExperts * kScanSlices; ++i) v += (&cnt[0][0])[i];
-      a.counts[a.experts] = v;
-    }
+    for (int b = int(threadIdx.x); b < a.blocks; b += 64) v += a.valid[b];
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+    if (threadIdx.x == 0) a.counts[a.experts] = v;
   }
 }
 
 // Third launch: the slot lists; the first workgroup also offsets and loss.
-__global__ __launch_bounds__(kThreads) void route_place_kernel(const RouteFwdArgs a) {
-  __shared__ RouteLds lds;
+template <int kJ>
+__global__ __launch_bounds__(route_threads<kJ>()) void route_place_kernel(const RouteFwdArgs a) {
+  constexpr int kThreads = route_threads<kJ>();
+  __shared__ RouteLds<kJ> lds;
   scan_counts(a.counts, a.experts, lds);
   if (blockIdx.x == 0) finish(a, a.counts, a.psum, a.counts[a.experts], lds);
   for (int e = int(threadIdx.x); e < a.experts; e += kThreads)
@@ -390,6 +481,18 @@ __global__ __launch_bounds__(kBwdThreads) void route_bwd_kernel(const RouteBwdAr
   }
 }
 
+// Registers a lane: 16 lanes hold a token in the forward kernels, 64 in the
+// backward one.
+template <typename F>
+auto by_row(int experts, F &&f) {
+  if (experts <= 16) return f(std::integral_constant<int, 1>());
+  if (experts <= 64) return f(std::integral_constant<int, 4>());
+  if (experts <= 128) return f(std::integral_constant<int, 8>());
+  if (experts <= 256) return f(std::integral_constant<int, 16>());
+  if (experts <= 384) return f(std::integral_constant<int, 24>());
+  if (experts <= 512) return f(std::integral_constant<int, 32>());
+  return f(std::integral_constant<int, 64>());
+}
 template <typename F>
 auto by_experts(int experts, F &&f) {
   if (experts <= 64) return f(std::integral_constant<int, 1>());
@@ -402,20 +505,20 @@ auto by_experts(int experts, F &&f) {
 
 template <typename T>
 hipError_t route_fwd(const RouteFwdArgs &a, hipStream_t s) {
-  return by_experts(a.experts, [&](auto kj) {
+  return by_row(a.experts, [&](auto kj) {
     constexpr int kJ = decltype(kj)::value;
     if (a.blocks == 0) {
-      hipLaunchKernelGGL((route_one_kernel<T, kJ>), dim3(1), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((route_one_kernel<T, kJ>), dim3(1), dim3(route_threads<kJ>()), 0, s, a);
       return hipGetLastError();
     }
-    hipLaunchKernelGGL((route_tokens_kernel<T, kJ>), dim3(unsigned(a.blocks)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((route_tokens_kernel<T, kJ>), dim3(unsigned(a.blocks)), dim3(route_threads<kJ>()), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(route_scan_kernel, dim3((a.experts + kScanExperts - 1) / kScanExperts),
                        dim3(kScanExperts * kScanSlices), 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(route_place_kernel, dim3(unsigned(a.blocks)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((route_place_kernel<kJ>), dim3(unsigned(a.blocks)), dim3(route_threads<kJ>()), 0, s, a);
     return hipGetLastError();
   });
 }

@@ -189,3 +189,14 @@ def test_binding_refuses_what_no_kernel_may_touch():
         mu.Checkpoint(t, scales)
     with pytest.raises(ValueError, match="scales"):
         mu.Checkpoint(codes, scales[:3])
+
+
+def test_exchanging_the_workspace():
+    p, n = ctypes.c_void_p(), ctypes.c_size_t()
+    swap = mu.lib().muon_exchange_workspace
+    assert swap(A, 512, p, n) == mu.MUON_OK and not p.value and n.value == 0
+    assert swap(A * 2 + 1, 256, p, n) == ALIGN and swap(None, 256, p, n) == INV
+    assert not p.value and n.value == 0
+    assert swap(A * 2, 256, p, n) == mu.MUON_OK and p.value == A and n.value == 512
+    assert swap(p, n, None, None) == mu.MUON_OK
+    assert mu.lib().muon_get_workspace(p, n) == mu.MUON_OK and p.value == A and n.value == 512
