@@ -113,6 +113,20 @@ __device__ inline uint32_t dpp(uint32_t v) {
 }
 constexpr int kQuadSwap1 = 0xB1, kQuadSwap2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
 
+// A value of this lane's row of 16 and the neighbouring row's (the even row's
+// first), or of both halves of the wave (the lower's first), without LDS.
+struct Pair {
+  float a, b;
+};
+__device__ inline Pair rows_16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(f32_bits(v), f32_bits(v), false, false);
+  return {bits_f32(r[0]), bits_f32(r[1])};
+}
+__device__ inline Pair halves_32(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(f32_bits(v), f32_bits(v), false, false);
+  return {bits_f32(r[0]), bits_f32(r[1])};
+}
+
 // Sum over the 64 lanes, the same value in each (a fixed tree: the result
 // depends on nothing but the inputs).
 __device__ inline float wave_sum(float v) {
@@ -120,9 +134,9 @@ __device__ inline float wave_sum(float v) {
   v += dpp<kQuadSwap2>(v);
   v += dpp<kHalfMirror>(v);
   v += dpp<kMirror>(v);
-  v += __shfl_xor(v, 16);
-  v += __shfl_xor(v, 32);
-  return v;
+  const Pair p = rows_16(v);
+  const Pair q = halves_32(p.a + p.b);
+  return q.a + q.b;
 }
 // Maximum of unsigned values over rows of 16 lanes, in each of them.
 __device__ inline uint32_t row16_max(uint32_t v) {

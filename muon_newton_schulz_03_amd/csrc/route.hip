@@ -34,18 +34,24 @@ __device__ inline float wave_max(float v) {
   v = fmaxf(v, dpp<kQuadSwap2>(v));
   v = fmaxf(v, dpp<kHalfMirror>(v));
   v = fmaxf(v, dpp<kMirror>(v));
-  v = fmaxf(v, __shfl_xor(v, 16));
-  v = fmaxf(v, __shfl_xor(v, 32));
-  return v;
+  const Pair p = rows_16(v);
+  const Pair q = halves_32(fmaxf(p.a, p.b));
+  return fmaxf(q.a, q.b);
 }
 
+// Expert 64 j + lane in register j, -inf past the last. Every load is issued
+// (past the end, of the last expert): one that a lane may skip would be waited
+// for before the next.
 template <typename T, int kJ>
 __device__ inline void load_logits(const T *p, int experts, int lane, float (&x)[kJ]) {
+  T raw[kJ];
 #pragma unroll
   for (int j = 0; j < kJ; ++j) {
     const int e = j * 64 + lane;
-    x[j] = e < experts ? float(p[e]) : kNegInf;
+    raw[j] = p[e < experts ? e : experts - 1];
   }
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) x[j] = j * 64 + lane < experts ? float(raw[j]) : kNegInf;
 }
 
 // p[j] = softmax; returns the row's maximum (NaN ignored), and the base and
@@ -70,8 +76,27 @@ __device__ inline float softmax(const float (&x)[kJ], float (&p)[kJ], float &bas
   return m;
 }
 
-// A token's logits over a row of 16 lanes, expert 16 j + lane in register j, and
-// the row's reductions (no traffic through LDS).
+// A token's logits over a row of 16 lanes, in runs of eight experts: register j
+// of lane l holds expert 8 l + expert_of(j).
+__device__ constexpr int expert_of(int j) { return j / 8 * 128 + j % 8; }
+template <typename T, int kJ>
+__device__ inline void load_runs(const T *p, int experts, int l, float (&x)[kJ]) {
+  Raw8<T> r[kJ / 8];
+  if (experts % 8 == 0) {  // a run is there or not: past the end, the first one is read
+#pragma unroll
+    for (int c = 0; c < kJ / 8; ++c) {
+      const int e = c * 128 + l * 8;
+      r[c] = load8(p + (e < experts ? e : 0), 8);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kJ / 8; ++c) r[c] = load8(p + c * 128 + l * 8, experts - c * 128 - l * 8);
+  }
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) x[j] = expert_of(j) + l * 8 < experts ? r[j / 8].get(j % 8) : kNegInf;
+}
+
+// Reductions of such a row (no traffic through LDS).
 __device__ inline float row_max(float v) {
   v = fmaxf(v, dpp<kQuadSwap1>(v));
   v = fmaxf(v, dpp<kQuadSwap2>(v));
@@ -84,6 +109,7 @@ __device__ inline float row_sum(float v) {
   v += dpp<kHalfMirror>(v);
   return v + dpp<kMirror>(v);
 }
+__device__ inline uint32_t row_max(uint32_t v) { return row16_max(v); }
 __device__ inline uint32_t row_min(uint32_t v) {
   v = min(v, dpp<kQuadSwap1>(v));
   v = min(v, dpp<kQuadSwap2>(v));
@@ -136,11 +162,7 @@ __device__ void route_tokens(const RouteFwdArgs &a, int begin, int end, RouteLds
     const int t = first + (lane >> 4);
     const T *logits = static_cast<const T *>(a.logits) + int64_t(t < end ? t : end - 1) * a.ld;
     float x[kJ], p[kJ], m = kNegInf, s = 0.f;
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-      const int e = j * 16 + l;
-      x[j] = e < a.experts ? float(logits[e]) : kNegInf;
-    }
+    load_runs<T, kJ>(logits, a.experts, l, x);
     // rows past the end count and choose nothing
     if (t >= end) {
 #pragma unroll
@@ -163,30 +185,56 @@ __device__ void route_tokens(const RouteFwdArgs &a, int begin, int end, RouteLds
     // choice i stays with lane i % 16 of the row
     int mine[2] = {-1, -1};
     float top[2] = {kNegInf, kNegInf};
-    for (int i = 0; i < a.topk; ++i) {
-      if (!__any(m > kNegInf)) break;  // nothing left to choose
-      uint32_t at = 0xffffu;
-#pragma unroll
-      for (int j = kJ - 1; j >= 0; --j) at = x[j] == m ? uint32_t(j * 16) : at;
-      const uint32_t e = row_min(at + uint32_t(l));
-      const bool some = m > kNegInf;
-      if (l == (i & 15) && some) {
-        if (i < 16) {
-          mine[0] = int(e);
-          top[0] = m;
-        } else {
-          mine[1] = int(e);
-          top[1] = m;
-        }
+    auto keep = [&](int i, int e, float v) {
+      if (l != (i & 15)) return;
+      if (i < 16) {
+        mine[0] = e;
+        top[0] = v;
+      } else {
+        mine[1] = e;
+        top[1] = v;
       }
-      const int gone = int(e) - l;  // 16 j of the register that holds it, in its lane
-      m = kNegInf;
+    };
+    if constexpr (sizeof(T) == 2) {
+      // bf16: the order of choice as one number, the value's bits (ascending with
+      // it) above 1023 - e, 0 for what is never chosen. All differ, so the next
+      // choice is the largest difference to this one that wraps below zero.
+      uint32_t key[kJ], best = 0;
 #pragma unroll
       for (int j = 0; j < kJ; ++j) {
-        x[j] = gone == j * 16 ? kNegInf : x[j];
-        m = fmaxf(m, x[j]);
+        const uint32_t u = f32_bits(x[j] + 0.f) >> 16;  // -0 is 0
+        const uint32_t up = u & 0x8000u ? u ^ 0xffffu : u | 0x8000u;
+        key[j] = x[j] > kNegInf ? up << 10 | uint32_t(1023 - expert_of(j) - l * 8) : 0u;
+        best = max(best, key[j]);
       }
-      m = row_max(m);
+      best = row_max(best);
+      for (int i = 0; i < a.topk; ++i) {
+        if (!__any(best != 0)) break;  // nothing left to choose
+        const uint32_t up = best >> 10;
+        if (best) keep(i, 1023 - int(best & 1023u), bits_f32((up & 0x8000u ? up & 0x7fffu : up ^ 0xffffu) << 16));
+        uint32_t below = 0;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) below = max(below, key[j] - best);
+        below = row_max(below);
+        best = below & 0x80000000u ? best + below : 0u;
+      }
+    } else {
+      for (int i = 0; i < a.topk; ++i) {
+        if (!__any(m > kNegInf)) break;  // nothing left to choose
+        uint32_t at = 0xffffu;
+#pragma unroll
+        for (int j = kJ - 1; j >= 0; --j) at = x[j] == m ? uint32_t(expert_of(j)) : at;
+        const uint32_t e = row_min(at + uint32_t(l * 8));
+        if (m > kNegInf) keep(i, int(e), m);
+        const int gone = int(e) - l * 8;  // expert_of the register that holds it, in its lane
+        m = kNegInf;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          x[j] = gone == expert_of(j) ? kNegInf : x[j];
+          m = fmaxf(m, x[j]);
+        }
+        m = row_max(m);
+      }
     }
     float w[2];
 #pragma unroll
@@ -211,9 +259,10 @@ __device__ void route_tokens(const RouteFwdArgs &a, int begin, int end, RouteLds
   // the waves' sums, added in wave order: the same result in every run
 #pragma unroll
   for (int j = 0; j < kJ; ++j) {
-    ps[j] += __shfl_xor(ps[j], 16);
-    ps[j] += __shfl_xor(ps[j], 32);
-    if (lane < 16) lds.wave_psum[wave][j * 16 + l] = ps[j];
+    const Pair q = rows_16(ps[j]);
+    const Pair h = halves_32(q.a + q.b);
+    ps[j] = h.a + h.b;
+    if (lane < 16) lds.wave_psum[wave][expert_of(j) + l * 8] = ps[j];
   }
   __syncthreads();
   for (int e = int(threadIdx.x); e < a.experts; e += kThreads) {
@@ -341,21 +390,27 @@ __global__ __launch_bounds__(route_threads<kJ>()) void route_tokens_kernel(const
 // and row 0 of psum the total, 16 experts a workgroup and 64 threads an
 // expert, each over a run of consecutive workgroups.
 constexpr int kScanExperts = 16, kScanSlices = 64;
+constexpr int kMaxBlocks = 1024;
+template <int kPer>  // workgroups a slice
 __global__ __launch_bounds__(kScanExperts * kScanSlices) void route_scan_kernel(const RouteFwdArgs a) {
   __shared__ int cnt[kScanSlices][kScanExperts];
   __shared__ float sum[kScanSlices][kScanExperts];
   const int le = int(threadIdx.x) % kScanExperts, sl = int(threadIdx.x) / kScanExperts;
   const int e = int(blockIdx.x) * kScanExperts + le;
-  const int per = (a.blocks + kScanSlices - 1) / kScanSlices;
-  const int b0 = sl * per, b1 = b0 + per < a.blocks ? b0 + per : a.blocks;
-  int c = 0;
-  float s = 0.f;
-  if (e < a.experts) {
-#pragma unroll 8
-    for (int b = b0; b < b1; ++b) {
-      c += a.hist[int64_t(b) * a.experts + e];
-      s += a.psum[int64_t(b) * a.experts + e];
-    }
+  const int b0 = sl * kPer, col = e < a.experts ? e : a.experts - 1;
+  int h[kPer], c = 0;
+  float p[kPer], s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {  // past the last workgroup: the last one's, not counted
+    const int64_t at = int64_t(b0 + i < a.blocks ? b0 + i : a.blocks - 1) * a.experts + col;
+    h[i] = a.hist[at];
+    p[i] = a.psum[at];
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (b0 + i >= a.blocks) break;
+    c += h[i];
+    s += p[i];
   }
   cnt[sl][le] = c;
   sum[sl][le] = s;
@@ -363,21 +418,21 @@ __global__ __launch_bounds__(kScanExperts * kScanSlices) void route_scan_kernel(
   if (e < a.experts) {
     int before = 0, total = 0;
     float all = 0.f;
-#pragma unroll 8
+#pragma unroll 16
     for (int j = 0; j < kScanSlices; ++j) {
       before += j < sl ? cnt[j][le] : 0;
       total += cnt[j][le];
       all += sum[j][le];
     }
-#pragma unroll 8
-    for (int b = b0; b < b1; ++b) {
-      const int h = a.hist[int64_t(b) * a.experts + e];
-      a.hist[int64_t(b) * a.experts + e] = before;
-      before += h;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (b0 + i >= a.blocks) break;
+      a.hist[int64_t(b0 + i) * a.experts + e] = before;
+      before += h[i];
     }
     if (sl == 0) {
       a.counts[e] = total;
-      a.psum[e] = all;  // row 0: its own slice has read it
+      a.psum[e] = all;  // row 0: this thread has read it
     }
   }
   if (blockIdx.x == 0 && threadIdx.x < 64) {
@@ -427,7 +482,12 @@ __global__ __launch_bounds__(kBwdThreads) void route_bwd_kernel(const RouteBwdAr
 #pragma unroll
   for (int j = 0; j < kJ; ++j) {
     const int e = j * 64 + lane;
-    dl[j] = a.dloss && e < a.experts ? coef * float(a.counts[e]) : 0.f;
+    dl[j] = float(a.counts[e < a.experts ? e : a.experts - 1]);  // every load issued, as for the logits
+  }
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
+    const int e = j * 64 + lane;
+    dl[j] = a.dloss && e < a.experts ? coef * dl[j] : 0.f;
   }
   const int waves = int(gridDim.x) * (kBwdThreads / 64);
   for (int t = int(blockIdx.x) * (kBwdThreads / 64) + wave; t < a.tokens; t += waves) {
@@ -485,8 +545,6 @@ __global__ __launch_bounds__(kBwdThreads) void route_bwd_kernel(const RouteBwdAr
 // backward one.
 template <typename F>
 auto by_row(int experts, F &&f) {
-  if (experts <= 16) return f(std::integral_constant<int, 1>());
-  if (experts <= 64) return f(std::integral_constant<int, 4>());
   if (experts <= 128) return f(std::integral_constant<int, 8>());
   if (experts <= 256) return f(std::integral_constant<int, 16>());
   if (experts <= 384) return f(std::integral_constant<int, 24>());
@@ -514,8 +572,8 @@ hipError_t route_fwd(const RouteFwdArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((route_tokens_kernel<T, kJ>), dim3(unsigned(a.blocks)), dim3(route_threads<kJ>()), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(route_scan_kernel, dim3((a.experts + kScanExperts - 1) / kScanExperts),
-                       dim3(kScanExperts * kScanSlices), 0, s, a);
+    hipLaunchKernelGGL(a.blocks <= 4 * kScanSlices ? route_scan_kernel<4> : route_scan_kernel<kMaxBlocks / kScanSlices>,
+                       dim3((a.experts + kScanExperts - 1) / kScanExperts), dim3(kScanExperts * kScanSlices), 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((route_place_kernel<kJ>), dim3(unsigned(a.blocks)), dim3(route_threads<kJ>()), 0, s, a);
@@ -542,7 +600,7 @@ void route_plan(RouteFwdArgs &a) {
   a.per_block = a.tokens;
   if (a.tokens <= 128) return;
   const int64_t subs = (int64_t(a.tokens) + kSub - 1) / kSub;
-  const int64_t each = (subs + 1023) / 1024;
+  const int64_t each = (subs + kMaxBlocks - 1) / kMaxBlocks;
   a.per_block = int32_t(each * kSub);
   a.blocks = int32_t((int64_t(a.tokens) + a.per_block - 1) / a.per_block);
 }
