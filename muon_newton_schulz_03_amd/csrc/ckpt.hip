@@ -84,10 +84,12 @@ __device__ inline u32x2 load_codes8(const uint8_t *p, int n) {
   u32x2 c = {0u, 0u};
   if (n >= 8) {
     c = *reinterpret_cast<const u32x2_any *>(p);
-  } else {
+  } else if (n > 0) {
+    uint32_t e[7];
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) c[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
+    for (int i = 0; i < 7; ++i) e[i] = p[i < n ? i : n - 1];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) c[i >> 2] |= (i < n ? e[i] : 0u) << (8 * (i & 3));
   }
   return c;
 }

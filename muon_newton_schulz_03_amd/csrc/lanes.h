@@ -36,16 +36,19 @@ struct Raw8<float> {
   __device__ float get(int i) const { return bits_f32(v[i >> 2][i & 3]); }
 };
 
-// The first min(n, 8) of them (zeros behind; n <= 0: none is read).
+// The first min(n, 8) of them (zeros behind; n <= 0: none is read). A run that is
+// cut repeats its last element, so that its loads are in flight together.
 __device__ inline Raw8<__bf16> load8(const __bf16 *p, int n) {
   Raw8<__bf16> r{};
   if (n >= 8) {
     r.v = *reinterpret_cast<const u32x4_any *>(p);
-  } else {
+  } else if (n > 0) {
     const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+    uint32_t e[7];
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) r.v[i >> 1] |= uint32_t(q[i]) << (16 * (i & 1));
+    for (int i = 0; i < 7; ++i) e[i] = q[i < n ? i : n - 1];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) r.v[i >> 1] |= (i < n ? e[i] : 0u) << (16 * (i & 1));
   }
   return r;
 }
@@ -54,11 +57,13 @@ __device__ inline Raw8<float> load8(const float *p, int n) {
   if (n >= 8) {
     r.v[0] = *reinterpret_cast<const u32x4_any *>(p);
     r.v[1] = *reinterpret_cast<const u32x4_any *>(p + 4);
-  } else {
+  } else if (n > 0) {
     const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
+    uint32_t e[7];
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) r.v[i >> 2][i & 3] = q[i];
+    for (int i = 0; i < 7; ++i) e[i] = q[i < n ? i : n - 1];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) r.v[i >> 2][i & 3] = i < n ? e[i] : 0u;
   }
   return r;
 }

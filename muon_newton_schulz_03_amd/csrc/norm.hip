@@ -130,8 +130,23 @@ template <typename T, bool kWf32, bool kCkpt, bool kWhole>
 hipError_t fwd(const NormFwdArgs &a, hipStream_t s) {
   auto go = [&](auto kernel, int tpr) {
     const int per = tpr < 256 ? 256 / tpr : 1;
-    hipLaunchKernelGGL(kernel, dim3(unsigned((a.rows + per - 1) / per)), dim3(tpr < 256 ? 256 : tpr), 0, s, a);
-    return hipGetLastError();
+    constexpr int64_t kMost = 1 << 21;  // workgroups a launch: fewer than 2^32 threads
+    for (int64_t r = 0; r < a.rows; r += kMost * per) {
+      NormFwdArgs part = a;
+      part.rows = a.rows - r < kMost * per ? a.rows - r : kMost * per;
+      part.x = static_cast<const T *>(a.x) + r * a.ld_x;
+      part.y = static_cast<T *>(a.y) + r * a.ld_y;
+      if (a.mean) part.mean = a.mean + r;
+      if (a.rstd) part.rstd = a.rstd + r;
+      if (kCkpt) {
+        part.ck.codes = a.ck.codes + r * a.ck.ld_codes;
+        part.ck.scales = a.ck.scales + r * a.ck.ld_scales;
+      }
+      hipLaunchKernelGGL(kernel, dim3(unsigned((part.rows + per - 1) / per)), dim3(tpr < 256 ? 256 : tpr), 0, s, part);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   };
   if (a.cols <= 512) return go(norm_fwd_kernel<T, kWf32, kCkpt, kWhole, 64, 1>, 64);
   if (a.cols <= 1024) return go(norm_fwd_kernel<T, kWf32, kCkpt, kWhole, 64, 2>, 64);

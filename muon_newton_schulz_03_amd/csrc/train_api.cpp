@@ -51,6 +51,8 @@ void launched(hipError_t e, const char *what) {
 }
 
 constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;
+// Pitches for which every offset, in bytes, stays far inside 64 bits.
+bool fits(int64_t count, int64_t pitch) { return pitch <= (int64_t(1) << 60) / (count > 1 ? count : 1); }
 
 // A buffer of the call: `rows` runs of `bytes`, `pitch` bytes apart.
 struct Span {
@@ -112,7 +114,7 @@ void matrix(const muon_mat *m, const char *name, int64_t max_cols) {
   if (m->dtype != MUON_F32 && m->dtype != MUON_BF16) refuse(MUON_ERR_DTYPE, "%s: unknown dtype", name);
   if (m->rows < 0 || m->rows > kMaxIndex || m->cols <= 0 || m->cols > max_cols)
     refuse(MUON_ERR_SHAPE, "%s: rows must lie in [0, 2^31), cols in [1, %lld]", name, (long long)max_cols);
-  if (m->ld < m->cols) refuse(MUON_ERR_SHAPE, "%s: ld < cols", name);
+  if (m->ld < m->cols || !fits(m->rows, m->ld)) refuse(MUON_ERR_SHAPE, "%s: ld < cols, or rows * ld > 2^60", name);
   if (m->rows > 0 && !m->data) refuse(MUON_ERR_INVALID_ARG, "%s: NULL data", name);
   if (reinterpret_cast<uintptr_t>(m->data) % esize(m->dtype))
     refuse(MUON_ERR_ALIGN, "%s: data not aligned to its element size", name);
@@ -148,6 +150,8 @@ CkptView checkpoint(const muon_ckpt *c, const char *name) {
     refuse(MUON_ERR_SHAPE, "%s: rows must lie in [0, 2^31), cols in [1, 2^30)", name);
   if (c->ld_codes < c->cols || c->ld_scales < groups_of(c->cols))
     refuse(MUON_ERR_SHAPE, "%s: ld_codes < cols or ld_scales < ceil(cols / 128)", name);
+  if (!fits(c->rows, c->ld_codes) || !fits(c->rows, c->ld_scales))
+    refuse(MUON_ERR_SHAPE, "%s: rows * pitch > 2^60", name);
   if (c->rows > 0 && (!c->codes || !c->scales)) refuse(MUON_ERR_INVALID_ARG, "%s: NULL codes or scales", name);
   return CkptView{static_cast<uint8_t *>(c->codes), static_cast<uint8_t *>(c->scales), c->ld_codes, c->ld_scales};
 }
@@ -370,6 +374,7 @@ muon_status muon_ckpt_weight_grad(const muon_mat *dy, const muon_ckpt *x, const 
     wgrad_shape(a, dy->dtype, dy->rows, dy->cols, x->cols, n_groups);
     if (n_groups > 1 && group_stride < (grads->rows - 1) * grads->ld + grads->cols)
       refuse(MUON_ERR_SHAPE, "group_stride: gradients overlap");
+    if (n_groups > 1 && !fits(n_groups, group_stride)) refuse(MUON_ERR_SHAPE, "group_stride: n_groups * group_stride > 2^60");
     if (n_groups > 1 && !offsets) refuse(MUON_ERR_INVALID_ARG, "offsets must not be NULL with more than one group");
     if (x->ld_codes > kMaxIndex || x->ld_scales > kMaxIndex) refuse(MUON_ERR_SHAPE, "x: pitches must lie below 2^31");
     if (rows_per_token < 1) refuse(MUON_ERR_INVALID_ARG, "rows_per_token must be >= 1");

@@ -85,6 +85,14 @@ __device__ inline u32x4 load16(GlobalPtr p) {
   return *reinterpret_cast<const __attribute__((address_space(1))) u32x4_any *>(p);
 }
 
+__device__ inline void store8_stream(__bf16 *p, const Raw8<__bf16> &r) {
+  __builtin_nontemporal_store(r.v, reinterpret_cast<u32x4_any *>(p));
+}
+__device__ inline void store8_stream(float *p, const Raw8<float> &r) {
+  __builtin_nontemporal_store(r.v[0], reinterpret_cast<u32x4_any *>(p));
+  __builtin_nontemporal_store(r.v[1], reinterpret_cast<u32x4_any *>(p + 4));
+}
+
 // Moves a run down by `bytes` (zeros behind it).
 template <int kDwords>
 __device__ inline void shift_down(uint32_t (&v)[kDwords], uint32_t bytes) {
@@ -406,7 +414,12 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
           store8(p, pack8(f, float()), a.k - k);
         } else {
           T *p = static_cast<T *>(a.out) + group * a.stride + n * a.ld_out + k;
-          store8(p, pack8(f, T()), a.k - k);
+          // past the caches: the gradients of a set of experts are more than they
+          // hold (128 of 768x2048: 217 us through them, 205 past)
+          if (a.k - k >= 8)
+            store8_stream(p, pack8(f, T()));
+          else
+            store8(p, pack8(f, T()), a.k - k);
         }
       }
     }
@@ -420,23 +433,24 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
 // result.
 template <typename T>
 __global__ __launch_bounds__(256) void wgrad_tiny_kernel(const WgradArgs a) {
-  const int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (u >= int64_t(a.groups) * a.n * a.k) return;
-  const int k = int(u % a.k), n = int(u / a.k % a.n), group = int(u / (int64_t(a.n) * a.k));
-  int64_t lo = 0, hi = a.slots;
-  if (a.offsets) {
-    lo = a.offsets[group] < 0 ? 0 : a.offsets[group];
-    hi = a.offsets[group + 1] > a.slots ? a.slots : a.offsets[group + 1];
+  const int64_t total = int64_t(a.groups) * a.n * a.k;
+  for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < total; u += int64_t(gridDim.x) * 256) {
+    const int k = int(u % a.k), n = int(u / a.k % a.n), group = int(u / (int64_t(a.n) * a.k));
+    int64_t lo = 0, hi = a.slots;
+    if (a.offsets) {
+      lo = a.offsets[group] < 0 ? 0 : a.offsets[group];
+      hi = a.offsets[group + 1] > a.slots ? a.slots : a.offsets[group + 1];
+    }
+    float s = 0.f;
+    for (int64_t i = lo; i < hi; ++i) {
+      const uint32_t token = uint32_t(a.rows ? a.rows[i] : int32_t(i)) / uint32_t(a.per_token);
+      if (token >= uint32_t(a.tokens)) continue;
+      const float x = bits_f32(decode2<0>(a.x.codes[token * a.x.ld_codes + k], 1.f) << 16) *
+                      scale_value(a.x.scales[token * a.x.ld_scales + (k >> 7)]);
+      s = fmaf(float(static_cast<const T *>(a.dy)[i * a.ld_dy + n]), x, s);
+    }
+    static_cast<T *>(a.out)[group * a.stride + n * a.ld_out + k] = T(s);
   }
-  float s = 0.f;
-  for (int64_t i = lo; i < hi; ++i) {
-    const uint32_t token = uint32_t(a.rows ? a.rows[i] : int32_t(i)) / uint32_t(a.per_token);
-    if (token >= uint32_t(a.tokens)) continue;
-    const float x = bits_f32(decode2<0>(a.x.codes[token * a.x.ld_codes + k], 1.f) << 16) *
-                    scale_value(a.x.scales[token * a.x.ld_scales + (k >> 7)]);
-    s = fmaf(float(static_cast<const T *>(a.dy)[i * a.ld_dy + n]), x, s);
-  }
-  static_cast<T *>(a.out)[group * a.stride + n * a.ld_out + k] = T(s);
 }
 
 // Adds the partials in split order; a thread takes eight columns of a row.
@@ -475,7 +489,7 @@ hipError_t wgrad(const WgradArgs &a, hipStream_t s) {
   if (a.slots > 0 && a.tokens > 0 &&
       ((a.slots - 1) * a.ld_dy + a.n < 8 || (a.tokens - 1) * a.x.ld_codes + a.k < 16)) {
     const int64_t total = int64_t(a.groups) * a.n * a.k;
-    hipLaunchKernelGGL(wgrad_tiny_kernel<T>, dim3(unsigned((total + 255) / 256)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(wgrad_tiny_kernel<T>, dim3(unsigned(std::min<int64_t>((total + 255) / 256, 1 << 20))), dim3(256), 0, s, a);
     return hipGetLastError();
   }
   const dim3 grid(work);

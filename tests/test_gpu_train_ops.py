@@ -489,3 +489,27 @@ def test_graph_replays(gpu_lib):
             if name != "ck":
                 assert torch.equal(captured[name], eager[name]), (seed, name)
     mu.muon_set_stream(None)
+
+
+def test_layernorm_of_more_rows_than_one_launch(gpu_lib):
+    """Past 2^32 threads' worth of rows: the last ones are those of a call on them alone."""
+    rows, cols = (1 << 23) + 5, 8
+    x = torch.empty((rows, cols), dtype=BF, device="cuda").normal_(generator=gen(31))
+    y, mean, rstd = torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    gpu_lib.muon_layernorm_forward(x, y, mean, rstd)
+    for part in (slice(0, 1000), slice((1 << 23) - 500, (1 << 23) + 5)):
+        y2, m2, r2 = torch.empty_like(x[part]), mean[part].clone(), rstd[part].clone()
+        gpu_lib.muon_layernorm_forward(x[part], y2, m2, r2)
+        assert torch.equal(y2, y[part]) and torch.equal(m2, mean[part]) and torch.equal(r2, rstd[part])
+        close(n64(y2), T.layernorm(n64(x[part]))[0], 2.0 ** -8 * np.abs(n64(y2)) + 2e-3, "y")
+
+
+def test_weight_grad_of_one_slot_into_many_groups(gpu_lib):
+    """Buffers smaller than a run, through the element form: the one slot belongs to group 2 of 40."""
+    ck, X = saved(gpu_lib, torch.tensor([[1.5, -2.0, 3.0]], device="cuda"))
+    dy = mat(torch.tensor([[0.5, 4.0]], device="cuda"), F32)
+    offsets = torch.tensor([0, 0, 0] + [1] * 38, dtype=torch.int32, device="cuda")
+    out = out_mat(40 * 2, 3, F32).view(40, 2, 3)
+    gpu_lib.muon_ckpt_weight_grad(dy, ck, out, offsets, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    ref, _ = T.weight_grad(n64(dy), X, offsets.tolist(), [0])
+    assert np.array_equal(n64(out), ref)  # exact in float32

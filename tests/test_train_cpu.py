@@ -200,3 +200,11 @@ def test_exchanging_the_workspace():
     assert swap(A * 2, 256, p, n) == mu.MUON_OK and p.value == A and n.value == 512
     assert swap(p, n, None, None) == mu.MUON_OK
     assert mu.lib().muon_get_workspace(p, n) == mu.MUON_OK and p.value == A and n.value == 512
+
+
+def test_pitches_whose_offsets_pass_64_bits():
+    far = 1 << 61
+    assert fwd(x=m(1, ld=far)) == SHAPE and fwd(y=m(2, ld=far)) == SHAPE
+    assert fwd(c=ck(7, ld_c=far)) == SHAPE and fwd(c=ck(7, ld_s=far)) == SHAPE
+    assert wgrad(g=m(3, 6, 8, ld=far)) == SHAPE and wgrad(stride=far) == SHAPE
+    assert rback(out=m(6, 6, 8, F32, ld=far)) == SHAPE
