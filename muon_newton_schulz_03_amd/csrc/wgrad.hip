@@ -16,9 +16,20 @@
 // Sums are float32 in the accumulators; the result is rounded once. Long sums
 // with few tiles are split into `splits` runs whose float32 partials a second
 // launch adds in order.
+//
+// A workgroup makes a 128 x 256 tile of the result in steps of 32 slots, which
+// go through two LDS stages. Dense, 8192 slots into 2048x7168 bf16, it runs at
+// 245 us (980 TFLOP/s) against the socket's power cap (1399 W, 2.1 GHz; a
+// gradient of zeros, which toggles less, takes 226 us at 2.4 GHz): dealing loads,
+// conversions and LDS traffic out between the products lost 10%, and tiles
+// ordered by XCD changed nothing. float32, 16384 slots into 512x2048: 113 us, 912
+// TFLOP/s of bf16 products. Many short groups, 128 of 256 slots into 768x2048:
+// 196 us, of which about 110 are the tiles' first loads and last stores (403 MB
+// of gradients at 5 TB/s are 81 us).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "lanes.h"
 #include "train.h"
@@ -33,7 +44,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kBM = 128;       // tile rows (n)
 constexpr int kBN = 256;       // tile columns (k)
 constexpr int kBK = 32;        // slots a step
-constexpr int kThreads = 256;  // 4 waves, each 128 x 64 of the tile
 constexpr int kABytes = kBK * kBM * 2;
 constexpr int kXBytes = kBK * kBN * 2;
 // slot / per_token for slots below 2^31, as the high half of 2 slot * mul
@@ -52,6 +62,19 @@ constexpr int stage_bytes() {
 // bytes), run i of row t at place i ^ (t & 3) within its four. A transposing
 // read takes 32 columns of four consecutive rows: four different quarters of
 // the 256-byte bank row.
+// Two forms of a tile's workgroup. Four waves of 128 x 64 each read the least
+// from LDS and hold two steps' loads; two workgroups fill a CU's registers.
+// Eight waves of 64 x 64 hold one step's loads and one group's fragments, and
+// twice as many waves hide what short groups mostly wait for: the first loads
+// and the last stores of a tile.
+template <int kWaves>
+struct Form {
+  static constexpr int kThreads = kWaves * 64;
+  static constexpr int kI = kWaves == 4 ? 4 : 2;        // 32-row runs of a wave's part
+  static constexpr int kR = kBK * 16 / kThreads;        // rows of a step that a thread stages
+  static constexpr int kAhead = kWaves == 4 ? 1 : 0;    // groups whose fragments are read ahead
+};
+
 __device__ inline int lds_at(int row, int col, int pitch) {
   const int run = col >> 5;
   return row * pitch + (((run & ~3) | ((run ^ row) & 3)) << 6) + (col & 31) * 2;
@@ -111,21 +134,24 @@ __device__ inline uint32_t raw_word(const Raw8<float> &r, int i) { return r.v[i 
 __device__ inline void raw_word(Raw8<__bf16> &r, int i, uint32_t w) { r.v[i] = w; }
 __device__ inline void raw_word(Raw8<float> &r, int i, uint32_t w) { r.v[i >> 2][i & 3] = w; }
 
-// What a thread holds of a step on its way to LDS: two rows' runs of 8
-// gradients, and two rows' runs of 16 codes with their scales.
-template <typename T>
+// What a thread holds of a step on its way to LDS: its rows' runs of 8
+// gradients, and their runs of 16 codes with their scales.
+template <typename T, int kR>
 struct Staged {
-  Raw8<T> dy[2];
-  u32x4 codes[2];
-  uint32_t scale[2];
+  Raw8<T> dy[kR];
+  u32x4 codes[kR];
+  uint32_t scale[kR];
   // bit r: row r adds nothing (past the group's end, or no such token); from
   // bit 4 + 4 r and 16 + 8 r: by how many bytes the run of row r was read too
   // early (codes, gradients), so as not to pass the buffer's end
   uint32_t fix;
 };
 
-template <typename T, bool kRows, bool kPartial>
-__global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, const TokenOf div) {
+template <typename T, int kWaves, bool kRows, bool kPartial>
+__global__ __launch_bounds__(kWaves * 64, kWaves / 2) void wgrad_kernel(const WgradArgs a, const TokenOf div) {
+  using F = Form<kWaves>;
+  constexpr int kI = F::kI, kR = F::kR, kAhead = F::kAhead;
+  using Held = Staged<T, kR>;
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kPlanes = kF32 ? 3 : 1;
   constexpr int kStage = stage_bytes<kF32>();
@@ -154,7 +180,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
   const int steps = (len + kBK - 1) / kBK;
 
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
-  const int srow = tid >> 4;               // staged rows srow and srow + 16 of a step
+  const int srow = tid >> 4;               // staged rows srow (and srow + 16) of a step
   const int dcol = n0 + (tid & 15) * 8;    // 8 gradients
   const int xcol = k0 + (tid & 15) * 16;   // 16 codes
   // this run's first slot, and where the buffers' last runs start (bytes)
@@ -164,8 +190,9 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
   const int32_t *rows = a.rows + lo;
   // runs that lie wholly past the tile's matrix read its first column instead
   const int dc = dcol < a.n ? dcol : 0, xc = xcol < a.k ? xcol : 0;
-  const int64_t dy_at[2] = {(srow * a.ld_dy + dc) * int64_t(sizeof(T)),
-                            ((srow + 16) * a.ld_dy + dc) * int64_t(sizeof(T))};
+  int64_t dy_at[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) dy_at[r] = ((srow + 16 * r) * a.ld_dy + dc) * int64_t(sizeof(T));
   const GlobalPtr codes = GlobalPtr(static_cast<const void *>(a.x.codes)) + xc;
   const GlobalPtr scales = GlobalPtr(static_cast<const void *>(a.x.scales)) + (xc >> 7);
   const uint32_t ld_codes = uint32_t(a.x.ld_codes), ld_scales = uint32_t(a.x.ld_scales);
@@ -174,11 +201,11 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
   const int32_t safe = spare < 0 ? -1 : int32_t(spare / a.x.ld_codes);
 
   // the slots of a step's rows (a row past the end repeats the last)
-  auto slots_of = [&](int step, uint32_t (&slot)[2]) {
+  auto slots_of = [&](int step, uint32_t (&slot)[kR]) {
     const int st = step < steps ? step : steps - 1;
     const int most = len - 1 - st * kBK;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < kR; ++r) {
       const int at = srow + 16 * r < most ? srow + 16 * r : most;
       slot[r] = kRows ? uint32_t(rows[st * kBK + at]) : uint32_t(int32_t(lo) + st * kBK + at);
     }
@@ -188,14 +215,16 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
   // later wait one for all loads in flight. A run that reaches past its row's
   // end reads what lies behind it in the buffer (those columns' sums are not
   // stored), and one that would pass the buffer starts that much earlier.
-  auto fetch = [&](int step, uint32_t (&slot)[2], Staged<T> &st) {
+  auto fetch = [&](int step, uint32_t (&slot)[kR], Held &st) {
     st.fix = 0;
     const int near = step < steps ? step : steps - 1;
     const GlobalPtr base = dy + near * dy_step;
-    int64_t p[2] = {dy_at[0], dy_at[1]};
+    int64_t p[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) p[r] = dy_at[r];
     if (step * kBK + kBK > len || dy_last - near * dy_step < dy_step) {  // the last steps
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < kR; ++r) {
         if (step * kBK + srow + 16 * r >= len) st.fix |= 1u << r;
         const int most = len - 1 - near * kBK;
         const int at = srow + 16 * r < most ? srow + 16 * r : most;
@@ -207,16 +236,16 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
         }
       }
     }
-    uint32_t q[2], early[2] = {0, 0};
+    uint32_t q[kR], early[kR] = {};
     bool odd = false;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < kR; ++r) {
       q[r] = __umulhi(slot[r] << 1, div.mul) >> div.shift;  // slot / per_token
       odd |= slot[r] >= div.end || int32_t(q[r]) > safe;
     }
     if (__any(odd)) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < kR; ++r) {
         if (slot[r] >= div.end) {  // no such token
           st.fix |= 1u << r;
           q[r] = 0;
@@ -229,7 +258,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
     }
     slots_of(step + 2, slot);  // before the codes: waiting for it is not waiting for them
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < kR; ++r) {
       if constexpr (kF32) {
         st.dy[r].v[0] = load16(base + p[r]);
         st.dy[r].v[1] = load16(base + p[r] + 16);
@@ -240,11 +269,11 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
       st.scale[r] = uint8_t(scales[uint64_t(q[r]) * ld_scales]);
     }
   };
-  auto to_lds = [&](Staged<T> &st, char *stage) {
+  auto to_lds = [&](Held &st, char *stage) {
     char *xs = stage + kPlanes * kABytes;
     if (__any(st.fix != 0)) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < kR; ++r) {
         constexpr int kDwords = int(sizeof(T)) * 2;
         uint32_t d[kDwords], c[4];
 #pragma unroll
@@ -261,7 +290,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
       }
     }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < kR; ++r) {
       const int row = srow + 16 * r;
       const int at = lds_at(row, dcol - n0, kBM * 2);
       if constexpr (kF32) {
@@ -292,9 +321,10 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
     }
   };
 
-  f32x16 acc[4][2];
+  f32x16 acc[kI][2];
+  const int wn = (wave >> 2) * 64, wk = (wave & 3) * 64;  // the wave's part of the tile
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kI; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -305,11 +335,11 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
   // 4 (lane % 4) of a 32-column run
   const int trow = 8 * (lane >> 5) + ((lane & 15) >> 2);
   const int tcol = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-  int aoff[4], xoff[2];
+  int aoff[kI], xoff[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) aoff[i] = lds_at(trow, 32 * i + tcol, kBM * 2);
+  for (int i = 0; i < kI; ++i) aoff[i] = lds_at(trow, wn + 32 * i + tcol, kBM * 2);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) xoff[j] = lds_at(trow, wave * 64 + 32 * j + tcol, kBN * 2);
+  for (int j = 0; j < 2; ++j) xoff[j] = lds_at(trow, wk + 32 * j + tcol, kBN * 2);
   typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
   auto frag = [&](const char *base, int off, int pitch) {
     typedef __attribute__((address_space(3))) const char *lds_char;
@@ -318,40 +348,43 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(p, q, 0, 1, 2, 3, 4, 5, 6, 7));
   };
   // The fragments of a group (16 slots of one part of dy) are read while the
-  // products of the group before run.
-  bf16x8 af[2][4], bf[2][2];
+  // products of the group before run (kAhead).
+  bf16x8 af[kAhead + 1][kI], bf[kAhead + 1][2];
   auto read_x = [&](const char *stage, int kk) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) bf[kk & 1][j] = frag(stage + kPlanes * kABytes + kk * 16 * kBN * 2, xoff[j], kBN * 2);
+    for (int j = 0; j < 2; ++j) bf[kk & kAhead][j] = frag(stage + kPlanes * kABytes + kk * 16 * kBN * 2, xoff[j], kBN * 2);
   };
   auto read_dy = [&](const char *stage, int g) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      af[g & 1][i] = frag(stage + (g % kPlanes) * kABytes + (g / kPlanes) * 16 * kBM * 2, aoff[i], kBM * 2);
+    for (int i = 0; i < kI; ++i)
+      af[g & kAhead][i] = frag(stage + (g % kPlanes) * kABytes + (g / kPlanes) * 16 * kBM * 2, aoff[i], kBM * 2);
   };
   constexpr int kGroups = kBK / 16 * kPlanes;
   auto compute = [&](const char *stage) {
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      if (g + 1 < kGroups) {
-        if ((g + 1) % kPlanes == 0) read_x(stage, (g + 1) / kPlanes);
-        read_dy(stage, g + 1);
+      const int next = g + kAhead;
+      if (next < kGroups) {
+        if (next % kPlanes == 0) read_x(stage, next / kPlanes);
+        read_dy(stage, next);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kI; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[g & 1][i], bf[g / kPlanes & 1][j], acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[g & kAhead][i], bf[g / kPlanes & kAhead][j], acc[i][j], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 
   // Step s is in LDS; step s + 1, loaded earlier, goes to the other stage, and
   // one further on is fetched into its registers.
-  auto pass = [&](int s, int fetched, Staged<T> &st, uint32_t (&slot)[2], char *now, char *next) {
-    read_x(now, 0);
-    read_dy(now, 0);
+  auto pass = [&](int s, int fetched, Held &st, uint32_t (&slot)[kR], char *now, char *next) {
+    if constexpr (kAhead) {
+      read_x(now, 0);
+      read_dy(now, 0);
+    }
     to_lds(st, next);
     fetch(fetched, slot, st);
     __builtin_amdgcn_sched_barrier(0);
@@ -359,11 +392,11 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
     __syncthreads();
   };
   if (steps > 0) {
-    uint32_t t0[2], t1[2];
+    uint32_t t0[kR], t1[kR];
     slots_of(0, t0);
     slots_of(1, t1);
-    if constexpr (kF32) {  // three products a step hide a load by themselves
-      Staged<T> st;
+    if constexpr (kF32 || kWaves == 8) {  // three products a step, or more waves, hide a load by themselves
+      Held st;
       fetch(0, t0, st);
       to_lds(st, lds);
       fetch(1, t1, st);
@@ -374,7 +407,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
         pass(s + 1, s + 3, st, t1, lds + kStage, lds);
       }
     } else {
-      Staged<T> s0, s1;
+      Held s0, s1;
       fetch(0, t0, s0);
       fetch(1, t1, s1);
       to_lds(s0, lds);
@@ -393,7 +426,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
   // 8 (r / 4) + 4 (lane / 32) + r % 4, column lane % 32.
   float *buf = reinterpret_cast<float *>(lds) + wave * 32 * kOutPitch;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kI; ++i) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -404,7 +437,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(const WgradArgs a, c
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int row = q * 8 + (lane >> 3), col = (lane & 7) * 8;
-      const int n = n0 + i * 32 + row, k = k0 + wave * 64 + col;
+      const int n = n0 + wn + i * 32 + row, k = k0 + wk + col;
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = buf[row * kOutPitch + col + e];
@@ -465,7 +498,7 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const WgradArgs a) {
   float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   const int64_t step = int64_t(a.groups) * a.n * a.k;
   const float *p = a.part + row * a.k + k;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < a.splits; ++s) {
     const Raw8<float> r = load8(p + s * step, a.k - k);
 #pragma unroll
@@ -476,9 +509,6 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const WgradArgs a) {
 
 template <typename T>
 hipError_t wgrad(const WgradArgs &a, hipStream_t s) {
-  constexpr int kStage = stage_bytes<sizeof(T) == 4>();
-  constexpr int kEpilogue = 4 * 32 * kOutPitch * 4;
-  constexpr int kLds = 2 * kStage > kEpilogue ? 2 * kStage : kEpilogue;
   const uint32_t work = uint32_t(a.tiles_n) * a.tiles_k * a.splits * a.groups;
   // mul = ceil(2^(31 + shift) / d) with 2^(shift - 1) < d <= 2^shift: exact up
   // to 2^31 (the excess mul d - 2^(31 + shift) < d adds less than 1 / d there)
@@ -493,9 +523,20 @@ hipError_t wgrad(const WgradArgs &a, hipStream_t s) {
     return hipGetLastError();
   }
   const dim3 grid(work);
-  auto kernel = a.splits == 1 ? (a.rows ? wgrad_kernel<T, true, false> : wgrad_kernel<T, false, false>)
-                              : (a.rows ? wgrad_kernel<T, true, true> : wgrad_kernel<T, false, true>);
-  hipLaunchKernelGGL(kernel, grid, dim3(kThreads), kLds, s, a, div);
+  auto go = [&](auto form) {
+    constexpr int kWaves = decltype(form)::value;
+    constexpr int kStage = stage_bytes<sizeof(T) == 4>(), kEpilogue = kWaves * 32 * kOutPitch * 4;
+    constexpr int kLds = 2 * kStage > kEpilogue ? 2 * kStage : kEpilogue;
+    auto kernel = a.splits == 1 ? (a.rows ? wgrad_kernel<T, kWaves, true, false> : wgrad_kernel<T, kWaves, false, false>)
+                                : (a.rows ? wgrad_kernel<T, kWaves, true, true> : wgrad_kernel<T, kWaves, false, true>);
+    hipLaunchKernelGGL(kernel, grid, dim3(kWaves * 64), kLds, s, a, div);
+  };
+  // Groups of 512 slots (64 of 768x2048): 179 us with eight waves, 186 with four;
+  // of 1024: 173 and 170; of 256 and fewer 5 to 20% in favour of eight.
+  if (a.slots < 768 * int64_t(a.groups))
+    go(std::integral_constant<int, 8>());
+  else
+    go(std::integral_constant<int, 4>());
   if (a.splits == 1) return hipGetLastError();
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -506,14 +547,26 @@ hipError_t wgrad(const WgradArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Splits: enough that two workgroups a CU have work, of 128 slots at least.
+// A sum is split where that is the shorter of both by these measured times: a
+// step of 32 slots takes 0.7 us (float32 1.8) with a workgroup a CU, a third
+// more with two; each split writes and reads 8 bytes an element at 5 TB/s and
+// adds a load to the joining launch, which itself takes 5 us. 512 slots into
+// 768x2048 take 16 us whole and 24 in four; 16384 into 512x2048 361 us whole and
+// 62 in sixteen.
 void wgrad_plan(WgradArgs &a, bool bf16) {
-  (void)bf16;
   a.tiles_n = (a.n + kBM - 1) / kBM;
   a.tiles_k = (a.k + kBN - 1) / kBN;
+  a.splits = 1;
   const int64_t tiles = int64_t(a.tiles_n) * a.tiles_k * a.groups;
-  const int64_t len = (a.slots + a.groups - 1) / a.groups;
-  a.splits = int32_t(std::max<int64_t>(1, std::min<int64_t>(512 / tiles, len / 128)));
+  const double steps = double(a.slots) / a.groups / kBK, step_us = bf16 ? 0.7 : 1.8;
+  const double each_us = double(a.groups) * a.n * a.k * 8 / 5e6 + 0.1;
+  double best = 0;
+  for (int64_t s = 1; s * tiles <= 512 && (s == 1 || s <= steps); s *= 2) {
+    const double us = steps / double(s) * step_us * (s * tiles > 256 ? 1.35 : 1.0) + (s > 1 ? 5 + double(s) * each_us : 0);
+    if (s > 1 && us >= best) continue;
+    best = us;
+    a.splits = int32_t(s);
+  }
 }
 
 size_t wgrad_part_bytes(const WgradArgs &a) {

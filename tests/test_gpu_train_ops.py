@@ -513,3 +513,24 @@ def test_weight_grad_of_one_slot_into_many_groups(gpu_lib):
     gpu_lib.muon_ckpt_weight_grad(dy, ck, out, offsets, torch.zeros(1, dtype=torch.int32, device="cuda"))
     ref, _ = T.weight_grad(n64(dy), X, offsets.tolist(), [0])
     assert np.array_equal(n64(out), ref)  # exact in float32
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tokens,topk,experts,n,k", [(1600, 2, 3, 129, 131), (900, 1, 1, 300, 515), (2500, 4, 8, 64, 48)])
+def test_weight_grad_long_groups(gpu_lib, tokens, topk, experts, n, k, dtype):
+    """Groups long enough for the wider form, through their lists, with slots of no token among them."""
+    mu, g = gpu_lib, gen(tokens + n)
+    ck, X = saved(mu, randn(g, tokens, k))
+    rows, offsets = lists(g, tokens, topk, experts)
+    dy = mat(randn(g, tokens * topk, n, scale=1e-3), dtype)
+    gone = torch.rand(len(rows), generator=g, device="cuda") < 0.01
+    bad = torch.where(torch.arange(len(rows), device="cuda") % 2 == 0, -1, tokens * topk).to(torch.int32)
+    rows = torch.where(gone, bad, rows)
+    dy[gone] = float("nan")  # what such a slot's gradient holds does not count
+    out = out_mat(experts * n, k, dtype)
+    mu.muon_ckpt_weight_grad(dy, ck, out.view(experts, n, k), offsets, rows, topk)
+    there = torch.where(gone, 0, rows)
+    D = np.where(gone.cpu().numpy()[:, None], 0.0, n64(dy))
+    ref, mag = T.weight_grad(D, X, offsets.tolist(), there.cpu().numpy(), topk)
+    length = int((offsets[1:] - offsets[:-1]).max())
+    close(n64(out).reshape(ref.shape), ref, wgrad_tol(dtype, ref, mag, length), "gradients")
