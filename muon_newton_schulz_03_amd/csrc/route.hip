@@ -11,6 +11,11 @@
 //   the weights' gradient g, d + g at the choice (plain weights) or
 //   w (g - sum w g) at the choice (shares).
 //
+// 16384 tokens to 8 of 384 experts, bf16: forward 24 us, of which the choice 15,
+// the sums over workgroups 5 and the lists 4: bound by the instructions of the
+// choice and by three launches, not by its 14 MB. Backward, float32, 13 us for
+// 51 MB (4.0 TB/s). 32 tokens to 8 of 128, one launch: 7.6 us.
+//
 // Forward, 16 lanes hold a token's logits, four tokens a wave: each of the k
 // rounds finds the maximum and its lowest index by lane permutations, and the
 // instructions of a round serve four tokens. Backward, a wave holds one token.
