@@ -71,6 +71,7 @@ struct WgradArgs {
   float *part;             // [splits][groups][n][k] float32, when splits > 1
   int32_t splits;
   int32_t tiles_n, tiles_k;
+  int4 *order;             // groups by length (group, first slot, end), or NULL: in the given order
 };
 
 struct RouteFwdArgs {
@@ -109,9 +110,11 @@ hipError_t launch_norm_fwd(const NormFwdArgs &a, bool bf16, hipStream_t s);
 hipError_t launch_norm_bwd(const NormBwdArgs &a, bool bf16, hipStream_t s);
 hipError_t launch_ckpt_save(const CkptArgs &a, bool bf16, hipStream_t s);
 hipError_t launch_ckpt_load(const CkptArgs &a, bool bf16, hipStream_t s);
-// Fills tiles and splits of a; the float32 partials take wgrad_part_bytes.
+// Fills tiles and splits of a; the float32 partials take wgrad_part_bytes, the
+// order of the groups wgrad_order_bytes.
 void wgrad_plan(WgradArgs &a, bool bf16);
 size_t wgrad_part_bytes(const WgradArgs &a);
+size_t wgrad_order_bytes(const WgradArgs &a);  // not with partials
 hipError_t launch_wgrad(const WgradArgs &a, bool bf16, hipStream_t s);
 void route_plan(RouteFwdArgs &a);
 hipError_t launch_route_fwd(const RouteFwdArgs &a, bool bf16, hipStream_t s);

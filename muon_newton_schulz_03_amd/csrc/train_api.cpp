@@ -356,7 +356,7 @@ muon_status muon_ckpt_weight_grad_workspace_size(int32_t dtype, int64_t slots, i
     need(bytes, "bytes");
     WgradArgs a{};
     wgrad_shape(a, dtype, slots, n, k, groups);
-    *bytes = groups > 0 ? wgrad_part_bytes(a) : 0;
+    *bytes = groups > 0 ? wgrad_part_bytes(a) + wgrad_order_bytes(a) : 0;
   });
 }
 
@@ -394,7 +394,8 @@ muon_status muon_ckpt_weight_grad(const muon_mat *dy, const muon_ckpt *x, const 
                     : b.add(grads->data, 1, (n_groups - 1) * group_stride * es + extent, 0, true, "grads");
     b.add(offsets, 1, (int64_t(n_groups) + 1) * 4, 0, false, "offsets");
     b.add(rows, 1, dy->rows * 4, 0, false, "rows");
-    char *ws = n_groups > 0 ? workspace(st, wgrad_part_bytes(a), b) : nullptr;
+    const size_t parts = n_groups > 0 ? wgrad_part_bytes(a) : 0, order = n_groups > 0 ? wgrad_order_bytes(a) : 0;
+    char *ws = workspace(st, parts + order, b);
     b.check();
     if (n_groups == 0) return;
     a.dy = dy->data;
@@ -407,6 +408,7 @@ muon_status muon_ckpt_weight_grad(const muon_mat *dy, const muon_ckpt *x, const 
     a.ld_out = grads->ld;
     a.stride = group_stride;
     a.part = reinterpret_cast<float *>(ws);
+    a.order = order ? reinterpret_cast<int4 *>(ws) : nullptr;
     launched(launch_wgrad(a, dy->dtype == MUON_BF16, st.stream), "weight gradient launch");
   });
 }

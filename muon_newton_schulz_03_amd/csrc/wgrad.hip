@@ -24,8 +24,8 @@
 // conversions and LDS traffic out between the products lost 10%, and tiles
 // ordered by XCD changed nothing. float32, 16384 slots into 512x2048: 113 us, 912
 // TFLOP/s of bf16 products. Many short groups, 128 of 256 slots into 768x2048:
-// 196 us, of which about 110 are the tiles' first loads and last stores (403 MB
-// of gradients at 5 TB/s are 81 us).
+// 191 us, of which about 95 are the tiles' first loads and last stores (403 MB of
+// gradients at 5 TB/s are 81 us); the socket draws 1399 W there too.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -51,6 +51,7 @@ constexpr int kXBytes = kBK * kBN * 2;
 struct TokenOf {
   uint32_t mul, shift, end;
 };
+constexpr int kOrderGroups = 512;  // more groups run in the given order
 constexpr int kOutPitch = 64 + 4;  // floats; epilogue rows of a wave
 
 template <bool kF32>
@@ -147,6 +148,32 @@ struct Staged {
   uint32_t fix;
 };
 
+__device__ inline void group_range(const WgradArgs &a, int group, int64_t &lo, int64_t &hi) {
+  lo = a.offsets[group];
+  hi = a.offsets[group + 1];
+  lo = lo < 0 ? 0 : lo;
+  hi = hi > a.slots ? a.slots : hi;
+}
+
+// The groups and their slots, the longest first (the lower index among
+// equals). Long groups started last would leave most of the chip idle: 16 groups
+// of 2048 slots on average, 768x2048 bf16, take 159 us in the given order and 135 in
+// this one, 64 of 512 slots, 768x768 float32, 193 and 157.
+__global__ __launch_bounds__(kOrderGroups) void wgrad_order_kernel(const WgradArgs a) {
+  __shared__ int len[kOrderGroups];
+  const int g = int(threadIdx.x);
+  int64_t lo = 0, hi = 0;
+  if (g < a.groups) group_range(a, g, lo, hi);
+  const int mine = hi > lo ? int(hi - lo) : 0;
+  len[g] = mine;
+  __syncthreads();
+  if (g >= a.groups) return;
+  int rank = 0;
+#pragma unroll 8
+  for (int i = 0; i < a.groups; ++i) rank += len[i] > mine || (len[i] == mine && i < g) ? 1 : 0;
+  a.order[rank] = int4{g, int(lo), int(hi), 0};
+}
+
 template <typename T, int kWaves, bool kRows, bool kPartial>
 __global__ __launch_bounds__(kWaves * 64, kWaves / 2) void wgrad_kernel(const WgradArgs a, const TokenOf div) {
   using F = Form<kWaves>;
@@ -161,15 +188,17 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 2) void wgrad_kernel(const Wg
   const uint32_t tiles = uint32_t(a.tiles_n) * a.tiles_k;
   const uint32_t tile = id % tiles;
   id /= tiles;
-  const int split = int(id % uint32_t(a.splits)), group = int(id / uint32_t(a.splits));
+  const int split = int(id % uint32_t(a.splits));
+  int group = int(id / uint32_t(a.splits));
   const int n0 = int(tile / uint32_t(a.tiles_k)) * kBM, k0 = int(tile % uint32_t(a.tiles_k)) * kBN;
 
   int64_t lo = 0, hi = a.slots;
-  if (a.offsets) {
-    lo = a.offsets[group];
-    hi = a.offsets[group + 1];
-    lo = lo < 0 ? 0 : lo;
-    hi = hi > a.slots ? a.slots : hi;
+  if (a.order) {
+    lo = a.order[group].y;
+    hi = a.order[group].z;
+    group = a.order[group].x;
+  } else if (a.offsets) {
+    group_range(a, group, lo, hi);
   }
   if (a.splits > 1 && hi > lo) {
     const int64_t each = ((hi - lo + a.splits - 1) / a.splits + kBK - 1) / kBK * kBK;
@@ -522,6 +551,11 @@ hipError_t wgrad(const WgradArgs &a, hipStream_t s) {
     hipLaunchKernelGGL(wgrad_tiny_kernel<T>, dim3(unsigned(std::min<int64_t>((total + 255) / 256, 1 << 20))), dim3(256), 0, s, a);
     return hipGetLastError();
   }
+  if (a.order) {
+    hipLaunchKernelGGL(wgrad_order_kernel, dim3(1), dim3(kOrderGroups), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   const dim3 grid(work);
   auto go = [&](auto form) {
     constexpr int kWaves = decltype(form)::value;
@@ -571,6 +605,17 @@ void wgrad_plan(WgradArgs &a, bool bf16) {
 
 size_t wgrad_part_bytes(const WgradArgs &a) {
   return a.splits > 1 ? size_t(a.splits) * a.groups * a.n * a.k * sizeof(float) : 0;
+}
+
+// Worth its launch where not all tiles are at work at once and the products
+// outweigh the stores: the order brings the long groups' products together, and
+// then the short ones' stores. 128 slots a group on average (32 groups of 768x2048
+// float32) take 110 us in the given order and 124 by length; 256 (128 groups, bf16)
+// 192 and 190.
+size_t wgrad_order_bytes(const WgradArgs &a) {
+  const int64_t tiles = int64_t(a.tiles_n) * a.tiles_k * a.groups;
+  if (a.groups < 2 || a.groups > kOrderGroups || tiles <= 512 || a.slots < 256 * int64_t(a.groups)) return 0;
+  return size_t(a.groups) * sizeof(int4);
 }
 
 hipError_t launch_wgrad(const WgradArgs &a, bool bf16, hipStream_t s) {

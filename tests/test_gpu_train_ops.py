@@ -534,3 +534,21 @@ def test_weight_grad_long_groups(gpu_lib, tokens, topk, experts, n, k, dtype):
     ref, mag = T.weight_grad(D, X, offsets.tolist(), there.cpu().numpy(), topk)
     length = int((offsets[1:] - offsets[:-1]).max())
     close(n64(out).reshape(ref.shape), ref, wgrad_tol(dtype, ref, mag, length), "gradients")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_weight_grad_of_more_tiles_than_run_at_once(gpu_lib, dtype):
+    """Groups by length: very uneven, equal and empty ones, and slots outside every group."""
+    mu, g = gpu_lib, gen(41)
+    tokens, n, k = 900, 256, 2304
+    counts = [700, 0, 500, 700, 3, 1, 0, 500] * 4
+    slots = sum(counts) + 9
+    ck, X = saved(mu, randn(g, tokens, k))
+    rows = torch.randint(0, tokens, (slots,), generator=g, device="cuda").to(torch.int32)
+    offsets = torch.tensor(np.append(0, np.cumsum(counts)), dtype=torch.int32, device="cuda")
+    dy = mat(randn(g, slots, n, scale=1e-3), dtype)
+    out = out_mat(len(counts) * n, k, dtype)
+    assert mu.muon_ckpt_weight_grad_workspace_size(mu.MUON_F32 if dtype == F32 else mu.MUON_BF16, slots, n, k, len(counts)) > 0
+    mu.muon_ckpt_weight_grad(dy, ck, out.view(len(counts), n, k), offsets, rows)
+    ref, mag = T.weight_grad(n64(dy), X, offsets.tolist(), rows.cpu().numpy())
+    close(n64(out).reshape(ref.shape), ref, wgrad_tol(dtype, ref, mag, max(counts)), "gradients")
