@@ -94,10 +94,15 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
     }
   }
   row_sum<kTpr, 1>(s, lds, slot);
-  const float rstd = 1.f / sqrtf(s[0] / float(a.cols) + a.eps);
+  const float var = s[0] / float(a.cols) + a.eps, rstd = 1.f / sqrtf(var);
+  // what rounding took from rstd, rstd (1 - var rstd^2) / 2 with the product in two
+  // parts: where y is kept in 8 bits, the last bit of y decides a code
+  const float vr = var * rstd;
+  float rest = 0.5f * rstd * (fmaf(-vr, rstd, 1.f) - fmaf(var, rstd, -vr) * rstd);
+  rest = rstd > 0.f && rstd < 1e30f ? rest : 0.f;
   if (t == 0) {
     if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
+    if (a.rstd) a.rstd[row] = rstd + rest;
   }
 #pragma unroll
   for (int v = 0; v < kNv; ++v) {
@@ -109,7 +114,10 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
     if (a.w) w = load_run<kWhole>(static_cast<const W *>(a.w) + c, n);
     if (a.b) b = load_run<kWhole>(static_cast<const W *>(a.b) + c, n);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fmaf((xr[v].get(i) - mean) * rstd, w.get(i), b.get(i));
+    for (int i = 0; i < 8; ++i) {
+      const float d = xr[v].get(i) - mean;
+      f[i] = fmaf(fmaf(d, rest, d * rstd), w.get(i), b.get(i));
+    }
     const Raw8<T> r = pack8(f, T());
     if (n > 0) store_run<kWhole>(y + c, r, n);
     if constexpr (kCkpt) {
