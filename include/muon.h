@@ -412,7 +412,8 @@ muon_status muon_ckpt_weight_grad_workspace_size(int32_t dtype, int64_t slots, i
  * the experts; the choice is the topk largest logits, the lower index first
  * among equals; -inf and NaN are never chosen, so that a token may have
  * fewer choices, or (masked wholly) none.
- *   logits   tokens x experts, experts <= 1024, topk <= min(experts, 32).
+ *   logits   tokens x experts, experts <= 1024, topk <= min(experts, 32),
+ *            tokens * topk <= 2^31 - 2^22.
  *   indices  tokens x topk int32, by falling logit; -1 where nothing is left.
  *   weights  tokens x topk float32: p of the choice, with renormalize != 0
  *            over the sum of the token's chosen p; 0 where nothing is left.

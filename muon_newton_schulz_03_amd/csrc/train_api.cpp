@@ -186,7 +186,7 @@ void route_shape(int64_t tokens, int64_t experts, int32_t topk) {
     refuse(MUON_ERR_SHAPE, "experts must lie in [1, %d]", kRouteMaxExperts);
   if (topk < 1 || topk > kRouteMaxTopk || topk > experts)
     refuse(MUON_ERR_INVALID_ARG, "topk must lie in [1, min(experts, %d)]", kRouteMaxTopk);
-  if (tokens < 0 || tokens > kMaxIndex / topk) refuse(MUON_ERR_SHAPE, "tokens * topk must lie in [0, 2^31)");
+  if (tokens < 0 || tokens > kMaxSlots / topk) refuse(MUON_ERR_SHAPE, "tokens * topk must lie in [0, 2^31 - 2^22]");
 }
 
 void wgrad_shape(WgradArgs &a, int32_t dtype, int64_t slots, int64_t n, int64_t k, int64_t groups) {

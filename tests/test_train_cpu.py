@@ -208,3 +208,19 @@ def test_pitches_whose_offsets_pass_64_bits():
     assert fwd(c=ck(7, ld_c=far)) == SHAPE and fwd(c=ck(7, ld_s=far)) == SHAPE
     assert wgrad(g=m(3, 6, 8, ld=far)) == SHAPE and wgrad(stride=far) == SHAPE
     assert rback(out=m(6, 6, 8, F32, ld=far)) == SHAPE
+
+
+MOST = (1 << 31) - (1 << 22)  # slots, and with them tokens, that 32-bit counters can step past
+
+
+@pytest.mark.parametrize("topk", [1, 2, 8])
+def test_routing_counts_that_device_counters_cannot_pass(topk):
+    most = MOST // topk
+    assert mu.muon_route_workspace_size(most, 8, topk) > 0
+    for tokens in (most + 1, ((1 << 31) - 1) // topk):
+        with pytest.raises(mu.MuonError) as e:
+            mu.muon_route_workspace_size(tokens, 8, topk)
+        assert e.value.status == SHAPE
+        x = m(1, tokens, 8)
+        assert route(x=x, topk=topk, idx=A * 64, w=A * 96, c=A * 128, o=A * 160, r=A * 192, loss=A * 224) == SHAPE
+        assert rback(x=x, topk=topk, idx=A * 64, c=A * 128, dw=A * 160, dl=A * 192, out=m(256, tokens, 8)) == SHAPE
