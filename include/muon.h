@@ -388,8 +388,9 @@ muon_status muon_ckpt_load(const muon_ckpt *ckpt, const muon_mat *out);
  * Weight gradients of a group of expert layers, from the checkpoint of their
  * input:  grad_g[n, k] = sum over offsets[g] <= s < offsets[g + 1] of
  *   dy[s, n] * x[rows[s] / rows_per_token, k].
- *   dy        slots x n, in slot order; bf16 (products of bf16 values with
- *             float32 sums) or float32 (products exact in float32).
+ *   dy        slots x n, in slot order, slots <= 2^31 - 2^22; bf16 (products
+ *             of bf16 values with float32 sums) or float32 (products exact in
+ *             float32).
  *   x         tokens x k.
  *   grads     descriptor of the first group's n x k gradient, dy's dtype;
  *             group g's lies g * group_stride elements further. Overwritten;

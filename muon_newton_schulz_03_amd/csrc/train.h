@@ -13,8 +13,9 @@ constexpr int kCkptGroup = 128;        // columns that share one scale byte
 constexpr int kNormMaxCols = 32768;    // a row lives in one workgroup's registers
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxTopk = 32;
-// Routed slots of a call. The routing kernels count tokens and slots in 32 bits
-// and step past the last one by up to a workgroup's run of tokens, 2^21.
+// Slots of a call. The kernels count tokens and slots in 32 bits and step past the
+// last one, routing by up to a workgroup's run of 2^21 tokens, weight gradients by
+// a few steps of 32 slots.
 constexpr int64_t kMaxSlots = (int64_t(1) << 31) - (int64_t(1) << 22);
 
 // A checkpoint: e4m3 codes and one power-of-two scale byte per group.

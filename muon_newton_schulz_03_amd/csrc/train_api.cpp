@@ -191,8 +191,8 @@ void route_shape(int64_t tokens, int64_t experts, int32_t topk) {
 
 void wgrad_shape(WgradArgs &a, int32_t dtype, int64_t slots, int64_t n, int64_t k, int64_t groups) {
   if (dtype != MUON_F32 && dtype != MUON_BF16) refuse(MUON_ERR_DTYPE, "dy: unknown dtype");
-  if (slots < 0 || slots > kMaxIndex || n < 1 || k < 1 || n > kMaxIndex / 2 || k > kMaxIndex / 2)
-    refuse(MUON_ERR_SHAPE, "slots must lie in [0, 2^31), n and k in [1, 2^30)");
+  if (slots < 0 || slots > kMaxSlots || n < 1 || k < 1 || n > kMaxIndex / 2 || k > kMaxIndex / 2)
+    refuse(MUON_ERR_SHAPE, "slots must lie in [0, 2^31 - 2^22], n and k in [1, 2^30)");
   if (groups < 0 || groups > 65536) refuse(MUON_ERR_INVALID_ARG, "groups must lie in [0, 65536]");
   if (groups > 0 && ((n + 127) / 128) * ((k + 255) / 256) > kMaxIndex / 512 / groups)
     refuse(MUON_ERR_SHAPE, "groups * n * k too large");

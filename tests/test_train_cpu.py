@@ -224,3 +224,15 @@ def test_routing_counts_that_device_counters_cannot_pass(topk):
         x = m(1, tokens, 8)
         assert route(x=x, topk=topk, idx=A * 64, w=A * 96, c=A * 128, o=A * 160, r=A * 192, loss=A * 224) == SHAPE
         assert rback(x=x, topk=topk, idx=A * 64, c=A * 128, dw=A * 160, dl=A * 192, out=m(256, tokens, 8)) == SHAPE
+
+
+def test_weight_grad_slots_that_device_counters_cannot_pass():
+    size = mu.muon_ckpt_weight_grad_workspace_size
+    assert size(BF, MOST, 8, 8, 1) > 0 and size(F32, MOST, 4096, 4096, 1) == 0
+    for slots in (MOST + 1, (1 << 31) - 1):
+        for dtype in (BF, F32):
+            with pytest.raises(mu.MuonError) as e:
+                size(dtype, slots, 8, 8, 1)
+            assert e.value.status == SHAPE
+            assert wgrad(dy=m(1, slots, 8, dtype), x=ck(64, 1, 8), g=m(65, 8, 8, dtype), groups=1, offs=None, rows=A * 66,
+                         per=1) == SHAPE
