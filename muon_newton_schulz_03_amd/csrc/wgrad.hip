@@ -505,8 +505,8 @@ __global__ __launch_bounds__(256) void wgrad_tiny_kernel(const WgradArgs a) {
     }
     float s = 0.f;
     for (int64_t i = lo; i < hi; ++i) {
-      const uint32_t token = uint32_t(a.rows ? a.rows[i] : int32_t(i)) / uint32_t(a.per_token);
-      if (token >= uint32_t(a.tokens)) continue;
+      const int32_t slot = a.rows ? a.rows[i] : int32_t(i), token = slot / a.per_token;
+      if (slot < 0 || token >= a.tokens) continue;
       const float x = bits_f32(decode2<0>(a.x.codes[token * a.x.ld_codes + k], 1.f) << 16) *
                       scale_value(a.x.scales[token * a.x.ld_scales + (k >> 7)]);
       s = fmaf(float(static_cast<const T *>(a.dy)[i * a.ld_dy + n]), x, s);

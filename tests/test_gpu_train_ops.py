@@ -552,3 +552,17 @@ def test_weight_grad_of_more_tiles_than_run_at_once(gpu_lib, dtype):
     mu.muon_ckpt_weight_grad(dy, ck, out.view(len(counts), n, k), offsets, rows)
     ref, mag = T.weight_grad(n64(dy), X, offsets.tolist(), rows.cpu().numpy())
     close(n64(out).reshape(ref.shape), ref, wgrad_tol(dtype, ref, mag, max(counts)), "gradients")
+
+
+@pytest.mark.parametrize("slots", [3, 40])
+def test_weight_grad_of_slots_below_zero(gpu_lib, slots):
+    """A negative slot has no token, however many slots a token has: both for buffers smaller than a run and through the tiles."""
+    mu, g = gpu_lib, gen(51)
+    ck, X = saved(mu, randn(g, 3, 40))
+    dy = mat(randn(g, slots, 2), F32)
+    rows = torch.tensor([-1, 0, -7] + [-(1 << 31)] * (slots - 3), dtype=torch.int32, device="cuda")
+    for per in ((1 << 31) - 1, 1 << 30, 1):
+        out = out_mat(2, 40, F32)
+        mu.muon_ckpt_weight_grad(dy, ck, out[None], rows=rows, rows_per_token=per)
+        ref, mag = T.weight_grad(n64(dy)[1:2], X, [0, 1], [0])
+        close(n64(out), ref[0], wgrad_tol(F32, ref[0], mag[0], 3), "gradient")
