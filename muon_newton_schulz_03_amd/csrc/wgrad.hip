@@ -316,6 +316,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves / 2) void wgrad_kernel(const Wg
         for (int i = 0; i < kDwords; ++i) raw_word(st.dy[r], i, none ? 0u : d[i]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) st.codes[r][i] = none ? 0u : c[i];
+        st.scale[r] = none ? 127u : st.scale[r];  // that of another token: 0 times an infinity is no 0
       }
     }
 #pragma unroll

@@ -566,3 +566,21 @@ def test_weight_grad_of_slots_below_zero(gpu_lib, slots):
         mu.muon_ckpt_weight_grad(dy, ck, out[None], rows=rows, rows_per_token=per)
         ref, mag = T.weight_grad(n64(dy)[1:2], X, [0, 1], [0])
         close(n64(out), ref[0], wgrad_tol(F32, ref[0], mag[0], 3), "gradient")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_weight_grad_slots_of_no_token_beside_any_checkpoint(gpu_lib, dtype):
+    """What lies in a token's codes and scales does not reach a sum that has no slot of it."""
+    mu, g = gpu_lib, gen(52)
+    ck, X = saved(mu, randn(g, 50, 200))
+    ck.codes.view(torch.uint8)[0] = 0x7F
+    rows = torch.arange(1, 41, device="cuda", dtype=torch.int32)
+    rows[::3] = -1
+    dy = mat(randn(g, 40, 24, scale=1e-3), dtype)
+    there = (rows > 0).cpu().numpy()
+    ref, mag = T.weight_grad(n64(dy)[there], X, [0, int(there.sum())], rows.cpu().numpy()[there])
+    for byte in (0, 247, 248, 254, 255):
+        ck.scales[0] = byte
+        out = out_mat(24, 200, dtype)
+        mu.muon_ckpt_weight_grad(dy, ck, out[None], rows=rows)
+        close(n64(out), ref[0], wgrad_tol(dtype, ref[0], mag[0], 40), f"gradient, scale byte {byte}")
