@@ -9,6 +9,7 @@ raises.
 import ctypes
 import functools
 import json
+import operator
 import os
 import struct
 
@@ -370,7 +371,16 @@ def muon_adamw_step(params, grads, exp_avg, exp_avg_sq, lr=1e-3, beta1=0.9, beta
 
 _MAT = struct.Struct("=Qqqqii").pack   # muon_mat: data, rows, cols, ld, dtype, col_blocks
 _CKPT = struct.Struct("=QQqqqq").pack  # muon_ckpt
-_torch = _codes = None
+_torch = _codes = _ckpt_dtypes = None
+
+
+def _load_torch():
+    """torch and the dtypes of operands, looked up by the first call; the dtypes of a checkpoint."""
+    global _torch, _codes, _ckpt_dtypes
+    import torch
+    _torch, _codes = torch, {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
+    _ckpt_dtypes = (torch.float8_e4m3fn, torch.uint8)
+    return _ckpt_dtypes
 
 
 # The smallest calls take about as long here as on the GPU, so these helpers ask
@@ -428,31 +438,55 @@ def _vec(name, t, dtype, shape, device):
 class Checkpoint:
     """An activation checkpoint in 8 bits (see muon_ckpt in muon.h): `codes`,
     rows x cols float8_e4m3fn, and `scales`, rows x ceil(cols / 128) uint8,
-    both with unit column stride."""
+    both with unit column stride. The two tensors stay the checkpoint's own; if
+    their memory is exchanged (`codes.data = ...`), later calls use the new."""
 
-    __slots__ = ("codes", "scales", "_packed")
+    __slots__ = ("_codes", "_scales", "_key", "_packed")
 
     def __init__(self, codes, scales):
-        import torch
-        if codes.dtype != torch.float8_e4m3fn or scales.dtype != torch.uint8:
+        self._codes, self._scales = codes, scales
+        self._pack()
+
+    def _pack(self):
+        codes, scales = self._codes, self._scales
+        if (codes.dtype, scales.dtype) != (_ckpt_dtypes or _load_torch()):
             raise TypeError("a checkpoint holds float8_e4m3fn codes and uint8 scales")
-        if codes.dim() != 2 or scales.dim() != 2:
+        strides_c, strides_s = codes.stride(), scales.stride()
+        if len(strides_c) != 2 or len(strides_s) != 2:
             raise ValueError("a checkpoint's codes and scales are 2-D")
         rows, cols = codes.shape
         groups = -(-cols // MUON_CKPT_GROUP)
         if scales.shape != (rows, groups):
             raise ValueError(f"scales: expected shape {(rows, groups)}, got {tuple(scales.shape)}")
-        ld_c, unit_c = codes.stride()
-        ld_s, unit_s = scales.stride()
+        ld_c, unit_c = strides_c
+        ld_s, unit_s = strides_s
         if (cols > 1 and unit_c != 1) or (groups > 1 and unit_s != 1):
             raise ValueError("a checkpoint's codes and scales have unit column stride")
         if rows <= 1:
             ld_c, ld_s = cols, groups
         if ld_c < cols or ld_s < groups:
             raise ValueError("a checkpoint's rows overlap")
-        _on_gpu("scales", scales, _on_gpu("codes", codes, None))
-        self.codes, self.scales = codes, scales
-        self._packed = _CKPT(codes.data_ptr(), scales.data_ptr(), rows, cols, ld_c, ld_s)
+        device = codes.get_device()
+        if device < 0 or scales.get_device() != device:
+            _on_gpu("scales", scales, _on_gpu("codes", codes, None))
+        at_c, at_s = codes.data_ptr(), scales.data_ptr()
+        self._key = (at_c, at_s, rows * cols, rows * groups)
+        self._packed = _CKPT(at_c, at_s, rows, cols, ld_c, ld_s)
+
+    def _desc(self, device):
+        """Packed muon_ckpt of the tensors as they are now, on a call's device."""
+        codes, scales = self._codes, self._scales
+        if self._key != (codes.data_ptr(), scales.data_ptr(), codes.numel(), scales.numel()):
+            for t in (codes, scales):
+                if t.numel() and not t.untyped_storage().nbytes():
+                    raise ValueError("the checkpoint's memory has been freed")
+            self._pack()
+        if codes.get_device() != device:
+            _on_gpu("ckpt", codes, device)
+        return self._packed
+
+    codes = property(operator.attrgetter("_codes"))
+    scales = property(operator.attrgetter("_scales"))
 
     @classmethod
     def empty(cls, rows, cols, device="cuda"):
@@ -463,19 +497,17 @@ class Checkpoint:
 
     @property
     def shape(self):
-        return self.codes.shape
+        return self._codes.shape
 
 
 def _enter(t):
     """The device index of a call's first tensor; its current stream becomes the call's."""
-    global _torch, _codes
     if _codes is None:
-        import torch
-        _torch, _codes = torch, {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
+        _load_torch()
     device = _on_gpu("argument", t, None)
-    if device != _torch.cuda.current_device():
+    # torch.cuda.current_device and the raw handle of torch.cuda.current_stream, without what they wrap around them
+    if device != _torch._C._cuda_getDevice():
         raise ValueError("the tensors are not on the current device")
-    # the raw handle of torch.cuda.current_stream, without an object around it
     _check((_lib or lib()).muon_set_stream(_torch._C._cuda_getCurrentRawStream(device)))
     return device
 
@@ -528,11 +560,9 @@ def muon_layernorm_forward(x, y, mean=None, rstd=None, weight=None, bias=None, e
     that receives y in 8 bits in the same pass."""
     d = _enter(x)
     f32, rows = _torch.float32, x.shape[:1]
-    if ckpt is not None:
-        _on_gpu("ckpt", ckpt.codes, d)
     _check(_lib.muon_layernorm_forward(
         _mat("x", x, d), _mat("y", y, d), _vec("mean", mean, f32, rows, d), _vec("rstd", rstd, f32, rows, d),
-        _mat("weight", weight, d), _mat("bias", bias, d), eps, None if ckpt is None else ckpt._packed))
+        _mat("weight", weight, d), _mat("bias", bias, d), eps, None if ckpt is None else ckpt._desc(d)))
 
 
 def muon_layernorm_backward(dy, x, mean, rstd, dx, weight=None, dweight=None, dbias=None, workspace=None):
@@ -550,15 +580,13 @@ def muon_layernorm_backward(dy, x, mean, rstd, dx, weight=None, dweight=None, db
 def muon_ckpt_save(x, ckpt):
     """Save the matrix x as an 8-bit checkpoint (see muon.h)."""
     d = _enter(x)
-    _on_gpu("ckpt", ckpt.codes, d)
-    _check(_lib.muon_ckpt_save(_mat("x", x, d), ckpt._packed))
+    _check(_lib.muon_ckpt_save(_mat("x", x, d), ckpt._desc(d)))
 
 
 def muon_ckpt_load(ckpt, out):
     """Load a checkpoint's values into the matrix out (see muon.h)."""
     d = _enter(out)
-    _on_gpu("ckpt", ckpt.codes, d)
-    _check(_lib.muon_ckpt_load(ckpt._packed, _mat("out", out, d)))
+    _check(_lib.muon_ckpt_load(ckpt._desc(d), _mat("out", out, d)))
 
 
 def muon_ckpt_weight_grad(dy, ckpt, grads, offsets=None, rows=None, rows_per_token=1, workspace=None):
@@ -577,14 +605,13 @@ def muon_ckpt_weight_grad(dy, ckpt, grads, offsets=None, rows=None, rows_per_tok
         raise ValueError("grads: expected unit column stride")
     if n <= 1:
         ld = k
-    _on_gpu("ckpt", ckpt.codes, d)
     dy_mat = _mat("dy", dy, d)
     if grads.dtype != dy.dtype:
         raise TypeError("dy and grads differ in dtype")
     code = _codes[dy.dtype]
     if groups > 1 and offsets is None:
         raise ValueError("offsets: needed with more than one group")
-    args = (dy_mat, ckpt._packed, _MAT(grads.data_ptr(), n, k, ld, code, 1), stride, groups,
+    args = (dy_mat, ckpt._desc(d), _MAT(grads.data_ptr(), n, k, ld, code, 1), stride, groups,
             _vec("offsets", offsets, _torch.int32, (groups + 1,), d), _vec("rows", rows, _torch.int32, dy.shape[:1], d),
             rows_per_token)
     _with_scratch(muon_ckpt_weight_grad_workspace_size(code, dy.shape[0], n, k, groups), workspace, d,

@@ -584,3 +584,24 @@ def test_weight_grad_slots_of_no_token_beside_any_checkpoint(gpu_lib, dtype):
         out = out_mat(24, 200, dtype)
         mu.muon_ckpt_weight_grad(dy, ck, out[None], rows=rows)
         close(n64(out), ref[0], wgrad_tol(dtype, ref[0], mag[0], 40), f"gradient, scale byte {byte}")
+
+
+def test_checkpoint_whose_memory_was_exchanged(gpu_lib):
+    """A save, a load and a weight gradient after the tensors' memory has been exchanged use the new memory."""
+    mu, g = gpu_lib, gen(53)
+    ck, _ = saved(mu, randn(g, 20, 256))
+    held = ck.codes.data, ck.scales.data
+    before = [t.view(torch.uint8).clone() for t in held]
+    ck.codes.data, ck.scales.data = torch.zeros_like(held[0]), torch.zeros_like(held[1])
+    x = randn(g, 20, 256)
+    mu.muon_ckpt_save(x, ck)
+    assert all(torch.equal(t.view(torch.uint8), b) for t, b in zip(held, before))
+    unit, sb = T.checkpoint(n64(x))
+    back = out_mat(20, 256, F32)
+    mu.muon_ckpt_load(ck, back)
+    X = T.values(unit, sb)
+    assert np.array_equal(n64(back), X)
+    dy, out = mat(randn(g, 20, 9), F32), out_mat(9, 256, F32)
+    mu.muon_ckpt_weight_grad(dy, ck, out[None])
+    ref, mag = T.weight_grad(n64(dy), X)
+    close(n64(out), ref[0], wgrad_tol(F32, ref[0], mag[0], 20), "gradient")

@@ -236,3 +236,35 @@ def test_weight_grad_slots_that_device_counters_cannot_pass():
             assert e.value.status == SHAPE
             assert wgrad(dy=m(1, slots, 8, dtype), x=ck(64, 1, 8), g=m(65, 8, 8, dtype), groups=1, offs=None, rows=A * 66,
                          per=1) == SHAPE
+
+
+def test_checkpoint_tensors_are_its_own(monkeypatch):
+    """A call takes the memory that the checkpoint's tensors have then, and never memory that is gone (the
+    descriptor stands for a call here; every tensor says that it is on a GPU)."""
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    new = lambda rows=4, cols=200: torch.zeros((rows, cols), dtype=torch.float8_e4m3fn)  # noqa: E731
+    codes, scales = new(), torch.zeros((4, 2), dtype=torch.uint8)
+    c = mu.Checkpoint(codes, scales)
+    at = lambda: mu.muon_ckpt.from_buffer_copy(c._desc(0))  # noqa: E731
+    assert (at().codes, at().scales, at().rows, at().cols) == (codes.data_ptr(), scales.data_ptr(), 4, 200)
+    with pytest.raises(AttributeError):
+        c.codes = new()
+    with pytest.raises(AttributeError):
+        c.scales = scales.clone()
+    assert c.codes is codes and c.scales is scales and c.shape == (4, 200)
+    old, other = codes.data, new()
+    codes.data = other
+    assert at().codes == other.data_ptr() != old.data_ptr()
+    codes.data = new(4, 384)[:, :200]
+    assert at().ld_codes == 384
+    codes.data = new(3)
+    with pytest.raises(ValueError, match="scales"):
+        at()
+    codes.data = new(5)[1:]
+    assert at().codes == codes.data_ptr()
+    codes.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="freed"):
+        at()
+    scales.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="freed"):
+        at()
