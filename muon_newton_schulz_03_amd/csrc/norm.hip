@@ -83,16 +83,23 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
             ((xr[v].get(4) + xr[v].get(5)) + (xr[v].get(6) + xr[v].get(7)));
   row_sum<kTpr, 1>(s, lds, slot);
   const float mean = s[0] / float(a.cols);
-  s[0] = 0.f;
+  // the squares as a tree: one after another, each addition would be rounded against
+  // the thread's largest square, and outliers are what activations have
+  float sq[kNv];
 #pragma unroll
   for (int v = 0; v < kNv; ++v) {
     const int n = a.cols - (v * kTpr + t) * 8;
+    float d[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = xr[v].get(i) - mean;
-      if (i < n) s[0] = fmaf(d, d, s[0]);
-    }
+    for (int i = 0; i < 8; ++i) d[i] = i < n ? xr[v].get(i) - mean : 0.f;
+    sq[v] = (fmaf(d[1], d[1], d[0] * d[0]) + fmaf(d[3], d[3], d[2] * d[2])) +
+            (fmaf(d[5], d[5], d[4] * d[4]) + fmaf(d[7], d[7], d[6] * d[6]));
   }
+#pragma unroll
+  for (int w = 1; w < kNv; w *= 2)
+#pragma unroll
+    for (int v = 0; v < kNv; v += 2 * w) sq[v] += sq[v + w];
+  s[0] = sq[0];
   row_sum<kTpr, 1>(s, lds, slot);
   const float var = s[0] / float(a.cols) + a.eps, rstd = 1.f / sqrtf(var);
   // what rounding took from rstd, rstd (1 - var rstd^2) / 2 with the product in two

@@ -605,3 +605,25 @@ def test_checkpoint_whose_memory_was_exchanged(gpu_lib):
     mu.muon_ckpt_weight_grad(dy, ck, out[None])
     ref, mag = T.weight_grad(n64(dy), X)
     close(n64(out), ref[0], wgrad_tol(F32, ref[0], mag[0], 20), "gradient")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols,early,waves,runs", [(1024, 512, 1, 2), (7168, 2048, 4, 4), (32768, 8192, 16, 4)])
+def test_layernorm_variance_is_no_chain(gpu_lib, cols, early, waves, runs, dtype):
+    """Each thread's first value is 1, and its others' squares lie just under the half step that adding them to 1 one by
+    one would lose. Neighbours are negatives of each other, so the mean is 0 exactly. A tree over a run of eight and over
+    the runs, then equal sums of the lanes (doublings, exact) and of the waves in turn; a square, a division, half of that
+    in rstd, its root and reciprocal."""
+    v = torch.full((3, cols), 2.0 ** -12 * 255 / 256, device="cuda")
+    v[:, :early:8] = 1
+    v[:, 8::16] *= -1
+    for i in range(1, 8):
+        v[:, i::16] *= (-1) ** i
+        v[:, 8 + i::16] *= -(-1) ** i
+    x, y = mat(v, dtype), out_mat(3, cols, dtype)
+    mean, rstd = torch.empty(3, device="cuda"), torch.empty(3, device="cuda")
+    gpu_lib.muon_layernorm_forward(x, y, mean, rstd, eps=0.0)
+    _, _, ref = T.layernorm(n64(x), eps=0.0)
+    assert not n64(mean).any()
+    levels = 3 + int(np.log2(runs)) + waves - 1
+    close(n64(rstd), ref, ((levels + 2) / 2 + 2) * U * ref, "rstd")
