@@ -294,6 +294,9 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_bwd_kernel(const
   leave(ab, part + a.cols);
 }
 
+// A tree: added one after another, each would be rounded against the largest sum.
+__device__ inline float sum8(const float (&v)[8]) { return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])); }
+
 // Sums the workgroups' partials: 32 columns a workgroup, 8 threads a column,
 // each over every eighth partial, joined in a fixed order.
 constexpr int kRedCols = 32, kRedSlices = 8;
@@ -304,22 +307,23 @@ __global__ __launch_bounds__(kRedCols * kRedSlices) void norm_grad_kernel(const 
   float s = 0.f;
   if (c < 2 * a.cols) {
     const float *p = a.part + c;
-    int b = sl;
-    for (; b + 7 * kRedSlices < a.blocks; b += 8 * kRedSlices) {
+    for (int b = sl; b < a.blocks; b += 8 * kRedSlices) {
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = p[int64_t(b + j * kRedSlices) * 2 * a.cols];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += v[j];
+      for (int j = 0; j < 8; ++j) {
+        const int at = b + j * kRedSlices;
+        v[j] = at < a.blocks ? p[int64_t(at) * 2 * a.cols] : 0.f;
+      }
+      s += sum8(v);
     }
-    for (; b < a.blocks; b += kRedSlices) s += p[int64_t(b) * 2 * a.cols];
   }
   lds[sl][lc] = s;
   __syncthreads();
   if (sl || c >= 2 * a.cols) return;
-  s = 0.f;
+  float v[kRedSlices];
 #pragma unroll
-  for (int j = 0; j < kRedSlices; ++j) s += lds[j][lc];
+  for (int j = 0; j < kRedSlices; ++j) v[j] = lds[j][lc];
+  s = sum8(v);
   void *out = c < a.cols ? a.dw : a.db;
   const int oc = c < a.cols ? c : c - a.cols;
   if (!out) return;

@@ -627,3 +627,24 @@ def test_layernorm_variance_is_no_chain(gpu_lib, cols, early, waves, runs, dtype
     assert not n64(mean).any()
     levels = 3 + int(np.log2(runs)) + waves - 1
     close(n64(rstd), ref, ((levels + 2) / 2 + 2) * U * ref, "rstd")
+
+
+def test_layernorm_gradient_sums_are_no_chain(gpu_lib):
+    """Each slice of the workgroups' partial sums starts with a 1 and goes on with values just under the half step that
+    adding them to it one by one would lose (167 workgroups of rows b and b + 167, eight slices). A row sum, a tree over
+    eight partials, three such groups in turn, eight slices, the result."""
+    mu, g = gpu_lib, gen(54)
+    rows, cols, blocks = 333, 2047, 167
+    dy = torch.zeros((rows, cols), device="cuda")
+    dy[:blocks] = 2.0 ** -24 * 255 / 256
+    dy[:8] = 1
+    x = randn(g, rows, cols).sign()  # mean 0 and rstd 1, as passed: dweight is the same sum but for the signs
+    x[:, ::2] = 1
+    dy, x, dx = mat(dy, F32), mat(x, F32), out_mat(rows, cols, F32)
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    dw, db = out_mat(1, cols, F32), out_mat(1, cols, F32)
+    mu.muon_layernorm_backward(dy, x, mean, rstd, dx, None, dw, db)
+    _, rdw, rdb = T.layernorm_grad(n64(dy), n64(x), n64(mean), n64(rstd))
+    tol = (1 + 3 + 2 + 3 + 1) * U * np.abs(n64(dy)).sum(0)
+    close(n64(db)[0], rdb, tol, "dbias")
+    close(n64(dw)[0], rdw, tol, "dweight")
