@@ -648,3 +648,51 @@ def test_layernorm_gradient_sums_are_no_chain(gpu_lib):
     tol = (1 + 3 + 2 + 3 + 1) * U * np.abs(n64(dy)).sum(0)
     close(n64(db)[0], rdb, tol, "dbias")
     close(n64(dw)[0], rdw, tol, "dweight")
+
+
+def test_layernorm_output_is_rounded_once(gpu_lib):
+    """Outputs that differ from the exact ones as float32, rounded to bf16. One does where a border between two bf16
+    values lies between them: with borders 2^-8 to 2^-7 apart and results a quarter of a unit of 2^-24 off, that is at
+    most 2^-18 of them. (A result with three roundings, each a third of a unit off, has five times as many.)"""
+    mu, g = gpu_lib, gen(55)
+    rows, cols = 2048, 7168
+    spread = torch.exp(0.5 * randn(g, cols))
+    spread[::250] *= 20
+    x = (randn(g, rows, cols) * spread + 0.3 * randn(g, cols)).to(BF)
+    w, b = (1 + 0.2 * randn(g, 1, cols)).to(BF), (0.1 * randn(g, 1, cols)).to(BF)
+    y, rstd = torch.empty_like(x), torch.empty(rows, device="cuda")
+    mu.muon_layernorm_forward(x, y, None, rstd, w, b)
+    X = x.double()
+    var, mean = torch.var_mean(X, 1, correction=0, keepdim=True)
+    ref = (X - mean) / (var + float(np.float32(1e-5))).sqrt() * w.double() + b.double()
+    off = int((y != ref.float().to(BF)).sum())
+    assert off <= rows * cols * 2.0 ** -18, off
+    # half a unit for its own rounding, a quarter as above
+    close(n64(rstd), 1 / np.sqrt(n64(var)[:, 0] + float(np.float32(1e-5))), 0.75 * 2 * U * n64(rstd), "rstd")
+
+
+@pytest.mark.parametrize("wdtype", [BF, F32])
+def test_layernorm_infinite_weight_and_bias(gpu_lib, wdtype):
+    """An infinite weight makes its column infinite, with the sign of x - mean, and no other."""
+    mu, g = gpu_lib, gen(56)
+    x = mat(randn(g, 5, 300), F32)
+    w, b = mat(torch.ones((1, 300), device="cuda"), wdtype), mat(torch.zeros((1, 300), device="cuda"), wdtype)
+    w[0, 3], w[0, 4], w[0, 5], b[0, 6], b[0, 7] = float("inf"), -float("inf"), float("nan"), -float("inf"), float("nan")
+    y, z = out_mat(5, 300, F32), out_mat(5, 300, F32)
+    mu.muon_layernorm_forward(x, y, weight=w, bias=b)
+    mu.muon_layernorm_forward(x, z)
+    inf = torch.full((5,), float("inf"), device="cuda")
+    assert torch.equal(y[:, 3], torch.copysign(inf, z[:, 3])) and torch.equal(y[:, 4], torch.copysign(inf, -z[:, 4]))
+    assert bool(torch.isnan(y[:, 5]).all()) and torch.equal(y[:, 6], -inf) and bool(torch.isnan(y[:, 7]).all())
+    assert torch.equal(y[:, 8:], z[:, 8:]) and torch.equal(y[:, :3], z[:, :3])
+
+
+@pytest.mark.parametrize("cols", [1, 7, 300, 7168, 20000])
+def test_layernorm_of_equal_values(gpu_lib, cols):
+    """A row of equal bf16 values has their mean exactly, variance 0 and the bias as its output."""
+    v = torch.tensor([[0.0], [1.0], [-0.1], [300.0], [3e-5]], device="cuda").to(BF)
+    x, b = mat(v.expand(5, cols), BF), mat(randn(gen(57), 1, cols), BF)
+    y, mean, rstd = out_mat(5, cols, BF), torch.empty(5, device="cuda"), torch.empty(5, device="cuda")
+    gpu_lib.muon_layernorm_forward(x, y, mean, rstd, None, b, eps=2.0 ** -16)
+    assert torch.equal(mean, v[:, 0].float()) and bool((rstd == 256).all())
+    assert torch.equal(y, b.expand(5, cols))
