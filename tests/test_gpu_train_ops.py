@@ -696,3 +696,86 @@ def test_layernorm_of_equal_values(gpu_lib, cols):
     gpu_lib.muon_layernorm_forward(x, y, mean, rstd, None, b, eps=2.0 ** -16)
     assert torch.equal(mean, v[:, 0].float()) and bool((rstd == 256).all())
     assert torch.equal(y, b.expand(5, cols))
+
+
+def check_groups(mu, dy, ck, X, out, offsets=None, rows=None, topk=1):
+    """All elements of the groups' gradients against 64-bit products on the GPU."""
+    X = torch.from_numpy(X).cuda()
+    ends = [0, dy.shape[0]] if offsets is None else offsets.tolist()
+    for i in range(len(ends) - 1):
+        s = torch.arange(ends[i], ends[i + 1], device="cuda")
+        x = X[torch.div(s if rows is None else rows[s].long(), topk, rounding_mode="floor")]
+        d = dy[s].double()
+        ref, mag = torch.mm(d.t(), x), torch.mm(d.abs().t(), x.abs())
+        tol = HALF[dy.dtype] * ref.abs() + (len(s) / 4 + 40) * U * mag  # as wgrad_tol
+        bad = ~((out[i].double() - ref).abs() <= tol)
+        assert not bool(bad.any()), f"group {i} of {len(s)} slots: {int(bad.sum())} off"
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("listed", [False, True])
+def test_weight_grad_of_long_sums_into_many_tiles(gpu_lib, listed, dtype):
+    """One group of 1000 slots into 17 x 17 tiles: four waves a tile and no partial sums, with and without a list."""
+    mu, g = gpu_lib, gen(61)
+    slots, n, k = 1000, 2050, 4100
+    assert mu.muon_ckpt_weight_grad_workspace_size(mu.MUON_F32 if dtype == F32 else mu.MUON_BF16, slots, n, k) == 0
+    ck, X = saved(mu, randn(g, slots, k) * torch.exp(randn(g, 1, k)))
+    dy, out = mat(randn(g, slots, n, scale=1e-3), dtype, 3), out_mat(n, k, dtype)
+    rows = torch.randperm(slots, generator=g, device="cuda").to(torch.int32) if listed else None
+    mu.muon_ckpt_weight_grad(dy, ck, out[None], rows=rows)
+    check_groups(mu, dy, ck, X, out[None], rows=rows)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,k,counts,ordered", [(1030, 2570, [1100, 31, 1300], False),
+                                                (2050, 1300, [2500, 0, 33, 900, 1200, 700], True)])
+def test_weight_grad_of_long_uneven_groups(gpu_lib, n, k, counts, ordered, dtype):
+    """768 slots a group and more on average: four waves a tile and no partial sums, in the given order and the longest first."""
+    mu, g = gpu_lib, gen(62)
+    slots, topk = sum(counts), 3
+    tokens = -(-slots // topk)
+    size = mu.muon_ckpt_weight_grad_workspace_size(mu.MUON_F32 if dtype == F32 else mu.MUON_BF16, slots, n, k, len(counts))
+    assert size == (16 * len(counts) if ordered else 0)
+    ck, X = saved(mu, randn(g, tokens, k))
+    rows = torch.randperm(tokens * topk, generator=g, device="cuda")[:slots].to(torch.int32)
+    offsets = torch.tensor(np.append(0, np.cumsum(counts)), dtype=torch.int32, device="cuda")
+    dy, out = mat(randn(g, slots, n, scale=1e-3), dtype), out_mat(len(counts) * n, k, dtype)
+    mu.muon_ckpt_weight_grad(dy, ck, out.view(len(counts), n, k), offsets, rows, topk)
+    check_groups(mu, dy, ck, X, out.view(len(counts), n, k), offsets, rows, topk)
+
+
+@pytest.mark.parametrize("dtype,wdtype", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("rows,cols,extra", [(515, 9000, 0), (700, 12287, 1), (520, 20001, 3), (515, 32768, 0)])
+def test_layernorm_wide_rows_of_several_to_a_workgroup(gpu_lib, rows, cols, extra, dtype, wdtype):
+    test_layernorm(gpu_lib, rows, cols, extra, dtype, wdtype)
+
+
+def test_buffers_that_interleave_without_overlap(gpu_lib):
+    """Operands whose rows lie between each other's are no overlap; one byte further they are."""
+    mu, g = gpu_lib, gen(63)
+    rows, cols = 37, 300
+    wide = torch.zeros((rows, 2 * cols), dtype=BF, device="cuda")
+    x, y = wide[:, :cols], wide[:, cols:]
+    x.copy_(randn(g, rows, cols))
+    want = torch.empty((rows, cols), dtype=BF, device="cuda")
+    mu.muon_layernorm_forward(x.clone(), want)
+    before = x.clone()
+    mu.muon_layernorm_forward(x, y)
+    assert torch.equal(y, want) and torch.equal(x, before)
+    with pytest.raises(mu.MuonError) as e:
+        mu.muon_layernorm_forward(x, wide[:, cols - 1:2 * cols - 1])
+    assert e.value.status == mu.MUON_ERR_ALIAS
+    # a row of values, then its codes, then its scales
+    buf = torch.zeros((rows, 3 * cols + 4), dtype=torch.uint8, device="cuda")
+    v = buf.view(BF)[:, :cols]
+    v.copy_(randn(g, rows, cols))
+    kept = v.clone()
+    ck = mu.Checkpoint(buf[:, 2 * cols:3 * cols].view(torch.float8_e4m3fn), buf[:, 3 * cols:3 * cols + 3])
+    mu.muon_ckpt_save(v, ck)
+    other = mu.Checkpoint.empty(rows, cols)
+    mu.muon_ckpt_save(kept, other)
+    assert torch.equal(v, kept) and torch.equal(ck.scales, other.scales) and not bool(buf[:, 3 * cols + 3].any())
+    assert torch.equal(ck.codes.view(torch.uint8), other.codes.view(torch.uint8))
+    with pytest.raises(mu.MuonError) as e:
+        mu.muon_ckpt_save(v, mu.Checkpoint(buf[:, 2 * cols - 1:3 * cols - 1].view(torch.float8_e4m3fn), buf[:, 3 * cols:3 * cols + 3]))
+    assert e.value.status == mu.MUON_ERR_ALIAS
