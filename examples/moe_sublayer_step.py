@@ -53,6 +53,7 @@ class MoeSublayer:
         self.rows = torch.empty(tokens * topk, **i32)
         self.balance = torch.empty(1, device="cuda")
         self.dexperts = torch.empty_like(self.experts)
+        self.drouter = torch.empty((1, experts, width), dtype=bf, device="cuda")
         self.dlogits = torch.empty((tokens, experts), dtype=f32, device="cuda")
         self.dnorm = [torch.empty_like(w) for w in self.norm]
         self.dx = torch.empty((tokens, width), dtype=bf, device="cuda")
@@ -87,8 +88,7 @@ class MoeSublayer:
         mu.muon_route_backward(logits, self.choice, self.counts, self.dlogits, dweights=dshare.view_as(self.share),
                                dloss=torch.ones(1, device="cuda"))
         dlogits = self.dlogits.to(torch.bfloat16)
-        drouter = torch.empty((1, *self.router.shape), dtype=torch.bfloat16, device="cuda")
-        mu.muon_ckpt_weight_grad(dlogits, self.ckpt, drouter)
+        mu.muon_ckpt_weight_grad(dlogits, self.ckpt, self.drouter)
         dy = (dlogits @ self.router).float()
         for e, w in enumerate(self.experts):
             if ends[e + 1] > ends[e]:
@@ -97,7 +97,7 @@ class MoeSublayer:
 
         # update
         self.steps += 1
-        mu.muon_step(self.matrices(), [*self.dexperts.unbind(0), drouter[0]], self.moms, lr=lr)
+        mu.muon_step(self.matrices(), [*self.dexperts.unbind(0), self.drouter[0]], self.moms, lr=lr)
         mu.muon_adamw_step(self.norm, self.dnorm, *self.adam, lr=norm_lr, step=self.steps)
         return error, self.balance.clone(), self.counts
 

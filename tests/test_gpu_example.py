@@ -46,3 +46,29 @@ def test_error_falls(gpu_lib):
     import moe_sublayer_step as ex
     errors = ex.main(tokens=1024, width=256, out=128, experts=8, topk=2, steps=12, quiet=True)
     assert errors[-1] < 0.8 * errors[0], errors
+
+
+def test_router_gradient_of_one_step(gpu_lib):
+    """The router's weight gradient, which takes the balance loss, the gate weights and the checkpoint together."""
+    import moe_sublayer_step as ex
+    tokens, width, out, experts, topk = 192, 128, 64, 8, 3
+    layer = ex.MoeSublayer(tokens, width, out, experts, topk, seed=5)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    x = torch.randn((tokens, width), generator=g, device="cuda").to(torch.bfloat16)
+    target = torch.randn((tokens, out), generator=g, device="cuda")
+    xl, we, gain, shift = [t.float().cpu() for t in (x, layer.experts, *layer.norm)]
+    router = layer.router.float().cpu().requires_grad_()
+    _, _, counts = layer.step(x, target)
+    y = torch.nn.functional.layer_norm(xl, (width,), gain[0], shift[0])
+    p = torch.softmax(y @ router.t(), 1)
+    idx = layer.choice.long().cpu()
+    w = torch.gather(p, 1, idx)
+    w = w / w.sum(1, keepdim=True)
+    z = (torch.stack([y @ e.t() for e in we], 1)[torch.arange(tokens)[:, None], idx] * w[:, :, None]).sum(1)
+    n = counts[:experts].float().cpu()
+    loss = (z - target.cpu()).square().mean() + 1e-2 * experts / (topk * tokens) * (n * p.sum(0) / tokens).sum()
+    loss.backward()
+    # e4m3 checkpoints, 2^-4 a value, as for the experts
+    rel = float((layer.drouter[0].float().cpu() - router.grad).norm() / router.grad.norm())
+    assert rel <= 2.0 ** -4, rel
