@@ -63,9 +63,17 @@ struct Span {
   uintptr_t end() const { return at + uintptr_t((rows - 1) * pitch + bytes); }
 };
 
-// Whether two buffers share a byte: the rows of one against the rows of the
-// other that each can reach. Only asked where their extents meet.
+// Whether two buffers share a byte. Only asked where their extents meet. With one
+// pitch, as the parts of a wide buffer have, the rows' distances are multiples of
+// it: the first that brings a's row past the start of b's decides. Else the rows
+// of one against the row of the other that each can reach.
 bool meet(const Span &a, const Span &b) {
+  if (a.rows > 1 && b.rows > 1 && a.pitch == b.pitch) {
+    const int64_t d = int64_t(a.at - b.at), over = -a.bytes - d;  // d + k * pitch > -a.bytes
+    int64_t k = over / a.pitch - (over % a.pitch < 0 ? 1 : 0) + 1;
+    if (k < 1 - b.rows) k = 1 - b.rows;
+    return k < a.rows && d + k * a.pitch < b.bytes;
+  }
   for (int64_t r = 0; r < a.rows; ++r) {
     const int64_t lo = int64_t(a.at - b.at) + r * a.pitch, hi = lo + a.bytes;  // against b's start
     if (hi <= 0) continue;

@@ -3,6 +3,8 @@ rejected on the host with the documented status before anything is launched
 (addresses here are fake and never dereferenced), the workspace sizes, and
 the binding's checks of tensors."""
 import ctypes
+import random
+import time
 
 import pytest
 import torch
@@ -268,3 +270,42 @@ def test_checkpoint_tensors_are_its_own(monkeypatch):
     scales.untyped_storage().resize_(0)
     with pytest.raises(ValueError, match="freed"):
         at()
+
+
+def x_meets_y(x, y):
+    """Whether the overlap check finds x and y to share a byte: the statistics overlap too, so that every call is refused."""
+    assert fwd(x=x, y=y, mean=A * 80, rstd=A * 80, w=None, b=None) == ALIAS
+    text = mu.muon_last_error()
+    assert text in ("x and y overlap", "mean and rstd overlap")
+    return text == "x and y overlap"
+
+
+def test_overlap_check_against_every_byte():
+    r = random.Random(0)
+    seen = [0, 0]
+    for _ in range(4000):
+        rows, cols = r.randint(1, 6), r.randint(1, 9)
+        ld = [cols + r.randint(0, 14) for _ in range(2)]
+        if r.random() < 0.6:
+            ld[1] = ld[0]
+        at = 2 * r.randint(-60, 60)
+        x, y = m(40, rows, cols, ld=ld[0]), mu.muon_mat(A * 40 + at, rows, cols, ld[1], BF, 1)
+        mine = {2 * (i * ld[0] + j) + b for i in range(rows) for j in range(cols) for b in range(2)}
+        other = {at + 2 * (i * ld[1] + j) + b for i in range(rows) for j in range(cols) for b in range(2)}
+        shared = not mine.isdisjoint(other)
+        assert x_meets_y(x, y) == shared, (rows, cols, ld, at)
+        seen[shared] += 1
+    assert min(seen) > 500
+
+
+def test_overlap_check_of_many_interleaved_rows():
+    """Two halves of a wide buffer, 2^30 rows: found apart (or a byte into each other) without a walk over the rows."""
+    start = time.perf_counter()
+    x = m(40, 1 << 30, 4, ld=8)
+    assert not x_meets_y(x, mu.muon_mat(A * 40 + 8, 1 << 30, 4, 8, BF, 1))
+    assert x_meets_y(x, mu.muon_mat(A * 40 + 6, 1 << 30, 4, 8, BF, 1))
+    # the last row of x under the first of y
+    far = ((1 << 30) - 1) * 16
+    assert x_meets_y(x, mu.muon_mat(A * 40 + far, 1 << 30, 4, 8, BF, 1))
+    assert not x_meets_y(x, mu.muon_mat(A * 40 + far + 8, 1 << 30, 4, 8, BF, 1))
+    assert time.perf_counter() - start < 0.5
