@@ -6,11 +6,8 @@
 //   dw = sum over rows of dy xh,  db = sum over rows of dy.
 //
 // Both passes are bound by memory: each element is read once into registers,
-// where a row's sums are taken (centred), and written once. A row belongs to one
-// wave (up to 1024 columns) or one workgroup. The forward pass takes the variance
-// and the output in 64 bits, in units that memory leaves idle: of 8192x7168 outputs
-// that go into 8-bit checkpoints 5 then differ from the exact ones rounded (in
-// float32 1200), for 0.3 us. Measured, bf16:
+// where a row's sums are taken (centred, in float32), and written once. A
+// row belongs to one wave (up to 1024 columns) or one workgroup. Measured, bf16:
 // forward with checkpoint 8192x7168 62 us (4.7 TB/s), backward 16384x7168 135 us
 // with the launch that adds the workgroups' partial sums (5.2 TB/s; a copy of
 // 1 GiB runs at 5.0). A backward pass of 333x2047 float32 is 7 + 3 us of two
@@ -61,45 +58,11 @@ __device__ inline void row_sum(float (&v)[kN], float *lds, int &slot) {
   }
 }
 
-// The same for one value in 64 bits.
-__device__ inline double join64(uint32_t lo, uint32_t hi) { return __builtin_bit_cast(double, uint64_t(lo) | uint64_t(hi) << 32); }
-template <int kCtrl>
-__device__ inline double dpp64(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  return join64(dpp<kCtrl>(uint32_t(u)), dpp<kCtrl>(uint32_t(u >> 32)));
-}
-template <typename F>
-__device__ inline double pair_sum64(double v, F &&swap) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const auto lo = swap(uint32_t(u)), hi = swap(uint32_t(u >> 32));
-  return join64(lo[0], hi[0]) + join64(lo[1], hi[1]);
-}
-template <int kTpr>
-__device__ inline double row_sum64(double v, double *lds, int &slot) {
-  v += dpp64<kQuadSwap1>(v);
-  v += dpp64<kQuadSwap2>(v);
-  v += dpp64<kHalfMirror>(v);
-  v += dpp64<kMirror>(v);
-  v = pair_sum64(v, [](uint32_t w) { return __builtin_amdgcn_permlane16_swap(w, w, false, false); });
-  v = pair_sum64(v, [](uint32_t w) { return __builtin_amdgcn_permlane32_swap(w, w, false, false); });
-  if constexpr (kTpr > 64) {
-    constexpr int kWaves = kTpr / 64;
-    double *area = lds + slot * kWaves;
-    slot ^= 1;
-    if ((threadIdx.x & 63) == 0) area[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += area[w];
-  }
-  return v;
-}
-
 // kTpr threads a row, kNv runs of 8 columns a thread.
 template <typename T, bool kWf32, bool kCkpt, bool kWhole, int kTpr, int kNv>
 __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const NormFwdArgs a) {
   constexpr int kBlock = kTpr < 256 ? 256 : kTpr;
-  __shared__ double lds[2 * (kTpr / 64)];
+  __shared__ float lds[2 * (kTpr / 64)];
   using W = std::conditional_t<kWf32, float, __bf16>;
   int slot = 0;
   const int t = int(threadIdx.x) % kTpr;
@@ -108,7 +71,7 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
   const T *x = static_cast<const T *>(a.x) + row * a.ld_x;
   T *y = static_cast<T *>(a.y) + row * a.ld_y;
   Raw8<T> xr[kNv];
-  float s = 0.f;
+  float s[1] = {0.f};
 #pragma unroll
   for (int v = 0; v < kNv; ++v) {
     const int c = (v * kTpr + t) * 8;
@@ -116,73 +79,60 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
   }
 #pragma unroll
   for (int v = 0; v < kNv; ++v)
-    s += ((xr[v].get(0) + xr[v].get(1)) + (xr[v].get(2) + xr[v].get(3))) +
-         ((xr[v].get(4) + xr[v].get(5)) + (xr[v].get(6) + xr[v].get(7)));
-  // The weight and bias are in flight while the row is summed, where registers are
-  // left for them (1024 threads of 32 columns would spill).
-  constexpr int kHeld = kTpr * kNv < 4096 ? kNv : 1;
-  Raw8<W> w[kHeld], b[kHeld];
-  auto load_channel = [&](int v) {
-    const int c = (v * kTpr + t) * 8, n = a.cols - c, at = kHeld == kNv ? v : 0;
-    const float one[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-    w[at] = pack8(one, W());
-    b[at] = {};
-    if (a.w) w[at] = load_run<kWhole>(static_cast<const W *>(a.w) + c, n);
-    if (a.b) b[at] = load_run<kWhole>(static_cast<const W *>(a.b) + c, n);
-  };
-  if constexpr (kHeld == kNv) {
-#pragma unroll
-    for (int v = 0; v < kNv; ++v) load_channel(v);
-  }
-  const double sum = row_sum64<kTpr>(s, lds, slot), q = sum * a.inv_cols;
-  const double q_lo = fma(-q, double(a.cols), sum) * a.inv_cols;  // a row of equal values has their mean
-  const double mean64 = q_lo == q_lo ? q + q_lo : q;
-  // the squares in 64 bits: outliers are what activations have, and a few of them
-  // decide what the roundings of a float32 sum come to
-  double sq[kNv];
+    s[0] += ((xr[v].get(0) + xr[v].get(1)) + (xr[v].get(2) + xr[v].get(3))) +
+            ((xr[v].get(4) + xr[v].get(5)) + (xr[v].get(6) + xr[v].get(7)));
+  row_sum<kTpr, 1>(s, lds, slot);
+  const float mean = s[0] / float(a.cols);
+  // the squares as a tree: one after another, each addition would be rounded against
+  // the thread's largest square, and outliers are what activations have
+  float sq[kNv];
 #pragma unroll
   for (int v = 0; v < kNv; ++v) {
     const int n = a.cols - (v * kTpr + t) * 8;
-    sq[v] = 0.;
-    if (n <= 0) continue;
+    float d[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double d = double(xr[v].get(i)) - mean64;
-      if (kWhole || i < n) sq[v] = fma(d, d, sq[v]);
-    }
+    for (int i = 0; i < 8; ++i) d[i] = i < n ? xr[v].get(i) - mean : 0.f;
+    sq[v] = (fmaf(d[1], d[1], d[0] * d[0]) + fmaf(d[3], d[3], d[2] * d[2])) +
+            (fmaf(d[5], d[5], d[4] * d[4]) + fmaf(d[7], d[7], d[6] * d[6]));
   }
 #pragma unroll
-  for (int v = 1; v < kNv; ++v) sq[0] += sq[v];
-  const double var = row_sum64<kTpr>(sq[0], lds, slot) * a.inv_cols + double(a.eps);
-  const float r = 1.f / sqrtf(float(var));
-  double rstd = r;  // and a Newton step, where that is a finite number
-  if (r > 0.f && r < 1e30f) rstd += 0.5 * rstd * (1. - var * rstd * rstd);
+  for (int w = 1; w < kNv; w *= 2)
+#pragma unroll
+    for (int v = 0; v < kNv; v += 2 * w) sq[v] += sq[v + w];
+  s[0] = sq[0];
+  row_sum<kTpr, 1>(s, lds, slot);
+  const float var = s[0] / float(a.cols) + a.eps, rstd = 1.f / sqrtf(var);
+  // what rounding took from rstd, rstd (1 - var rstd^2) / 2 with the product in two
+  // parts: where y is kept in 8 bits, the last bit of y decides a code
+  const float vr = var * rstd;
+  float rest = 0.5f * rstd * (fmaf(-vr, rstd, 1.f) - fmaf(var, rstd, -vr) * rstd);
+  rest = rstd > 0.f && rstd < 1e30f ? rest : 0.f;
   if (t == 0) {
-    if (a.mean) a.mean[row] = float(mean64);
-    if (a.rstd) a.rstd[row] = float(rstd);
+    if (a.mean) a.mean[row] = mean;
+    if (a.rstd) a.rstd[row] = rstd + rest;
   }
 #pragma unroll
   for (int v = 0; v < kNv; ++v) {
     const int c = (v * kTpr + t) * 8, n = a.cols - c;
-    if (kCkpt ? !__any(n > 0) : n <= 0) break;
-    if constexpr (kHeld != kNv) load_channel(v);
-    const Raw8<W> &wv = w[kHeld == kNv ? v : 0], &bv = b[kHeld == kNv ? v : 0];
+    if (!kCkpt && n <= 0) break;
     float f[8];
-    // To float32, then to T, as two steps: the compiler may make one of them, which
-    // rounds ties of the second differently and takes more instructions.
+    const float one[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    Raw8<W> w = pack8(one, W()), b{};
+    if (a.w) w = load_run<kWhole>(static_cast<const W *>(a.w) + c, n);
+    if (a.b) b = load_run<kWhole>(static_cast<const W *>(a.b) + c, n);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-#pragma clang fp contract(off)
-      f[i] = float(fma((double(xr[v].get(i)) - mean64) * rstd, double(wv.get(i)), double(bv.get(i))));
+      const float d = xr[v].get(i) - mean;
+      f[i] = fmaf(fmaf(d, rest, d * rstd), w.get(i), b.get(i));
     }
-    const Raw8<T> yr = pack8(f, T());
-    if (n > 0) store_run<kWhole>(y + c, yr, n);
+    const Raw8<T> r = pack8(f, T());
+    if (n > 0) store_run<kWhole>(y + c, r, n);
     if constexpr (kCkpt) {
       // the checkpoint of y as stored; its groups of 128 columns are 16 lanes
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        f[i] = (kWhole ? n > 0 : i < n) ? yr.get(i) : 0.f;
+        f[i] = i < n ? r.get(i) : 0.f;
         m = max(m, finite_mag(f[i]));
       }
       const uint32_t sb = scale_byte(row16_max(m));
