@@ -317,7 +317,8 @@ muon_status muon_place(const double *costs, int32_t n_mats, int32_t ranks, uint3
  *   - Matrices may have no rows (their data may then be NULL); outputs that
  *     sum over rows are then written as zeros.
  *   - Any pitch and any alignment to the element size run the same kernels.
- *   - Sums, statistics and softmax are float32; each result is rounded once.
+ *   - Sums, statistics and softmax are float32 (64 bits where noted at a
+ *     kernel); each result is rounded once from float32.
  *     The order of every sum is fixed: the same inputs give the same bits.
  *   - An operand named NULL-able may be NULL where its comment says so.
  *   - Their launches are not recorded by muon_set_phase_timing.

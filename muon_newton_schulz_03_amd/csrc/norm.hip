@@ -7,7 +7,11 @@
 //
 // Both passes are bound by memory: each element is read once into registers,
 // where a row's sums are taken (centred, in float32), and written once. A
-// row belongs to one wave (up to 1024 columns) or one workgroup. Measured, bf16:
+// row belongs to one wave (up to 1024 columns) or one workgroup. The forward pass
+// ends the variance's sum in 64 bits and computes what lies near a border of the
+// 8-bit codes again in 64 bits: of 8192x7168 codes 20 to 30 then differ from those
+// of the exact output (in float32 alone 50), at no cost from memory and 2 us of 38
+// where the activations are in the cache. Measured, bf16:
 // forward with checkpoint 8192x7168 62 us (4.7 TB/s), backward 16384x7168 135 us
 // with the launch that adds the workgroups' partial sums (5.2 TB/s; a copy of
 // 1 GiB runs at 5.0). A backward pass of 333x2047 float32 is 7 + 3 us of two
@@ -58,11 +62,50 @@ __device__ inline void row_sum(float (&v)[kN], float *lds, int &slot) {
   }
 }
 
+// The sum over the kTpr threads of a row, the last two levels of a wave and the
+// waves in 64 bits: their few roundings are half of what such a sum is off by.
+__device__ inline double join64(uint32_t lo, uint32_t hi) { return __builtin_bit_cast(double, uint64_t(lo) | uint64_t(hi) << 32); }
+template <int kTpr>
+__device__ inline double row_sum64(float v, double *lds) {
+  v += dpp<kQuadSwap1>(v);
+  v += dpp<kQuadSwap2>(v);
+  v += dpp<kHalfMirror>(v);
+  v += dpp<kMirror>(v);
+  const Pair p = rows_16(v);
+  const uint64_t u = __builtin_bit_cast(uint64_t, double(p.a) + double(p.b));
+  const auto lo = __builtin_amdgcn_permlane32_swap(uint32_t(u), uint32_t(u), false, false);
+  const auto hi = __builtin_amdgcn_permlane32_swap(uint32_t(u >> 32), uint32_t(u >> 32), false, false);
+  double s = join64(lo[0], hi[0]) + join64(lo[1], hi[1]);
+  if constexpr (kTpr > 64) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = 0.;
+#pragma unroll
+    for (int w = 0; w < kTpr / 64; ++w) s += lds[w];
+  }
+  return s;
+}
+
+// At most 2 kSlack where a result lies within kSlack units of its last bit of a border
+// that decides its 8-bit code: the middle between two codes has its low 20 bits at
+// 0x80000; bf16 results become that middle, or pass it, half a bf16 step to its sides.
+// (Codes below 2^-6 of their scale have fewer bits and other middles. They are a
+// step of the smallest off, at most.)
+constexpr uint32_t kSlack = 4;
+template <typename T>
+__device__ inline uint32_t border(float f) {
+  if constexpr (sizeof(T) == 2)
+    return (f32_bits(f) + kSlack - 0x78000u) & 0xeffffu;
+  else
+    return (f32_bits(f) + kSlack - 0x80000u) & 0xfffffu;
+}
+
 // kTpr threads a row, kNv runs of 8 columns a thread.
 template <typename T, bool kWf32, bool kCkpt, bool kWhole, int kTpr, int kNv>
 __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const NormFwdArgs a) {
   constexpr int kBlock = kTpr < 256 ? 256 : kTpr;
   __shared__ float lds[2 * (kTpr / 64)];
+  __shared__ double lds64[kTpr / 64];
   using W = std::conditional_t<kWf32, float, __bf16>;
   int slot = 0;
   const int t = int(threadIdx.x) % kTpr;
@@ -89,9 +132,11 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
 #pragma unroll
   for (int v = 0; v < kNv; ++v) {
     const int n = a.cols - (v * kTpr + t) * 8;
+    sq[v] = 0.f;
+    if (n <= 0) continue;
     float d[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] = i < n ? xr[v].get(i) - mean : 0.f;
+    for (int i = 0; i < 8; ++i) d[i] = kWhole || i < n ? xr[v].get(i) - mean : 0.f;
     sq[v] = (fmaf(d[1], d[1], d[0] * d[0]) + fmaf(d[3], d[3], d[2] * d[2])) +
             (fmaf(d[5], d[5], d[4] * d[4]) + fmaf(d[7], d[7], d[6] * d[6]));
   }
@@ -99,13 +144,10 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
   for (int w = 1; w < kNv; w *= 2)
 #pragma unroll
     for (int v = 0; v < kNv; v += 2 * w) sq[v] += sq[v + w];
-  s[0] = sq[0];
-  row_sum<kTpr, 1>(s, lds, slot);
-  const float var = s[0] / float(a.cols) + a.eps, rstd = 1.f / sqrtf(var);
-  // what rounding took from rstd, rstd (1 - var rstd^2) / 2 with the product in two
-  // parts: where y is kept in 8 bits, the last bit of y decides a code
-  const float vr = var * rstd;
-  float rest = 0.5f * rstd * (fmaf(-vr, rstd, 1.f) - fmaf(var, rstd, -vr) * rstd);
+  const double var = row_sum64<kTpr>(sq[0], lds64) * a.inv_cols + double(a.eps);
+  const float rstd = 1.f / sqrtf(float(var));
+  const double r64 = rstd;
+  float rest = float(0.5 * r64 * (1. - var * r64 * r64));
   rest = rstd > 0.f && rstd < 1e30f ? rest : 0.f;
   if (t == 0) {
     if (a.mean) a.mean[row] = mean;
@@ -114,16 +156,32 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
 #pragma unroll
   for (int v = 0; v < kNv; ++v) {
     const int c = (v * kTpr + t) * 8, n = a.cols - c;
-    if (!kCkpt && n <= 0) break;
+    if (kCkpt ? !__any(n > 0) : n <= 0) break;
     float f[8];
     const float one[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
     Raw8<W> w = pack8(one, W()), b{};
     if (a.w) w = load_run<kWhole>(static_cast<const W *>(a.w) + c, n);
     if (a.b) b = load_run<kWhole>(static_cast<const W *>(a.b) + c, n);
+    // In float32, and the runs with a value near a border again in 64 bits: one in a
+    // hundred of a wave's. (As two steps, to float32 and then to T: the compiler may
+    // make one of them, which rounds other ties of the second.) Not above 16384
+    // columns, where the registers for it leave one workgroup a CU (without a
+    // checkpoint 2048x32768 59 us, 48 so).
+    constexpr bool kAgain = kTpr * kNv <= 2048;
+    uint32_t near = ~0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float d = xr[v].get(i) - mean;
       f[i] = fmaf(fmaf(d, rest, d * rstd), w.get(i), b.get(i));
+      near = min(near, border<T>(f[i]));
+    }
+    if (kAgain && near <= 2 * kSlack) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma clang fp contract(off)
+        __builtin_amdgcn_sched_barrier(0);  // one after another: few registers, and it is rare
+        f[i] = float(fma((double(xr[v].get(i)) - double(mean)) * (r64 + double(rest)), double(w.get(i)), double(b.get(i))));
+      }
     }
     const Raw8<T> r = pack8(f, T());
     if (n > 0) store_run<kWhole>(y + c, r, n);
@@ -132,7 +190,7 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_fwd_kernel(const
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        f[i] = i < n ? r.get(i) : 0.f;
+        f[i] = (kWhole ? n > 0 : i < n) ? r.get(i) : 0.f;
         m = max(m, finite_mag(f[i]));
       }
       const uint32_t sb = scale_byte(row16_max(m));

@@ -35,6 +35,7 @@ struct NormFwdArgs {
   int32_t cols;
   int32_t w_f32;      // w and b are float32 (else bf16)
   float eps;
+  double inv_cols;    // 1 / cols
   CkptView ck;
 };
 

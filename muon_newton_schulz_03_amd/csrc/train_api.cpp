@@ -254,6 +254,7 @@ muon_status muon_layernorm_forward(const muon_mat *x, const muon_mat *y, float *
     a.cols = int32_t(x->cols);
     a.w_f32 = wt == MUON_F32;
     a.eps = eps;
+    a.inv_cols = 1. / double(a.cols);
     launched(launch_norm_fwd(a, x->dtype == MUON_BF16, st.stream), "layer norm launch");
   });
 }

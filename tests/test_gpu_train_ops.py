@@ -758,3 +758,29 @@ def test_buffers_that_interleave_without_overlap(gpu_lib):
     with pytest.raises(mu.MuonError) as e:
         mu.muon_ckpt_save(v, mu.Checkpoint(buf[:, 2 * cols - 1:3 * cols - 1].view(torch.float8_e4m3fn), buf[:, 3 * cols:3 * cols + 3]))
     assert e.value.status == mu.MUON_ERR_ALIAS
+
+
+def test_layernorm_codes_near_their_borders(gpu_lib):
+    """8-bit codes of the output that differ from those of the exact output (in 64 bits, as float32, rounded to bf16). One
+    does where a border between two codes lies between both: borders are 2^-4 to 2^-3 apart, so that a result a quarter
+    of a unit of 2^-24 off passes one in 2^-22 of cases; and where such a result rounds to another float32 value, a
+    quarter of cases, one of 2^20 patterns decides on either side, 2^-21. A result with three float32 roundings is off by
+    half a unit or more, and has twice as many."""
+    mu, g = gpu_lib, gen(58)
+    rows, cols = 8192, 7168
+    spread = torch.exp(0.5 * randn(g, cols))
+    spread[::250] *= 20
+    x = (randn(g, rows, cols) * spread + 0.3 * randn(g, cols)).to(BF)
+    w, b = (1 + 0.2 * randn(g, 1, cols)).to(BF), (0.1 * randn(g, 1, cols)).to(BF)
+    y, ck, want = torch.empty_like(x), mu.Checkpoint.empty(rows, cols), mu.Checkpoint.empty(rows, cols)
+    mu.muon_layernorm_forward(x, y, None, None, w, b, ckpt=ck)
+    X = x.double()
+    var, mean = torch.var_mean(X, 1, correction=0, keepdim=True)
+    ref = (X - mean) / (var + float(np.float32(1e-5))).sqrt() * w.double() + b.double()
+    mu.muon_ckpt_save(ref.float().to(BF), want)
+    off = int((ck.codes.view(torch.uint8) != want.codes.view(torch.uint8)).sum())
+    assert off <= rows * cols * (2.0 ** -22 + 2.0 ** -21), off
+    # the same bits without a checkpoint
+    z = torch.empty_like(y)
+    mu.muon_layernorm_forward(x, z, None, None, w, b)
+    assert torch.equal(y, z)
