@@ -391,7 +391,8 @@ muon_status muon_ckpt_load(const muon_ckpt *ckpt, const muon_mat *out);
  *   dy[s, n] * x[rows[s] / rows_per_token, k].
  *   dy        slots x n, in slot order, slots <= 2^31 - 2^22; bf16 (products
  *             of bf16 values with float32 sums) or float32 (products exact in
- *             float32).
+ *             float32, but for what of dy lies below 2^-133; where x is 2^128,
+ *             see muon_ckpt_load, the sum may be NaN).
  *   x         tokens x k.
  *   grads     descriptor of the first group's n x k gradient, dy's dtype;
  *             group g's lies g * group_stride elements further. Overwritten;

@@ -10,12 +10,17 @@
 // row belongs to one wave (up to 1024 columns) or one workgroup. The forward pass
 // ends the variance's sum in 64 bits and computes what lies near a border of the
 // 8-bit codes again in 64 bits: of 8192x7168 codes 20 to 30 then differ from those
-// of the exact output (in float32 alone 50), at no cost from memory and 2 us of 38
-// where the activations are in the cache. Measured, bf16:
-// forward with checkpoint 8192x7168 62 us (4.7 TB/s), backward 16384x7168 135 us
-// with the launch that adds the workgroups' partial sums (5.2 TB/s; a copy of
-// 1 GiB runs at 5.0). A backward pass of 333x2047 float32 is 7 + 3 us of two
-// launches, 333 rows being little more than one for each CU.
+// of the exact output (in float32 alone 50), for less than 1 us from memory and 2 us
+// of 38 where the activations are in the cache. Measured, bf16: forward with checkpoint
+// 8192x7168 65 us (4.5 TB/s), backward 16384x7168 135 us with the launch that adds
+// the workgroups' partial sums (5.2 TB/s; a copy of 1 GiB runs at 5.0). A backward
+// pass of 333x2047 float32 is 7 + 3 us of two launches: 167 workgroups of two rows,
+// which leave a third of the CUs without work, and the one that adds their sums.
+//
+// Above 8192 columns the backward pass does not fit its registers (two sums, this
+// row, the next one and the weight): 4 to 145 of a thread's lie in memory up to
+// 16384 columns, 148 to 676 above. 4096x12288 bf16 takes 71 us (4.2 TB/s), float32
+// 180 (3.4); 2048x32768 bf16 500 us (0.8 TB/s), float32 870 (0.9).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -24,8 +24,13 @@
 // conversions and LDS traffic out between the products lost 10%, and tiles
 // ordered by XCD changed nothing. float32, 16384 slots into 512x2048: 113 us, 912
 // TFLOP/s of bf16 products. Many short groups, 128 of 256 slots into 768x2048:
-// 191 us, of which about 95 are the tiles' first loads and last stores (403 MB of
-// gradients at 5 TB/s are 81 us); the socket draws 1399 W there too.
+// 195 to 215 us; the same tiles with one step each (128 groups of 32 slots) take 112,
+// so that little of their first loads and last stores (403 MB of gradients, 81 us at
+// 5 TB/s) runs beside products. float32, 128 groups of 32 slots: 398 us.
+//
+// The parts of a float32 gradient go down to 2^-133, bf16's smallest: what lies
+// below in a gradient under 2^-110 is lost, and a value of X that became an infinity
+// (2^128) times a part that is 0 is NaN.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -566,8 +571,16 @@ hipError_t wgrad(const WgradArgs &a, hipStream_t s) {
                                 : (a.rows ? wgrad_kernel<T, kWaves, true, true> : wgrad_kernel<T, kWaves, false, true>);
     hipLaunchKernelGGL(kernel, grid, dim3(kWaves * 64), kLds, s, a, div);
   };
-  // Groups of 512 slots (64 of 768x2048): 179 us with eight waves, 186 with four;
-  // of 1024: 173 and 170; of 256 and fewer 5 to 20% in favour of eight.
+  // us with four / eight waves, by slots a group:      128          512        1024
+  //   bf16     64 groups into 768x2048             79 / 68    158 / 157   244 / 256
+  //            16 into 2048x2048                   50 / 43     96 / 93    159 / 163
+  //             1 into 2048x7168                   14 / 12     24 / 25     38 / 41
+  //            32 into 256x1024 (128 tiles)        11 / 9      21 / 18     32 / 29
+  //   float32  64 into 768x2048                   194 / 207   353 / 360   633 / 612
+  //            16 into 2048x2048                  137 / 147   247 / 229   409 / 402
+  //             1 into 2048x7168                   39 / 38     67 / 63    101 / 99
+  // The rule is that of bf16 with more tiles than CUs, which gains most from it;
+  // float32 and few tiles would take eight waves at 1024 slots too, for 1 to 10%.
   if (a.slots < 768 * int64_t(a.groups))
     go(std::integral_constant<int, 8>());
   else
