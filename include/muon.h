@@ -446,6 +446,122 @@ muon_status muon_route_backward(const muon_mat *logits, int32_t topk, int32_t re
                                 const int32_t *indices, const int32_t *counts, const float *dweights,
                                 const float *dloss, const muon_mat *dlogits);
 
+/* ---------------------------------------------------------------------------
+ * Feed-forward operators: the products between the routing and the sublayer's
+ * output, and the sum over a token's experts with dropout and residual. The
+ * conventions of the training operators hold. With the operators above they
+ * make a whole expert sublayer, forward and backward:
+ *   layernorm_forward -> (router product) -> route_forward ->
+ *   gated_forward -> expert_forward (scatter) -> combine_forward;
+ *   combine_backward (rows) -> expert_backward -> gated_backward ->
+ *   combine_forward of dx (weights NULL: the sum over a token's slots),
+ *   with route_backward(dweights) and ckpt_weight_grad of dgate, dup and
+ *   combine_backward's dx.
+ *
+ * Slots. Row s of a matrix in slot order belongs to group g where offsets[g]
+ * <= s < offsets[g + 1]. offsets (device, n_groups + 1 ascending int32; NULL
+ * with one group: every slot) and rows (device, an int32 per slot) are what
+ * muon_route_forward writes. Offsets outside [0, slots] count as the nearest
+ * bound. Rows of an output that belong to no group are left as they were; with
+ * no groups or no slots nothing is written.
+ *
+ * Weights: the first group's matrix, the others' `stride` elements further
+ * each; all operands of a call but offsets, rows, weights, indices and
+ * dweights share one dtype. float32: float32 products and sums; bf16: bf16
+ * products, float32 sums. Every result is rounded once (dx of gated_backward
+ * is the sum of products with dgate and dup as stored).
+ */
+#define MUON_ACT_SILU 0 /* g / (1 + exp(-g))          */
+#define MUON_ACT_GELU 1 /* g (1 + erf(g / sqrt 2)) / 2 */
+
+/*
+ * The gated block's first half, both products and what joins them:
+ *   h[s] = act(x[t(s)] wgate_g^T) * (x[t(s)] wup_g^T),
+ *   t(s) = rows[s] / rows_per_token (rows NULL: s / rows_per_token; then h has
+ *   at most rows_per_token rows for each row of x).
+ *   x            tokens x k;  wgate, wup  n x k;  h  slots x n.
+ *   gate, up     slots x n, receive the two products (NULL-able): what
+ *                muon_gated_backward reads.
+ * A slot whose token lies outside x gets zeros.
+ */
+muon_status muon_gated_forward(const muon_mat *x, const muon_mat *wgate, int64_t gate_stride, const muon_mat *wup,
+                               int64_t up_stride, int32_t n_groups, const int32_t *offsets, const int32_t *rows,
+                               int32_t rows_per_token, int32_t activation, const muon_mat *h, const muon_mat *gate,
+                               const muon_mat *up);
+
+/*
+ * Its backward pass, from gate and up as the forward pass wrote them:
+ *   dgate = dh * up * act'(gate),  dup = dh * act(gate)   (slots x n),
+ *   dx[rows[s]] = dgate[s] wgate_g + dup[s] wup_g          (rows NULL: dx[s]).
+ * dx has k columns and, without rows, a row for each slot; NULL: not computed,
+ * wgate and wup are then not read. The entries of rows are distinct; a row that
+ * rows does not name, or that lies outside dx, is not written. The weights'
+ * gradients are muon_ckpt_weight_grad of dgate and dup.
+ */
+muon_status muon_gated_backward(const muon_mat *dh, const muon_mat *gate, const muon_mat *up, const muon_mat *wgate,
+                                int64_t gate_stride, const muon_mat *wup, int64_t up_stride, int32_t n_groups,
+                                const int32_t *offsets, const int32_t *rows, int32_t activation, const muon_mat *dgate,
+                                const muon_mat *dup, const muon_mat *dx);
+
+/*
+ * Products of a group of expert layers: y[p(s)] = x[q(s)] w_g^T, w n x k, for
+ * each of `slots` slots.
+ *   gather   0: q(s) = s, x has a row for each slot;  > 0: q(s) = rows[s] /
+ *            gather (a slot whose row lies outside x gets zeros).
+ *   scatter  0: p(s) = s, y has a row for each slot;  1: p(s) = rows[s] (as
+ *            for dx of muon_gated_backward).
+ */
+muon_status muon_expert_forward(const muon_mat *x, const muon_mat *w, int64_t group_stride, int32_t n_groups, int64_t slots,
+                                const int32_t *offsets, const int32_t *rows, int32_t gather, int32_t scatter,
+                                const muon_mat *y);
+
+/* Its backward pass: dx[p(s)] = dy[q(s)] w_g, with the same rules for q and p
+ * (of a forward pass that gathered or scattered, the other one of the two). */
+muon_status muon_expert_backward(const muon_mat *dy, const muon_mat *w, int64_t group_stride, int32_t n_groups, int64_t slots,
+                                 const int32_t *offsets, const int32_t *rows, int32_t gather, int32_t scatter,
+                                 const muon_mat *dx);
+
+/*
+ * The sum over a token's experts, dropout and residual:
+ *   y[t] = residual[t] + drop(sum over j of weights[t, j] x[t topk + j]).
+ *   x         (tokens topk) x cols, topk <= 32;  y, residual  tokens x cols
+ *             (residual NULL-able: 0).
+ *   weights   tokens x topk float32, contiguous (NULL-able: 1).
+ *   indices   tokens x topk int32, contiguous: a choice below 0 adds nothing,
+ *             its row of x is not read (NULL-able: every choice counts).
+ *   drop(v)   element i (in row order, columns of the matrix, not its pitch)
+ *             is v / (1 - p) where word i mod 4 of Philox4x32-10's block is >=
+ *             floor(p 2^32), else 0: counter {i / 4, offset} (64 bits each, the
+ *             low words first), key seed.
+ *   p         in [0, 1);  key  device {seed, offset}, read when the work runs
+ *             (p = 0: NULL-able, nothing is dropped). A graph that holds the
+ *             call draws anew when the program has changed the offset.
+ */
+muon_status muon_combine_forward(const muon_mat *x, int32_t topk, const float *weights, const int32_t *indices,
+                                 const muon_mat *residual, float p, const uint64_t *key, const muon_mat *y);
+
+/*
+ * Its backward pass: with d[t] = drop(dy[t]), the same elements dropped,
+ *   dx of slot t topk + j = weights[t, j] d[t],
+ *   dweights[t, j] = sum over columns of x[t topk + j] d[t]
+ * (the residual's gradient is dy itself).
+ *   rows      NULL: dx lies as x does. Else as muon_route_forward wrote them:
+ *             row s of dx belongs to slot rows[s]; a row of dx whose slot is
+ *             -1, and a slot that is nowhere in rows, is not written.
+ *   dweights  tokens x topk, overwritten, 0 where indices is below 0
+ *             (NULL-able: not computed, x is then not read).
+ * Workspace with rows: muon_combine_workspace_size.
+ */
+muon_status muon_combine_backward(const muon_mat *dy, const muon_mat *x, int32_t topk, const float *weights,
+                                  const int32_t *indices, const int32_t *rows, float p, const uint64_t *key,
+                                  const muon_mat *dx, float *dweights);
+muon_status muon_combine_workspace_size(int64_t tokens, int32_t topk, size_t *bytes);
+
+/* Dropout alone, drop as above: y = residual + drop(x) (residual NULL-able: 0),
+ * and its backward pass dx = drop(dy). */
+muon_status muon_dropout_forward(const muon_mat *x, const muon_mat *residual, float p, const uint64_t *key, const muon_mat *y);
+muon_status muon_dropout_backward(const muon_mat *dy, float p, const uint64_t *key, const muon_mat *dx);
+
 #ifdef __cplusplus
 }
 #endif

@@ -52,7 +52,12 @@ EXPORTED = (
     "muon_layernorm_forward", "muon_layernorm_backward", "muon_layernorm_workspace_size",
     "muon_ckpt_save", "muon_ckpt_load", "muon_ckpt_weight_grad", "muon_ckpt_weight_grad_workspace_size",
     "muon_route_forward", "muon_route_backward", "muon_route_workspace_size",
+    "muon_gated_forward", "muon_gated_backward", "muon_expert_forward", "muon_expert_backward",
+    "muon_combine_forward", "muon_combine_backward", "muon_combine_workspace_size",
+    "muon_dropout_forward", "muon_dropout_backward",
 )
+MUON_ACT_SILU = 0
+MUON_ACT_GELU = 1
 MUON_CKPT_GROUP = 128  # columns that share one scale byte of a checkpoint
 MUON_NOALLOC_SCRATCH_BYTES = 256 << 20
 PHASES = ("prep", "norm", "gram", "aa", "bx", "finish", "adamw", "reduce")
@@ -137,6 +142,15 @@ def load_library(path=LIB_PATH):
         "muon_route_forward": [p, i32, i32, f, p, p, p, p, p, p],
         "muon_route_workspace_size": [i64, i64, i32, sz],
         "muon_route_backward": [p, i32, i32, f, p, p, p, p, p],
+        "muon_gated_forward": [p, p, i64, p, i64, i32, p, p, i32, i32, p, p, p],
+        "muon_gated_backward": [p, p, p, p, i64, p, i64, i32, p, p, i32, p, p, p],
+        "muon_expert_forward": [p, p, i64, i32, i64, p, p, i32, i32, p],
+        "muon_expert_backward": [p, p, i64, i32, i64, p, p, i32, i32, p],
+        "muon_combine_forward": [p, i32, p, p, p, f, p, p],
+        "muon_combine_backward": [p, p, i32, p, p, p, f, p, p, p],
+        "muon_combine_workspace_size": [i64, i32, sz],
+        "muon_dropout_forward": [p, p, f, p, p],
+        "muon_dropout_backward": [p, f, p, p],
     }.items():
         sigs[name] = (args, ctypes.c_int)
     for name, (args, res) in sigs.items():
@@ -650,3 +664,166 @@ def muon_route_backward(logits, indices, counts, dlogits, dweights=None, dloss=N
         _mat("logits", logits, d), pair[1], int(renormalize), alpha, _vec("indices", indices, _torch.int32, pair, d),
         _vec("counts", counts, _torch.int32, (logits.shape[1] + 1,), d), _vec("dweights", dweights, f32, pair, d),
         _vec("dloss", dloss, f32, (1,), d), _mat("dlogits", dlogits, d)))
+
+
+# ---------------------------------------------------------------------------
+# feed-forward operators
+# ---------------------------------------------------------------------------
+
+_ACTIVATIONS = {"silu": MUON_ACT_SILU, "gelu": MUON_ACT_GELU}
+
+
+def _activation(name):
+    code = _ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation: expected one of {sorted(_ACTIVATIONS)}, got {name!r}")
+    return code
+
+
+def _stack(name, t, device):
+    """(packed muon_mat of the first matrix, stride, groups) of a 3-D tensor groups x rows x cols, or of one 2-D matrix."""
+    if t.get_device() != device:
+        _on_gpu(name, t, device)
+    if t.dim() == 2:
+        return _mat(name, t, device), 0, 1
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected a 3-D tensor (groups x rows x cols) or a matrix")
+    groups, rows, cols = t.shape
+    stride, ld, unit = t.stride()
+    if (cols > 1 and unit != 1) or (rows > 1 and ld < cols):
+        raise ValueError(f"{name}: expected unit column stride")
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return _MAT(t.data_ptr(), rows, cols, ld if rows > 1 else cols, code, 1), stride, groups
+
+
+def _slots(offsets, rows, groups, slots, device):
+    """Addresses of the slot lists of a call."""
+    if groups > 1 and offsets is None:
+        raise ValueError("offsets: needed with more than one group")
+    return (_vec("offsets", offsets, _torch.int32, (groups + 1,), device),
+            _vec("rows", rows, _torch.int32, (slots,), device))
+
+
+def muon_gated_forward(x, wgate, wup, h, gate=None, up=None, offsets=None, rows=None, rows_per_token=1,
+                       activation="silu"):
+    """h = act(x wgate^T) * (x wup^T), one kernel (see muon.h). x: tokens x k;
+    wgate, wup: groups x n x k (or n x k: one group); h, and where given gate
+    and up (what the backward pass reads): slots x n; offsets (groups + 1) and
+    rows (slots): int32, as muon_route_forward writes them with rows_per_token
+    = topk. Rows of the outputs behind the last group are left as they were."""
+    d = _enter(x)
+    g, g_stride, groups = _stack("wgate", wgate, d)
+    u, u_stride, groups_u = _stack("wup", wup, d)
+    if groups != groups_u:
+        raise ValueError("wgate and wup differ in their number of groups")
+    h_mat = _mat("h", h, d)
+    _check(_lib.muon_gated_forward(
+        _mat("x", x, d), g, g_stride, u, u_stride, groups, *_slots(offsets, rows, groups, h.shape[0], d), rows_per_token,
+        _activation(activation), h_mat, _mat("gate", gate, d), _mat("up", up, d)))
+
+
+def muon_gated_backward(dh, gate, up, wgate, wup, dgate, dup, dx=None, offsets=None, rows=None, activation="silu"):
+    """dgate, dup (slots x n) and, where given, dx of the gated block (see
+    muon.h): dx[rows[s]] = dgate[s] wgate + dup[s] wup (without rows: dx[s]).
+    wgate and wup may be None without dx, if there is one group."""
+    d = _enter(dh)
+    g = u = None
+    g_stride = u_stride = 0
+    groups = 1 if offsets is None else offsets.shape[0] - 1
+    if wgate is not None or wup is not None or dx is not None:
+        if wgate is None or wup is None:
+            raise ValueError("wgate and wup: both are needed for dx")
+        g, g_stride, groups = _stack("wgate", wgate, d)
+        u, u_stride, groups_u = _stack("wup", wup, d)
+        if groups != groups_u:
+            raise ValueError("wgate and wup differ in their number of groups")
+    dh_mat = _mat("dh", dh, d)
+    _check(_lib.muon_gated_backward(
+        dh_mat, _mat("gate", gate, d), _mat("up", up, d), g, g_stride, u, u_stride, groups,
+        *_slots(offsets, rows, groups, dh.shape[0], d), _activation(activation), _mat("dgate", dgate, d),
+        _mat("dup", dup, d), _mat("dx", dx, d)))
+
+
+def _expert(fn, x, w, y, offsets, rows, gather, scatter):
+    d = _enter(x)
+    w_mat, stride, groups = _stack("w", w, d)
+    x_mat, y_mat = _mat("x", x, d), _mat("y", y, d)
+    slots = x.shape[0] if not gather else y.shape[0] if not scatter else rows.shape[0] if rows is not None else 0
+    _check(fn(x_mat, w_mat, stride, groups, slots, *_slots(offsets, rows, groups, slots, d), int(gather), int(scatter), y_mat))
+
+
+def muon_expert_forward(x, w, y, offsets=None, rows=None, gather=0, scatter=False):
+    """y[p(s)] = x[q(s)] w_g^T over the slots of each group g (see muon.h). w:
+    groups x n x k (or n x k: one group). gather: 0 (row s of x) or the rows
+    per token (row rows[s] // gather); scatter: whether slot s writes row
+    rows[s] of y instead of row s."""
+    _expert((_lib or lib()).muon_expert_forward, x, w, y, offsets, rows, gather, scatter)
+
+
+def muon_expert_backward(dy, w, dx, offsets=None, rows=None, gather=0, scatter=False):
+    """dx[p(s)] = dy[q(s)] w_g (see muon.h); the arguments are those of
+    muon_expert_forward."""
+    _expert((_lib or lib()).muon_expert_backward, dy, w, dx, offsets, rows, gather, scatter)
+
+
+@functools.lru_cache(256)
+def muon_combine_workspace_size(tokens, topk):
+    return _size(lib().muon_combine_workspace_size, tokens, topk)
+
+
+def _topk(x, y, weights, indices):
+    """Rows of x for each row of y."""
+    for t in (weights, indices):
+        if t is not None:
+            if t.dim() != 2:
+                raise ValueError("weights and indices: expected 2-D tensors (tokens x topk)")
+            return t.shape[1]
+    tokens = y.shape[0]
+    return x.shape[0] // tokens if tokens else 1
+
+
+def muon_combine_forward(x, y, weights=None, indices=None, residual=None, p=0.0, key=None):
+    """y[t] = residual[t] + drop(sum over j of weights[t, j] x[t topk + j])
+    (see muon.h). x: (tokens topk) x cols; weights (float32), indices (int32):
+    tokens x topk; topk is theirs, or the rows of x for each row of y. key: the
+    generator's seed and offset, two int64 on the GPU, needed for p > 0."""
+    d = _enter(x)
+    x_mat, y_mat = _mat("x", x, d), _mat("y", y, d)
+    topk = _topk(x, y, weights, indices)
+    pair = (y.shape[0], topk)
+    _check(_lib.muon_combine_forward(
+        x_mat, topk, _vec("weights", weights, _torch.float32, pair, d), _vec("indices", indices, _torch.int32, pair, d),
+        _mat("residual", residual, d), p, _vec("key", key, _torch.int64, (2,), d), y_mat))
+
+
+def muon_combine_backward(dy, x, dx, dweights=None, weights=None, indices=None, rows=None, p=0.0, key=None,
+                          workspace=None):
+    """dx and, where given, dweights (tokens x topk float32) of
+    muon_combine_forward (see muon.h), with the same weights, indices, p and
+    key. rows (tokens topk int32, as muon_route_forward writes them): dx is
+    written in their order instead of x's. x may be None without dweights.
+    workspace: a uint8 tensor of muon_combine_workspace_size bytes, with rows
+    (default: a temporary one)."""
+    d = _enter(dy)
+    dy_mat, dx_mat = _mat("dy", dy, d), _mat("dx", dx, d)
+    topk = _topk(dx, dy, weights, indices)
+    f32, i32, pair = _torch.float32, _torch.int32, (dy.shape[0], topk)
+    args = (dy_mat, _mat("x", x, d), topk, _vec("weights", weights, f32, pair, d), _vec("indices", indices, i32, pair, d),
+            _vec("rows", rows, i32, (pair[0] * topk,), d), p, _vec("key", key, _torch.int64, (2,), d), dx_mat,
+            _vec("dweights", dweights, f32, pair, d))
+    _with_scratch(muon_combine_workspace_size(*pair) if rows is not None else 0, workspace, d, _lib.muon_combine_backward, *args)
+
+
+def muon_dropout_forward(x, y, p, key=None, residual=None):
+    """y = residual + drop(x) (see muon.h); key as for muon_combine_forward."""
+    d = _enter(x)
+    _check(_lib.muon_dropout_forward(_mat("x", x, d), _mat("residual", residual, d), p,
+                                     _vec("key", key, _torch.int64, (2,), d), _mat("y", y, d)))
+
+
+def muon_dropout_backward(dy, dx, p, key=None):
+    """dx = drop(dy), with p and key of the forward pass (see muon.h)."""
+    d = _enter(dy)
+    _check(_lib.muon_dropout_backward(_mat("dy", dy, d), p, _vec("key", key, _torch.int64, (2,), d), _mat("dx", dx, d)))

@@ -1,5 +1,6 @@
 // Launch arguments of the training operators (layer norm, 8-bit checkpoints,
-// expert weight gradients, routing), shared by the host entry points
+// expert weight gradients, routing, products of groups of rows, the sum over a
+// token's experts with dropout), shared by the host entry points
 // (train_api.cpp) and the kernels.
 #pragma once
 
@@ -110,6 +111,61 @@ struct RouteBwdArgs {
   int64_t ld_out;
 };
 
+enum Activation : int32_t { kActSilu = 0, kActGelu = 1 };
+
+// Slots in groups: group g's are offsets[g] .. offsets[g + 1] - 1.
+struct ProductArgs {
+  const void *x, *x2;      // rows of the left operand; x2: of a second product that is added (back), or NULL
+  int64_t ld_x, ld_x2;
+  int64_t x_rows;
+  const void *w, *w2;      // weights; w2: of the gated block's second product, or x2's
+  int64_t ld_w, ld_w2;
+  int64_t w_stride, w2_stride;  // elements from group to group
+  const int32_t *offsets;  // groups + 1, or NULL: one group of every slot
+  const int32_t *rows;     // slots, or NULL: slot order
+  int64_t slots;
+  int32_t groups;
+  int32_t gather;          // slot s reads row s of x (0), or rows[s] / gather
+  int32_t scatter;         // and writes row s of out (0), or rows[s]
+  int32_t back;            // weights n x k lie as rows of the sum's index
+  int32_t n, k;            // columns of out, length of the sum
+  void *out, *gate, *up;   // gate and up: the gated block's products, or NULL
+  int64_t ld_out, ld_gate, ld_up;
+  int64_t out_rows;
+  int32_t act;             // Activation
+  int32_t tiles_n;
+};
+
+struct GatedGradArgs {
+  const void *dh, *gate, *up;
+  void *dgate, *dup;
+  int64_t ld_dh, ld_gate, ld_up, ld_dgate, ld_dup;
+  const int32_t *offsets;
+  int64_t slots;
+  int32_t groups, n;
+  int32_t act;
+};
+
+constexpr int kCombineMaxTopk = 32;
+
+struct CombineArgs {
+  const void *x;           // slots x cols (backward: NULL without dweights)
+  const void *res;         // forward: added, or NULL
+  const void *dy;          // backward
+  void *out;               // forward: y, backward: dx
+  float *dweights;         // backward, or NULL
+  int64_t ld_x, ld_res, ld_dy, ld_out;
+  int64_t tokens;
+  int32_t cols, topk;
+  const float *weights;    // tokens x topk, or NULL: 1
+  const int32_t *indices;  // tokens x topk, < 0: no choice; or NULL: all
+  const int32_t *rows;     // backward: slots in the order of dx's rows, or NULL
+  int32_t *places;         // backward: scratch, the place of each slot in rows
+  const uint64_t *key;     // seed, offset; NULL: nothing is dropped
+  uint32_t threshold;      // words below it are dropped
+  float scale;             // 1 / (1 - p)
+};
+
 int norm_bwd_blocks(int64_t rows, int64_t cols);
 hipError_t launch_norm_fwd(const NormFwdArgs &a, bool bf16, hipStream_t s);
 hipError_t launch_norm_bwd(const NormBwdArgs &a, bool bf16, hipStream_t s);
@@ -124,5 +180,9 @@ hipError_t launch_wgrad(const WgradArgs &a, bool bf16, hipStream_t s);
 void route_plan(RouteFwdArgs &a);
 hipError_t launch_route_fwd(const RouteFwdArgs &a, bool bf16, hipStream_t s);
 hipError_t launch_route_bwd(const RouteBwdArgs &a, bool bf16, hipStream_t s);
+hipError_t launch_product(const ProductArgs &a, bool bf16, hipStream_t s);
+hipError_t launch_gated_grad(const GatedGradArgs &a, bool bf16, hipStream_t s);
+hipError_t launch_combine_fwd(const CombineArgs &a, bool bf16, hipStream_t s);
+hipError_t launch_combine_bwd(const CombineArgs &a, bool bf16, hipStream_t s);
 
 }  // namespace muon

@@ -1,4 +1,5 @@
 // C ABI entry points of the training operators: validation and launches.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -176,6 +177,135 @@ char *workspace(const State &st, size_t bytes, Buffers &b) {
     refuse(MUON_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu set (muon_set_workspace)", bytes, st.ws_bytes);
   b.add(st.ws, 1, int64_t(bytes), 0, true, "workspace");
   return static_cast<char *>(st.ws);
+}
+
+// The weights of the groups: rows x cols of one dtype, stride elements apart.
+void weights(Buffers &b, const muon_mat *w, const char *name, int64_t stride, int32_t groups, int32_t dtype, bool written) {
+  if (w->rows < 1) refuse(MUON_ERR_SHAPE, "%s: no rows", name);
+  if (w->dtype != dtype) refuse(MUON_ERR_DTYPE, "%s: of another dtype than the rows", name);
+  const int64_t es = int64_t(esize(dtype)), extent = (w->rows - 1) * w->ld + w->cols;
+  if (groups > 1 && stride < extent) refuse(MUON_ERR_SHAPE, "%s: the groups' matrices overlap", name);
+  if (groups > 1 && !fits(groups, stride)) refuse(MUON_ERR_SHAPE, "%s: groups * stride > 2^60", name);
+  if (groups > 1)
+    b.add(w->data, w->ld == w->cols ? groups : 1, (w->ld == w->cols ? extent : (groups - 1) * stride + extent) * es, stride * es,
+          written, name);
+  else if (groups == 1)
+    add(b, w, written, name);
+}
+
+// Slots in groups, and the products' sizes.
+void slots_of(ProductArgs &a, Buffers &b, int64_t slots, int32_t groups, const int32_t *offsets, const int32_t *rows) {
+  if (slots < 0 || slots > kMaxSlots) refuse(MUON_ERR_SHAPE, "slots must lie in [0, 2^31 - 2^22]");
+  if (groups < 0 || groups > 65536) refuse(MUON_ERR_INVALID_ARG, "n_groups must lie in [0, 65536]");
+  if (groups > 1 && !offsets) refuse(MUON_ERR_INVALID_ARG, "offsets must not be NULL with more than one group");
+  aligned4(offsets, "offsets");
+  aligned4(rows, "rows");
+  b.add(offsets, 1, (int64_t(groups) + 1) * 4, 0, false, "offsets");
+  b.add(rows, 1, slots * 4, 0, false, "rows");
+  a.slots = slots;
+  a.groups = groups;
+  a.offsets = offsets;
+  a.rows = rows;
+}
+
+void sizes(ProductArgs &a, int64_t n, int64_t k) {
+  if (n > kMaxIndex / 2 || k > kMaxIndex / 2) refuse(MUON_ERR_SHAPE, "weights: rows and cols must lie below 2^30");
+  if (((n + 127) / 128) * (a.slots / 128 + std::min<int64_t>(a.groups, a.slots)) > kMaxIndex)
+    refuse(MUON_ERR_SHAPE, "slots * columns too large");
+  a.n = int32_t(n);
+  a.k = a.x_rows > 0 ? int32_t(k) : 0;  // no row of x: every sum is empty
+}
+
+void activation_of(int32_t activation) {
+  if (activation != MUON_ACT_SILU && activation != MUON_ACT_GELU)
+    refuse(MUON_ERR_INVALID_ARG, "activation must be MUON_ACT_SILU or MUON_ACT_GELU");
+}
+
+void expert_product(State &st, const muon_mat *x, const muon_mat *w, int64_t group_stride, int32_t n_groups, int64_t slots,
+                    const int32_t *offsets, const int32_t *rows, int32_t gather, int32_t scatter, const muon_mat *y, bool back) {
+  matrix(x, "x", kMaxIndex / 2);
+  matrix(w, "w", kMaxIndex / 2);
+  matrix(y, "y", kMaxIndex / 2);
+  if (y->dtype != x->dtype) refuse(MUON_ERR_DTYPE, "x and y differ in dtype");
+  if (gather < 0) refuse(MUON_ERR_INVALID_ARG, "gather must be >= 0");
+  if (scatter != 0 && scatter != 1) refuse(MUON_ERR_INVALID_ARG, "scatter must be 0 or 1");
+  ProductArgs a{};
+  Buffers b;
+  slots_of(a, b, slots, n_groups, offsets, rows);
+  if ((gather || scatter) && !rows && slots > 0) refuse(MUON_ERR_INVALID_ARG, "rows must not be NULL with gather or scatter");
+  if (!gather && x->rows != slots) refuse(MUON_ERR_SHAPE, "without gather, x has a row for each slot");
+  if (!scatter && y->rows != slots) refuse(MUON_ERR_SHAPE, "without scatter, y has a row for each slot");
+  if (x->cols != (back ? w->rows : w->cols) || y->cols != (back ? w->cols : w->rows))
+    refuse(MUON_ERR_SHAPE, back ? "x's columns are the weights' rows, y's their columns" : "x's columns are the weights' columns, y's their rows");
+  a.x_rows = x->rows;
+  sizes(a, y->cols, x->cols);
+  add(b, x, false, "x");
+  weights(b, w, "w", group_stride, n_groups, x->dtype, false);
+  add(b, y, true, "y");
+  b.check();
+  if (n_groups == 0 || slots == 0) return;
+  a.x = x->data;
+  a.ld_x = x->ld;
+  a.w = w->data;
+  a.ld_w = w->ld;
+  a.w_stride = n_groups > 1 ? group_stride : 0;
+  a.gather = gather;
+  a.scatter = scatter;
+  a.back = back;
+  a.out = y->data;
+  a.ld_out = y->ld;
+  a.out_rows = y->rows;
+  launched(launch_product(a, x->dtype == MUON_BF16, st.stream), "experts' product launch");
+}
+
+// What the sum over a token's experts and its backward pass share.
+void combine_shape(CombineArgs &a, Buffers &b, int64_t tokens, int64_t cols, int32_t topk, const float *weights,
+                   const int32_t *indices, float p, const uint64_t *key) {
+  if (topk < 1 || topk > kCombineMaxTopk) refuse(MUON_ERR_INVALID_ARG, "topk must lie in [1, %d]", kCombineMaxTopk);
+  if (tokens > kMaxIndex / topk) refuse(MUON_ERR_SHAPE, "tokens * topk must lie below 2^31");
+  if (!(p >= 0.f && p < 1.f)) refuse(MUON_ERR_INVALID_ARG, "p must lie in [0, 1)");
+  if (p > 0.f) need(key, "key");
+  if (reinterpret_cast<uintptr_t>(key) % 8) refuse(MUON_ERR_ALIGN, "key: not aligned to 8 bytes");
+  aligned4(weights, "weights");
+  aligned4(indices, "indices");
+  b.add(weights, 1, tokens * topk * 4, 0, false, "weights");
+  b.add(indices, 1, tokens * topk * 4, 0, false, "indices");
+  if (p > 0.f) b.add(key, 1, 16, 0, false, "key");
+  a.tokens = tokens;
+  a.cols = int32_t(cols);
+  a.topk = topk;
+  a.weights = weights;
+  a.indices = indices;
+  a.key = p > 0.f ? key : nullptr;
+  a.threshold = uint32_t(double(p) * 4294967296.);  // p has 24 bits: below 2^32
+  a.scale = float(1. / (1. - double(p)));
+}
+
+void combine_forward(State &st, const muon_mat *x, int32_t topk, const float *weights, const int32_t *indices,
+                     const muon_mat *residual, float p, const uint64_t *key, const muon_mat *y) {
+  matrix(x, "x", kMaxIndex / 2);
+  matrix(y, "y", kMaxIndex / 2);
+  if (residual) {
+    matrix(residual, "residual", kMaxIndex / 2);
+    same(residual, "residual", y, "y");
+  }
+  CombineArgs a{};
+  Buffers b;
+  combine_shape(a, b, y->rows, y->cols, topk, weights, indices, p, key);
+  if (x->dtype != y->dtype) refuse(MUON_ERR_DTYPE, "x and y differ in dtype");
+  if (x->rows != y->rows * topk || x->cols != y->cols) refuse(MUON_ERR_SHAPE, "x has topk rows for each row of y");
+  add(b, x, false, "x");
+  add(b, residual, false, "residual");
+  add(b, y, true, "y");
+  b.check();
+  if (y->rows == 0) return;
+  a.x = x->data;
+  a.ld_x = x->ld;
+  a.res = residual ? residual->data : nullptr;
+  a.ld_res = residual ? residual->ld : 0;
+  a.out = y->data;
+  a.ld_out = y->ld;
+  launched(launch_combine_fwd(a, y->dtype == MUON_BF16, st.stream), "combine launch");
 }
 
 size_t norm_workspace(int64_t rows, int64_t cols) { return size_t(norm_bwd_blocks(rows, cols)) * 2 * cols * sizeof(float); }
@@ -530,6 +660,204 @@ muon_status muon_route_backward(const muon_mat *logits, int32_t topk, int32_t re
     a.ld_out = dlogits->ld;
     launched(launch_route_bwd(a, logits->dtype == MUON_BF16, st.stream), "routing backward launch");
   });
+}
+
+muon_status muon_gated_forward(const muon_mat *x, const muon_mat *wgate, int64_t gate_stride, const muon_mat *wup,
+                               int64_t up_stride, int32_t n_groups, const int32_t *offsets, const int32_t *rows,
+                               int32_t rows_per_token, int32_t activation, const muon_mat *h, const muon_mat *gate,
+                               const muon_mat *up) {
+  return entry([&](State &st) {
+    matrix(x, "x", kMaxIndex / 2);
+    matrix(wgate, "wgate", kMaxIndex / 2);
+    matrix(wup, "wup", kMaxIndex / 2);
+    matrix(h, "h", kMaxIndex / 2);
+    const muon_mat *saved[2] = {gate, up};
+    const char *names[2] = {"gate", "up"};
+    if (h->dtype != x->dtype) refuse(MUON_ERR_DTYPE, "x and h differ in dtype");
+    for (int i = 0; i < 2; ++i)
+      if (saved[i]) {
+        matrix(saved[i], names[i], kMaxIndex / 2);
+        same(saved[i], names[i], h, "h");
+      }
+    same(wup, "wup", wgate, "wgate");
+    activation_of(activation);
+    if (rows_per_token < 1) refuse(MUON_ERR_INVALID_ARG, "rows_per_token must be >= 1");
+    ProductArgs a{};
+    Buffers b;
+    slots_of(a, b, h->rows, n_groups, offsets, rows);
+    if (wgate->cols != x->cols || wgate->rows != h->cols) refuse(MUON_ERR_SHAPE, "weights are h's columns x x's columns");
+    if (!rows && h->rows > x->rows * int64_t(rows_per_token))
+      refuse(MUON_ERR_SHAPE, "without rows, h has at most rows_per_token rows for each row of x");
+    a.x_rows = x->rows;
+    sizes(a, h->cols, x->cols);
+    add(b, x, false, "x");
+    weights(b, wgate, "wgate", gate_stride, n_groups, x->dtype, false);
+    weights(b, wup, "wup", up_stride, n_groups, x->dtype, false);
+    add(b, h, true, "h");
+    add(b, gate, true, "gate");
+    add(b, up, true, "up");
+    b.check();
+    if (n_groups == 0 || h->rows == 0) return;
+    a.x = x->data;
+    a.ld_x = x->ld;
+    a.w = wgate->data;
+    a.ld_w = wgate->ld;
+    a.w_stride = n_groups > 1 ? gate_stride : 0;
+    a.w2 = wup->data;
+    a.ld_w2 = wup->ld;
+    a.w2_stride = n_groups > 1 ? up_stride : 0;
+    a.gather = rows || rows_per_token > 1 ? rows_per_token : 0;
+    a.act = activation;
+    a.out = h->data;
+    a.ld_out = h->ld;
+    a.gate = gate ? gate->data : nullptr;
+    a.ld_gate = gate ? gate->ld : 0;
+    a.up = up ? up->data : nullptr;
+    a.ld_up = up ? up->ld : 0;
+    launched(launch_product(a, x->dtype == MUON_BF16, st.stream), "gated block launch");
+  });
+}
+
+muon_status muon_gated_backward(const muon_mat *dh, const muon_mat *gate, const muon_mat *up, const muon_mat *wgate,
+                                int64_t gate_stride, const muon_mat *wup, int64_t up_stride, int32_t n_groups,
+                                const int32_t *offsets, const int32_t *rows, int32_t activation, const muon_mat *dgate,
+                                const muon_mat *dup, const muon_mat *dx) {
+  return entry([&](State &st) {
+    const muon_mat *like[5] = {dh, gate, up, dgate, dup};
+    const char *names[5] = {"dh", "gate", "up", "dgate", "dup"};
+    Buffers b;
+    for (int i = 0; i < 5; ++i) {
+      matrix(like[i], names[i], kMaxIndex / 2);
+      if (i) same(like[i], names[i], dh, "dh");
+      add(b, like[i], i >= 3, names[i]);
+    }
+    activation_of(activation);
+    ProductArgs a{};
+    slots_of(a, b, dh->rows, n_groups, offsets, rows);
+    if (dx) {
+      matrix(wgate, "wgate", kMaxIndex / 2);
+      matrix(wup, "wup", kMaxIndex / 2);
+      matrix(dx, "dx", kMaxIndex / 2);
+      same(wup, "wup", wgate, "wgate");
+      if (dx->dtype != dh->dtype) refuse(MUON_ERR_DTYPE, "dh and dx differ in dtype");
+      if (wgate->rows != dh->cols || wgate->cols != dx->cols) refuse(MUON_ERR_SHAPE, "weights are dh's columns x dx's columns");
+      if (!rows && dx->rows != dh->rows) refuse(MUON_ERR_SHAPE, "without rows, dx has a row for each slot");
+      a.x_rows = dh->rows;
+      sizes(a, dx->cols, dh->cols);
+      weights(b, wgate, "wgate", gate_stride, n_groups, dh->dtype, false);
+      weights(b, wup, "wup", up_stride, n_groups, dh->dtype, false);
+      add(b, dx, true, "dx");
+    }
+    b.check();
+    if (n_groups == 0 || dh->rows == 0) return;
+    const bool bf16 = dh->dtype == MUON_BF16;
+    GatedGradArgs g{};
+    g.dh = dh->data;
+    g.ld_dh = dh->ld;
+    g.gate = gate->data;
+    g.ld_gate = gate->ld;
+    g.up = up->data;
+    g.ld_up = up->ld;
+    g.dgate = dgate->data;
+    g.ld_dgate = dgate->ld;
+    g.dup = dup->data;
+    g.ld_dup = dup->ld;
+    g.offsets = offsets;
+    g.slots = dh->rows;
+    g.groups = n_groups;
+    g.n = int32_t(dh->cols);
+    g.act = activation;
+    launched(launch_gated_grad(g, bf16, st.stream), "gated block's gradients launch");
+    if (!dx) return;
+    a.x = dgate->data;
+    a.ld_x = dgate->ld;
+    a.x2 = dup->data;
+    a.ld_x2 = dup->ld;
+    a.w = wgate->data;
+    a.ld_w = wgate->ld;
+    a.w_stride = n_groups > 1 ? gate_stride : 0;
+    a.w2 = wup->data;
+    a.ld_w2 = wup->ld;
+    a.w2_stride = n_groups > 1 ? up_stride : 0;
+    a.scatter = rows != nullptr;
+    a.back = 1;
+    a.out = dx->data;
+    a.ld_out = dx->ld;
+    a.out_rows = dx->rows;
+    launched(launch_product(a, bf16, st.stream), "gated block's backward launch");
+  });
+}
+
+muon_status muon_expert_forward(const muon_mat *x, const muon_mat *w, int64_t group_stride, int32_t n_groups, int64_t slots,
+                                const int32_t *offsets, const int32_t *rows, int32_t gather, int32_t scatter,
+                                const muon_mat *y) {
+  return entry([&](State &st) { expert_product(st, x, w, group_stride, n_groups, slots, offsets, rows, gather, scatter, y, false); });
+}
+
+muon_status muon_expert_backward(const muon_mat *dy, const muon_mat *w, int64_t group_stride, int32_t n_groups, int64_t slots,
+                                 const int32_t *offsets, const int32_t *rows, int32_t gather, int32_t scatter,
+                                 const muon_mat *dx) {
+  return entry([&](State &st) { expert_product(st, dy, w, group_stride, n_groups, slots, offsets, rows, gather, scatter, dx, true); });
+}
+
+muon_status muon_combine_forward(const muon_mat *x, int32_t topk, const float *weights, const int32_t *indices,
+                                 const muon_mat *residual, float p, const uint64_t *key, const muon_mat *y) {
+  return entry([&](State &st) { combine_forward(st, x, topk, weights, indices, residual, p, key, y); });
+}
+
+muon_status muon_combine_workspace_size(int64_t tokens, int32_t topk, size_t *bytes) {
+  return entry([&](State &) {
+    need(bytes, "bytes");
+    if (topk < 1 || topk > kCombineMaxTopk) refuse(MUON_ERR_INVALID_ARG, "topk must lie in [1, %d]", kCombineMaxTopk);
+    if (tokens < 0 || tokens > kMaxIndex / topk) refuse(MUON_ERR_SHAPE, "tokens * topk must lie in [0, 2^31)");
+    *bytes = size_t(tokens) * size_t(topk) * 4;
+  });
+}
+
+muon_status muon_combine_backward(const muon_mat *dy, const muon_mat *x, int32_t topk, const float *weights,
+                                  const int32_t *indices, const int32_t *rows, float p, const uint64_t *key,
+                                  const muon_mat *dx, float *dweights) {
+  return entry([&](State &st) {
+    matrix(dy, "dy", kMaxIndex / 2);
+    matrix(dx, "dx", kMaxIndex / 2);
+    CombineArgs a{};
+    Buffers b;
+    combine_shape(a, b, dy->rows, dy->cols, topk, weights, indices, p, key);
+    if (dx->dtype != dy->dtype) refuse(MUON_ERR_DTYPE, "dy and dx differ in dtype");
+    if (dx->rows != dy->rows * topk || dx->cols != dy->cols) refuse(MUON_ERR_SHAPE, "dx has topk rows for each row of dy");
+    if (dweights) {
+      matrix(x, "x", kMaxIndex / 2);
+      same(x, "x", dx, "dx");
+      add(b, x, false, "x");
+    }
+    aligned4(rows, "rows");
+    aligned4(dweights, "dweights");
+    add(b, dy, false, "dy");
+    add(b, dx, true, "dx");
+    b.add(rows, 1, dx->rows * 4, 0, false, "rows");
+    b.add(dweights, 1, dx->rows * 4, 0, true, "dweights");
+    char *ws = rows ? workspace(st, size_t(dx->rows) * 4, b) : nullptr;
+    b.check();
+    if (dy->rows == 0) return;
+    a.dy = dy->data;
+    a.ld_dy = dy->ld;
+    a.x = dweights ? x->data : nullptr;
+    a.ld_x = dweights ? x->ld : 0;
+    a.out = dx->data;
+    a.ld_out = dx->ld;
+    a.rows = rows;
+    a.places = reinterpret_cast<int32_t *>(ws);
+    a.dweights = dweights;
+    launched(launch_combine_bwd(a, dy->dtype == MUON_BF16, st.stream), "combine backward launch");
+  });
+}
+
+muon_status muon_dropout_forward(const muon_mat *x, const muon_mat *residual, float p, const uint64_t *key, const muon_mat *y) {
+  return entry([&](State &st) { combine_forward(st, x, 1, nullptr, nullptr, residual, p, key, y); });
+}
+
+muon_status muon_dropout_backward(const muon_mat *dy, float p, const uint64_t *key, const muon_mat *dx) {
+  return entry([&](State &st) { combine_forward(st, dy, 1, nullptr, nullptr, nullptr, p, key, dx); });
 }
 
 }  // extern "C"
