@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "lanes.h"
 #include "train.h"
@@ -29,20 +30,29 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kRowBytes = 64;      // of a step in LDS: 32 bf16 or 16 float32 of the sum's index
-constexpr int kTileN = 256;        // columns of a tile (gated: 128 of each product)
 constexpr int kBand = 8;           // tiles of a group that take turns within one column of tiles
-constexpr int kOutPitch = 64 + 4;  // floats; epilogue rows of a wave
 
-// kWM x 4 waves of 128 x 64. One wave row: 72 KiB of LDS, two workgroups a CU.
-// Two: one workgroup a CU, which reads each operand half as often from L2.
-template <int kWM>
+// A workgroup's tile: kWM x kWN waves of 32 kI x 64 (gated: 32 columns of each
+// product), the 32-row blocks dealt to the wave rows in turn, so that a tile
+// with few rows leaves each of them few. kK > 1: as many waves per part of the
+// tile share its sum, each with an LDS ring of its own, and add up at the end.
+template <int kWM_, int kWN_, int kI_, int kK_, int kStages_>
 struct Form {
-  static constexpr int kThreads = kWM * 256;
-  static constexpr int kBM = kWM * 128;
+  static constexpr int kWM = kWM_, kWN = kWN_, kI = kI_, kK = kK_, kStages = kStages_;
+  static constexpr int kWaves = kWM * kWN * kK, kThreads = kWaves * 64;
+  static constexpr int kBM = kWM * kI * 32, kBN = kWN * 64;
   static constexpr int kABytes = kBM * kRowBytes;
-  static constexpr int kStage = kABytes + kTileN * kRowBytes;
-  static constexpr int kStages = kWM == 1 ? 3 : 5;
+  static constexpr int kStage = kABytes + kBN * kRowBytes;  // a ring's
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kLoaders = kK > 1 ? 1 : kWaves < 4 ? kWaves : 4;  // waves that load a ring
+  static constexpr int kX = kABytes / 1024 / kLoaders, kW = kBN * kRowBytes / 1024 / kLoaders;  // their loads, a KiB each
+  static_assert(kX * kLoaders * 1024 == kABytes && kW * kLoaders * 1024 == kBN * kRowBytes);
+  static constexpr int kPerSimd = kWaves >= 8 ? 2 : kWaves * (kRing * kK > 80 * 1024 ? 1 : 2) / 4;
 };
+using Large = Form<2, 4, 4, 1, 5>;  // 256 x 256, 160 KiB of LDS
+using Wide = Form<1, 4, 4, 1, 3>;   // 128 x 256, 72 KiB: two workgroups a CU
+using Small = Form<2, 2, 1, 1, 4>;  // 64 x 128, 48 KiB
+using Thin = Form<1, 1, 1, 4, 3>;   // 32 x 64, four waves to a sum, 72 KiB
 
 __device__ inline float act_value(float g, int act, float &slope) {
   if (act == kActSilu) {
@@ -80,31 +90,40 @@ __device__ inline int wave_scan(int v, int lane) {  // inclusive
   return v;
 }
 
-// The slots of a group, cut to what there is.
-__device__ inline void group_slots(const ProductArgs &a, int g, int &lo, int &hi) {
-  lo = g < a.groups ? a.offsets[g] : 0;
-  hi = g < a.groups ? a.offsets[g + 1] : 0;
-  lo = lo < 0 ? 0 : lo;
-  hi = hi > int(a.slots) ? int(a.slots) : hi;
+// An offset, cut to what there is.
+__device__ inline int slot_bound(const ProductArgs &a, int g) {
+  const int o = a.offsets[g];
+  return o < 0 ? 0 : o > int(a.slots) ? int(a.slots) : o;
 }
 
-// The tile of this workgroup, of rows x tiles_n tiles of `rows` slots. The
-// tiles of a group lie in bands of kBand row tiles; every eighth workgroup runs
-// on one XCD, which gets a contiguous part of them.
+// The tile of this workgroup, of tiles_n across and `rows` slots each. A
+// group's tiles lie in bands of kBand row tiles; every eighth workgroup runs on
+// one XCD, which gets a contiguous part of them. Each wave counts the tiles of
+// all groups by itself: a lane those of kRun groups, whose offsets it loads at
+// once, again for more groups than 64 kRun.
 __device__ inline Tile find_tile(const ProductArgs &a, int rows, int lane) {
+  constexpr int kRun = 8;
   const uint32_t b = blockIdx.y * gridDim.x + blockIdx.x;
   Tile t{-1, 0, 0, 0};
-  uint32_t total;  // row tiles
-  if (a.offsets) {
-    int sum = 0;
-    for (int g0 = 0; g0 < a.groups; g0 += 64) {
-      int lo, hi;
-      group_slots(a, g0 + lane, lo, hi);
-      sum += hi > lo ? (hi - lo + rows - 1) / rows : 0;
+  uint32_t total = uint32_t((a.slots + rows - 1) / rows);  // row tiles
+  const int run = a.groups >= 64 * kRun ? kRun : (a.groups + 63) / 64;  // groups of a lane
+  int at[kRun + 1], upto = 0, before = 0;
+  auto tiles_of = [&](int r) { return at[r + 1] > at[r] ? (at[r + 1] - at[r] + rows - 1) / rows : 0; };
+  auto scan = [&](int g0) {  // the tiles up to a lane's last group
+#pragma unroll
+    for (int r = 0; r <= kRun; ++r) {
+      const int g = g0 + lane * run + (r < run ? r : run);
+      at[r] = slot_bound(a, g < a.groups ? g : a.groups);
     }
-    total = uint32_t(__builtin_amdgcn_readlane(wave_scan(sum, lane), 63));
-  } else {
-    total = uint32_t((a.slots + rows - 1) / rows);
+    int sum = 0;
+#pragma unroll
+    for (int r = 0; r < kRun; ++r) sum += tiles_of(r);
+    upto = before + wave_scan(sum, lane);
+    before = __builtin_amdgcn_readlane(upto, 63);
+  };
+  if (a.offsets) {
+    for (int g0 = 0; g0 < a.groups; g0 += 64 * run) scan(g0);
+    total = uint32_t(before);
   }
   const uint32_t tiles = total * uint32_t(a.tiles_n), per = (tiles + 7) / 8;
   const uint32_t id = (b & 7) * per + (b >> 3);
@@ -114,23 +133,28 @@ __device__ inline Tile find_tile(const ProductArgs &a, int rows, int lane) {
   int64_t lo = 0, hi = a.slots;
   t.group = 0;
   if (a.offsets) {
-    uint32_t before = 0;
-    for (int g0 = 0; g0 < a.groups; g0 += 64) {
-      int glo, ghi;
-      group_slots(a, g0 + lane, glo, ghi);
-      const int mine = ghi > glo ? (ghi - glo + rows - 1) / rows : 0;
-      const uint32_t upto = before + uint32_t(wave_scan(mine, lane));
-      const uint64_t past = __ballot(upto > row);
-      if (past) {
-        const int at = __builtin_amdgcn_readfirstlane(__builtin_ctzll(past));
-        t.group = g0 + at;
-        count = uint32_t(__builtin_amdgcn_readlane(mine, at));
-        first = uint32_t(__builtin_amdgcn_readlane(int(upto), at)) - count;
-        lo = __builtin_amdgcn_readlane(glo, at);
-        hi = __builtin_amdgcn_readlane(ghi, at);
+    int g0 = 0;
+    if (a.groups > 64 * run) {
+      before = 0;
+      for (scan(0); uint32_t(before) <= row; scan(g0)) g0 += 64 * run;
+    }
+    const int owner = __builtin_amdgcn_readfirstlane(__builtin_ctzll(__ballot(uint32_t(upto) > row)));
+    int sum = 0;
+#pragma unroll
+    for (int r = 0; r < kRun; ++r) sum += tiles_of(r);
+    first = uint32_t(__builtin_amdgcn_readlane(upto - sum, owner));
+    t.group = g0 + owner * run;
+#pragma unroll
+    for (int r = 0; r < kRun; ++r) {
+      const uint32_t mine = uint32_t(__builtin_amdgcn_readlane(tiles_of(r), owner));
+      if (first <= row && row < first + mine) {
+        t.group = g0 + owner * run + r;
+        count = mine;
+        lo = __builtin_amdgcn_readlane(at[r], owner);
+        hi = __builtin_amdgcn_readlane(at[r + 1], owner);
         break;
       }
-      before = uint32_t(__builtin_amdgcn_readlane(int(upto), 63));
+      first += mine;
     }
   }
   const uint32_t local = id - first * uint32_t(a.tiles_n);
@@ -138,8 +162,12 @@ __device__ inline Tile find_tile(const ProductArgs &a, int rows, int lane) {
   const uint32_t wide = count - band * kBand < kBand ? count - band * kBand : kBand;
   t.n = __builtin_amdgcn_readfirstlane(int(in / wide));
   const int m = __builtin_amdgcn_readfirstlane(int(band * kBand + in % wide));
-  t.lo = lo + int64_t(m) * rows;
-  t.hi = t.lo + rows < hi ? t.lo + rows : hi;
+  // the group's 32-row blocks, dealt evenly to its tiles: a tile of few rows
+  // would wait for its weights at every step
+  const int each = int((uint32_t(hi - lo + 31) / 32 + count - 1) / count) * 32;
+  t.lo = lo + int64_t(m) * each;
+  t.hi = t.lo + each < hi ? t.lo + each : hi;
+  if (t.lo >= t.hi) t.group = -1;
   return t;
 }
 
@@ -158,13 +186,48 @@ __device__ inline int64_t source_row(const ProductArgs &a, int64_t s) {
 // the tiled kernel
 // ---------------------------------------------------------------------------
 
-// 16 bytes of a fragment: eight bf16 or four float32 of the sum's index.
+// 16 bytes of a fragment: eight bf16 or four float32 of the sum's index. The
+// weights come first: a lane's 16 sums are then columns of one row of x, 4 (lane
+// / 32) .. + 3 of each eight, which leave from the registers.
 __device__ inline void multiply(f32x16 &acc, const u32x4 &x, const u32x4 &w, __bf16) {
-  acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), acc, 0, 0, 0);
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
 }
 __device__ inline void multiply(f32x16 &acc, const u32x4 &x, const u32x4 &w, float) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(bits_f32(x[e]), bits_f32(w[e]), acc, 0, 0, 0);
+  for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(bits_f32(w[e]), bits_f32(x[e]), acc, 0, 0, 0);
+}
+
+// The 32 columns of a row that the lanes l and l + 32 hold, to p, the first n of them.
+__device__ inline void store_row(__bf16 *p, const float (&f)[16], int fh, int n) {
+  uint32_t d[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t lo = __builtin_bit_cast(uint16_t, __bf16(f[2 * i])), hi = __builtin_bit_cast(uint16_t, __bf16(f[2 * i + 1]));
+    d[i] = lo | hi << 16;
+  }
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    // the lower lane takes the first of two runs of eight columns, the upper one the second
+    const auto a = __builtin_amdgcn_permlane32_swap(d[4 * g], d[4 * g + 2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(d[4 * g + 1], d[4 * g + 3], false, false);
+    Raw8<__bf16> r;
+    r.v = u32x4{uint32_t(a[0]), uint32_t(b[0]), uint32_t(a[1]), uint32_t(b[1])};
+    const int c = 16 * g + 8 * fh;
+    store8(p + c, r, n - c);
+  }
+}
+__device__ inline void store_row(float *p, const float (&f)[16], int fh, int n) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int c = 8 * g + 4 * fh;
+    if (n - c >= 4) {
+      *reinterpret_cast<u32x4_any *>(p + c) = u32x4{f32_bits(f[4 * g]), f32_bits(f[4 * g + 1]), f32_bits(f[4 * g + 2]), f32_bits(f[4 * g + 3])};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < n - c) p[c + e] = f[4 * g + e];
+    }
+  }
 }
 
 // The first min(n, 16 / sizeof(T)) elements at p, zeros behind them.
@@ -184,68 +247,90 @@ __device__ inline u32x4 load_chunk(const T *p, int n) {
   return v;
 }
 
-__device__ inline __amdgpu_buffer_rsrc_t whole(const void *p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, -1, 0x00020000);
+// Buffer resource over the 4 GiB from p (raw, untyped loads; the last dword is
+// the gfx9 default format).
+__device__ inline u32x4 whole(const void *p) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  return u32x4{uint32_t(__builtin_amdgcn_readfirstlane(int(at))), uint32_t(__builtin_amdgcn_readfirstlane(int(at >> 32) & 0xffff)),
+               0xffffffffu, 0x00020000u};
 }
-__device__ inline void to_lds(__amdgpu_buffer_rsrc_t r, char *lds, uint32_t voff, uint32_t soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, voff, soff, 0, 0);
+// 16 bytes a lane from the buffer straight to LDS (lane l's at lds + 16 l). In
+// assembly, because the compiler would wait for all of these loads before each
+// transposing LDS read; the waits that they need stand at the top of each step.
+// The wait states: one between m0 and the load, five from a vector instruction
+// that has written a scalar operand.
+__device__ inline void to_lds(const u32x4 &r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "memory");
 }
 
 // Where column col of row r of a backward product's weight tile lies in its
-// stage (bf16): rows of 256 columns in runs of 32, run i of row r at place
-// i ^ (r & 3) within its four, so that a transposing read, 32 columns of four
-// consecutive rows, takes four different quarters of the banks.
+// stage (bf16): rows of `wide` columns in runs of 32, run i of row r at place
+// i ^ (r & 3) within its four (of two, i ^ (r & 1)), so that a transposing
+// read, 32 columns of four consecutive rows, spreads over the banks.
+template <int kBN>
+__device__ inline int tr_run(int row, int run) {
+  return kBN >= 128 ? (run & ~3) | ((run ^ row) & 3) : run ^ (row & 1);
+}
+template <int kBN>
 __device__ inline int tr_at(int row, int col) {
-  const int run = col >> 5;
-  return row * (kTileN * 2) + (((run & ~3) | ((run ^ row) & 3)) << 6) + (col & 31) * 2;
+  return row * (kBN * 2) + (tr_run<kBN>(row, col >> 5) << 6) + (col & 31) * 2;
 }
 
 // kDirect: 16-byte loads straight to LDS. Needs operands whose rows start on
 // 16-byte boundaries, whole chunks in each row, and byte offsets below 2^32.
-template <typename T, int kWM, bool kBack, bool kGated, bool kDirect>
-__global__ __launch_bounds__(kWM * 256) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void product_kernel(const ProductArgs a) {
-  using F = Form<kWM>;
+template <typename T, class F, bool kBack, bool kGated, bool kDirect>
+__global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const ProductArgs a) {
   constexpr int kE = 16 / int(sizeof(T));            // elements of a chunk
   constexpr int kStep = kRowBytes / int(sizeof(T));  // sum indices of a step
   constexpr bool kBf16 = sizeof(T) == 2;
-  __shared__ __attribute__((aligned(1024))) char smem[F::kStages * F::kStage];
+  constexpr int kI = F::kI, kBN = F::kBN;
+  __shared__ __attribute__((aligned(1024))) char smem[F::kRing * F::kK];
 
   const int tid = int(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Tile t = find_tile(a, F::kBM, lane);
   if (t.group < 0) return;
   const int count = int(t.hi - t.lo);  // slots of the tile
-  const int n0 = t.n * (kGated ? kTileN / 2 : kTileN);
+  const int n0 = t.n * (kGated ? kBN / 2 : kBN);
   const T *w = static_cast<const T *>(a.w) + t.group * a.w_stride;
   const T *w2 = static_cast<const T *>(a.w2) + t.group * a.w2_stride;
 
   const int each = (a.k + kStep - 1) / kStep;  // steps of a part
   const int steps = kBack && a.x2 ? 2 * each : each;
 
-  const int wm = kWM == 1 ? 0 : wave >> 2, wn = wave & 3;
+  const int wk = F::kK == 1 ? 0 : wave, wm = F::kK > 1 ? 0 : wave / F::kWN, wn = F::kK > 1 ? 0 : wave % F::kWN;
   const int fr = lane & 31, fh = lane >> 5;
-  f32x16 acc[4][2];
+  // the wave's 32-row blocks i kWM + wm that have slots
+  const int live = __builtin_amdgcn_readfirstlane(((count + 31) / 32 - wm + F::kWM - 1) / F::kWM);
+  // its steps: all, or those of its part of the sum
+  const int share = (steps + F::kK - 1) / F::kK;
+  const int first = wk * share, last = first + share < steps ? first + share : steps;
+  char *ring = smem + wk * F::kRing;
+  f32x16 acc[kI][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kI; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
   // fragments: 64-byte rows of four chunks, chunk c at place c ^ (row >> 2 & 3)
-  const int fa = (wm * 128 + fr) * kRowBytes, fb = F::kABytes + (wn * 64 + fr) * kRowBytes, fx = (fr >> 2) & 3;
+  const int fa = (wm * 32 + fr) * kRowBytes, fb = F::kABytes + (wn * 64 + fr) * kRowBytes, fx = (fr >> 2) & 3;
   int tr[2] = {0, 0};
   if constexpr (kBack && kBf16) {
     // row 8 (lane / 32) + (lane % 16) / 4 (second read: four rows on), columns
     // 16 (lane / 16 % 2) + 4 (lane % 4) of a 32-column run
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      tr[j] = F::kABytes + tr_at(8 * fh + ((lane & 15) >> 2), wn * 64 + 32 * j + 16 * ((lane >> 4) & 1) + 4 * (lane & 3));
+      tr[j] = F::kABytes + tr_at<kBN>(8 * fh + ((lane & 15) >> 2), wn * 64 + 32 * j + 16 * ((lane >> 4) & 1) + 4 * (lane & 3));
   }
-  auto read_x = [&](const char *stage, int kk, u32x4 (&f)[4]) {
+  auto read_x = [&](const char *stage, int kk, u32x4 (&f)[kI], auto blocks) {
     const int ch = ((kk * 2 + fh) ^ fx) << 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const u32x4 *>(stage + fa + i * 32 * kRowBytes + ch);
+    for (int i = 0; i < decltype(blocks)::value; ++i)
+      f[i] = *reinterpret_cast<const u32x4 *>(stage + fa + i * F::kWM * 32 * kRowBytes + ch);
   };
   auto read_w = [&](const char *stage, int kk, u32x4 (&f)[2]) {
     if constexpr (!kBack) {
@@ -256,9 +341,9 @@ void product_kernel(const ProductArgs a) {
       typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const char *p = stage + tr[j] + kk * 16 * kTileN * 2;
+        const char *p = stage + tr[j] + kk * 16 * kBN * 2;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 4 * kTileN * 2));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 4 * kBN * 2));
         f[j] = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
       }
     } else {
@@ -266,192 +351,206 @@ void product_kernel(const ProductArgs a) {
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          f[j][e] = *reinterpret_cast<const uint32_t *>(stage + F::kABytes + (kk * 8 + fh * 4 + e) * kTileN * 4 +
+          f[j][e] = *reinterpret_cast<const uint32_t *>(stage + F::kABytes + (kk * 8 + fh * 4 + e) * kBN * 4 +
                                                         (wn * 64 + 32 * j + fr) * 4);
     }
   };
   // Zeros where the sum has ended: the tile of a part's last step is loaded whole.
-  auto cut = [&](int step, int kk, u32x4 (&x)[4], u32x4 (&v)[2]) {
+  auto cut = [&](int step, int kk, u32x4 (&x)[kI], u32x4 (&v)[2]) {
     const int at = (step >= each ? step - each : step) * kStep;
     if (at + kStep <= a.k) return;
     if (at + (kk * 2 + fh) * kE >= a.k) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = u32x4{0u, 0u, 0u, 0u};
+      for (int i = 0; i < kI; ++i) x[i] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
       for (int j = 0; j < 2; ++j) v[j] = u32x4{0u, 0u, 0u, 0u};
     }
   };
-  auto products = [&](const u32x4 (&x)[4], const u32x4 (&v)[2]) {
+  auto products = [&](const u32x4 (&x)[kI], const u32x4 (&v)[2], auto blocks) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < decltype(blocks)::value; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) multiply(acc[i][j], x[i], v[j], T());
   };
-  u32x4 xf[2][4], wf[2][2];
+  // f with the number of live blocks as a constant
+  auto with_blocks = [&](auto f) {
+    if (live <= 0)
+      f(std::integral_constant<int, 0>());
+    else if (kI == 1 || live == 1)
+      f(std::integral_constant<int, 1>());
+    else if (live == 2)
+      f(std::integral_constant<int, (kI < 2 ? kI : 2)>());
+    else if (live == 3)
+      f(std::integral_constant<int, (kI < 3 ? kI : 3)>());
+    else
+      f(std::integral_constant<int, kI>());
+  };
 
-  if (steps > 0) {
-    if constexpr (kDirect) {
-      // Waves 0..3 load: 2 kWM KiB of x and 4 KiB of the weights each, a KiB an instruction.
-      constexpr int kX = 2 * kWM;
-      const bool loader = wave < 4;
-      const T *xb = static_cast<const T *>(a.x), *xb2 = static_cast<const T *>(a.x2);
-      if (!a.gather) {
-        xb += t.lo * a.ld_x;
-        if (kBack && a.x2) xb2 += t.lo * a.ld_x;
-      }
-      const __amdgpu_buffer_rsrc_t rx = whole(xb), rx2 = whole(kBack && a.x2 ? xb2 : xb);
-      const __amdgpu_buffer_rsrc_t rw = whole(w), rw2 = whole(kGated || (kBack && a.x2) ? w2 : w);
-      uint32_t vx[kX], vw[4];
-      uint32_t cx[kX], cw[4];  // the chunk's first sum index within a step
-      if (loader) {
-#pragma unroll
-        for (int q = 0; q < kX; ++q) {
-          const int r = (wave * kX + q) * 16 + (lane >> 2);
-          const int c = (lane & 3) ^ ((r >> 2) & 3);
-          int64_t row = r < count ? r : count - 1;
-          if (a.gather) {
-            row = source_row(a, t.lo + row);
-            row = row < 0 ? 0 : row;
-          }
-          cx[q] = uint32_t(c * kE);
-          vx[q] = uint32_t(row * a.ld_x * int64_t(sizeof(T))) + uint32_t(c * 16);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if constexpr (!kBack) {
-            const int r = (wave * 4 + q) * 16 + (lane >> 2);
-            const int c = (lane & 3) ^ ((r >> 2) & 3);
-            int col = kGated ? n0 + 32 * wave + (q & 1) * 16 + (lane >> 2) : n0 + r;
-            col = col < a.n ? col : a.n - 1;
-            cw[q] = uint32_t(c * kE);
-            vw[q] = uint32_t(col * (kGated && q >= 2 ? a.ld_w2 : a.ld_w) * int64_t(sizeof(T))) + uint32_t(c * 16);
-          } else {
-            const int place = (wave * 4 + q) * 64 + lane;  // 16-byte places of the stage
-            int r, col;
-            if constexpr (kBf16) {
-              r = place >> 5;
-              const int run = (place & 31) >> 2;
-              col = ((run & ~3) | ((run ^ r) & 3)) * 32 + (place & 3) * 8;
-            } else {
-              r = place >> 6;
-              col = (place & 63) * 4;
-            }
-            col = n0 + col < a.n ? n0 + col : n0;
-            cw[q] = uint32_t(r);
-            vw[q] = uint32_t((r * a.ld_w + col) * int64_t(sizeof(T)));
-          }
-        }
-      }
-      auto load = [&](int step) {
-        if (!loader) return;
-        char *st = smem + (step % F::kStages) * F::kStage;
-        const bool second = kBack && step >= each;
-        const uint32_t at = uint32_t(second ? step - each : step) * kStep;
-        const uint32_t sx = at * uint32_t(sizeof(T));
-        const uint32_t sw = kBack ? uint32_t(at * a.ld_w * int64_t(sizeof(T))) : sx;
-        uint32_t ox[kX], ow[4];
-#pragma unroll
-        for (int q = 0; q < kX; ++q) ox[q] = vx[q];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ow[q] = vw[q];
-        if (at + kStep > uint32_t(a.k)) {  // chunks past the sum's end: the step's first
-#pragma unroll
-          for (int q = 0; q < kX; ++q) ox[q] -= at + cx[q] >= uint32_t(a.k) ? cx[q] * uint32_t(sizeof(T)) : 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            ow[q] -= at + cw[q] >= uint32_t(a.k) ? cw[q] * uint32_t(sizeof(T)) * (kBack ? uint32_t(a.ld_w) : 1u) : 0;
-        }
-#pragma unroll
-        for (int q = 0; q < kX; ++q) to_lds(second ? rx2 : rx, st + (wave * kX + q) * 1024, ox[q], sx);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          to_lds(second || (kGated && q >= 2) ? rw2 : rw, st + F::kABytes + (wave * 4 + q) * 1024, ow[q], sw);
-      };
-      // s_waitcnt with vmcnt alone constrained: the loads of `n` steps may be under way
-      auto landed = [&](int n) {
-        constexpr int kL = kX + 4;
-        if (!loader) return;
-        if (n >= 3)
-          __builtin_amdgcn_s_waitcnt((3 * kL & 15) | (3 * kL >> 4) << 14 | 0x0F70);
-        else if (n == 2)
-          __builtin_amdgcn_s_waitcnt((2 * kL & 15) | (2 * kL >> 4) << 14 | 0x0F70);
-        else if (n == 1)
-          __builtin_amdgcn_s_waitcnt((kL & 15) | (kL >> 4) << 14 | 0x0F70);
-        else
-          __builtin_amdgcn_s_waitcnt(0x0F70);
-      };
-      // Loads run kStages - 1 steps ahead of the products. At the top of step s
-      // the loads of the steps behind it stay under way; after the barrier, which
-      // every wave reaches with its reads of step s - 1 done, the stage of that
-      // step takes step s + kStages - 1.
-      constexpr int kAhead = F::kStages - 1;
-      for (int s = 0; s < kAhead && s < steps; ++s) load(s);
-#pragma unroll 1
-      for (int s = 0; s < steps; ++s) {
-        const int behind = steps - 1 - s;
-        if (behind >= kAhead - 1)
-          landed(kAhead - 1);
-        else if (kAhead > 2 && behind == 2)
-          landed(2);
-        else if (behind == 1)
-          landed(1);
-        else
-          landed(0);
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (s + kAhead < steps) load(s + kAhead);
-        const char *st = smem + (s % F::kStages) * F::kStage;
-        read_x(st, 0, xf[0]);
-        read_w(st, 0, wf[0]);
-        if (s) products(xf[1], wf[1]);
-        read_x(st, 1, xf[1]);
-        read_w(st, 1, wf[1]);
-        cut(s, 0, xf[0], wf[0]);
-        products(xf[0], wf[0]);
-        cut(s, 1, xf[1], wf[1]);
-      }
-      products(xf[1], wf[1]);
-    } else {
-      // Through registers: any alignment and width.
-      constexpr int kX = F::kBM * 4 / F::kThreads, kW = 1024 / F::kThreads;
-      const T *px[kX], *px2[kX];
-      int cx[kX];
+  if constexpr (kDirect) {
+    constexpr int kX = F::kX, kW = F::kW, kAhead = F::kStages - 1;
+    const bool loader = F::kK > 1 || wave < F::kLoaders;
+    const int lw = F::kK > 1 ? 0 : wave;
+    const T *xb = static_cast<const T *>(a.x), *xb2 = static_cast<const T *>(a.x2);
+    if (!a.gather) {
+      xb += t.lo * a.ld_x;
+      if (kBack && a.x2) xb2 += t.lo * a.ld_x;
+    }
+    const u32x4 rx = whole(xb), rx2 = whole(kBack && a.x2 ? xb2 : xb);
+    const u32x4 rw = whole(w), rw2 = whole(kGated || (kBack && a.x2) ? w2 : w);
+    uint32_t vx[kX], vw[kW];
+    uint32_t cx[kX], cw[kW];  // the chunk's first sum index within a step
+    if (loader && first < last) {
 #pragma unroll
       for (int q = 0; q < kX; ++q) {
-        const int place = q * F::kThreads + tid, r = place >> 2;
-        int64_t row = t.lo + (r < count ? r : count - 1);
-        if (a.gather) row = source_row(a, row);
-        row = row < 0 ? 0 : row;
-        cx[q] = ((place & 3) ^ ((r >> 2) & 3)) * kE;
-        px[q] = static_cast<const T *>(a.x) + row * a.ld_x + cx[q];
-        px2[q] = kBack ? static_cast<const T *>(a.x2) + row * a.ld_x2 + cx[q] : nullptr;
-      }
-      u32x4 hx[kX], hw[kW];
-      auto fetch = [&](int step) {
-        const bool second = kBack && step >= each;
-        const int at = (second ? step - each : step) * kStep;
-#pragma unroll
-        for (int q = 0; q < kX; ++q) hx[q] = load_chunk((second ? px2[q] : px[q]) + at, a.k - at - cx[q]);
-#pragma unroll
-        for (int q = 0; q < kW; ++q) {
-          const int place = q * F::kThreads + tid;
-          if constexpr (!kBack) {
-            const int r = place >> 2, c = ((place & 3) ^ ((r >> 2) & 3)) * kE;
-            const bool up = kGated && (r >> 5 & 1);
-            const int col = kGated ? n0 + 32 * (r >> 6) + (r & 31) : n0 + r;
-            const T *p = up ? w2 + col * a.ld_w2 : w + col * a.ld_w;
-            hw[q] = load_chunk(p + at + c, col < a.n ? a.k - at - c : 0);
-          } else {
-            const int r = kBf16 ? place >> 5 : place >> 6;
-            const int run = (place & 31) >> 2;
-            const int col = n0 + (kBf16 ? ((run & ~3) | ((run ^ r) & 3)) * 32 + (place & 3) * 8 : (place & 63) * 4);
-            const T *p = second ? w2 + (at + r) * a.ld_w2 : w + (at + r) * a.ld_w;
-            hw[q] = load_chunk(p + col, at + r < a.k ? a.n - col : 0);
-          }
+        const int r = (lw * kX + q) * 16 + (lane >> 2);
+        const int c = (lane & 3) ^ ((r >> 2) & 3);
+        int64_t row = r < count ? r : count - 1;
+        if (a.gather) {
+          row = source_row(a, t.lo + row);
+          row = row < 0 ? 0 : row;
         }
-      };
-      fetch(0);
+        cx[q] = uint32_t(c * kE);
+        vx[q] = uint32_t(row * a.ld_x * int64_t(sizeof(T))) + uint32_t(c * 16);
+      }
+#pragma unroll
+      for (int q = 0; q < kW; ++q) {
+        if constexpr (!kBack) {
+          const int r = (lw * kW + q) * 16 + (lane >> 2);
+          const int c = (lane & 3) ^ ((r >> 2) & 3);
+          int col = kGated ? n0 + (r >> 6) * 32 + (r & 31) : n0 + r;
+          col = col < a.n ? col : a.n - 1;
+          cw[q] = uint32_t(c * kE);
+          vw[q] = uint32_t(col * (kGated && (r & 32) ? a.ld_w2 : a.ld_w) * int64_t(sizeof(T))) + uint32_t(c * 16);
+        } else {
+          const int place = (lw * kW + q) * 64 + lane;  // 16-byte places of the stage
+          constexpr int kPlaces = kBN * int(sizeof(T)) / 16;  // of a row
+          const int r = place / kPlaces, in = place % kPlaces;
+          int col = kBf16 ? tr_run<kBN>(r, in >> 2) * 32 + (in & 3) * 8 : in * 4;
+          col = n0 + col < a.n ? n0 + col : n0;
+          cw[q] = uint32_t(r);
+          vw[q] = uint32_t((r * a.ld_w + col) * int64_t(sizeof(T)));
+        }
+      }
+    }
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(
+        int(uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)smem)) + wk * F::kRing));
+    auto load = [&](int step, uint32_t stage) {  // stage: where it begins in the ring
+      if (!loader) return;
+      const uint32_t st = lds + stage;
+      const bool second = kBack && step >= each;
+      const uint32_t at = uint32_t(second ? step - each : step) * kStep;
+      const uint32_t sx = at * uint32_t(sizeof(T));
+      const uint32_t sw = kBack ? uint32_t(at * a.ld_w * int64_t(sizeof(T))) : sx;
+      uint32_t ox[kX], ow[kW];
+#pragma unroll
+      for (int q = 0; q < kX; ++q) ox[q] = vx[q];
+#pragma unroll
+      for (int q = 0; q < kW; ++q) ow[q] = vw[q];
+      if (at + kStep > uint32_t(a.k)) {  // chunks past the sum's end: the step's first
+#pragma unroll
+        for (int q = 0; q < kX; ++q) ox[q] -= at + cx[q] >= uint32_t(a.k) ? cx[q] * uint32_t(sizeof(T)) : 0;
+#pragma unroll
+        for (int q = 0; q < kW; ++q)
+          ow[q] -= at + cw[q] >= uint32_t(a.k) ? cw[q] * uint32_t(sizeof(T)) * (kBack ? uint32_t(a.ld_w) : 1u) : 0;
+      }
+#pragma unroll
+      for (int q = 0; q < kX; ++q) to_lds(second ? rx2 : rx, st + (lw * kX + q) * 1024, ox[q], sx);
+#pragma unroll
+      for (int q = 0; q < kW; ++q) {
+        // 16 rows a load: of one of the gated block's products
+        const bool other = second || (kGated && ((lw * kW + q) & 2));
+        to_lds(other ? rw2 : rw, st + F::kABytes + (lw * kW + q) * 1024, ow[q], sw);
+      }
+    };
+    // s_waitcnt with vmcnt alone constrained: the loads of `n` steps may be under way
+    auto landed = [&](int n) {
+      constexpr int kL = kX + kW;
+      static_assert(kL * (kAhead - 1) < 64 && kAhead <= 4);
+      if (!loader) return;
+      if (n >= 3 && kAhead > 3)
+        __builtin_amdgcn_s_waitcnt((3 * kL & 15) | (3 * kL >> 4) << 14 | 0x0F70);
+      else if (n >= 2 && kAhead > 2)
+        __builtin_amdgcn_s_waitcnt((2 * kL & 15) | (2 * kL >> 4) << 14 | 0x0F70);
+      else if (n >= 1)
+        __builtin_amdgcn_s_waitcnt((kL & 15) | (kL >> 4) << 14 | 0x0F70);
+      else
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+    };
+    // Loads run kStages - 1 steps ahead of the products. At the top of step s
+    // the loads of the steps behind it stay under way; after the barrier, which
+    // every wave reaches with its reads of step s - 1 done, the stage of that
+    // step takes step s + kStages - 1. A ring of one wave needs no barrier.
+    with_blocks([&](auto blocks) {
+      u32x4 xf[2][kI], wf[2][2];
+      for (int s = 0; s < kAhead && first + s < last; ++s) load(first + s, uint32_t(s * F::kStage));
+      uint32_t here = 0, there = kAhead * F::kStage;  // the stages of step s and of the step that is loaded
+#pragma unroll 1
+      for (int s = first; s < last; ++s) {
+        landed(last - 1 - s);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        if constexpr (F::kK == 1) __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (s + kAhead < last) load(s + kAhead, there);
+        const char *st = ring + here;
+        there = here;
+        here = here == (F::kStages - 1) * F::kStage ? 0 : here + F::kStage;
+        if constexpr (decltype(blocks)::value > 0) {
+          read_x(st, 0, xf[0], blocks);
+          read_w(st, 0, wf[0]);
+          if (s > first) products(xf[1], wf[1], blocks);
+          read_x(st, 1, xf[1], blocks);
+          read_w(st, 1, wf[1]);
+          cut(s, 0, xf[0], wf[0]);
+          products(xf[0], wf[0], blocks);
+          cut(s, 1, xf[1], wf[1]);
+        }
+      }
+      if constexpr (decltype(blocks)::value > 0)
+        if (first < last) products(xf[1], wf[1], blocks);
+    });
+  } else {
+    // Through registers: any alignment and width.
+    static_assert(F::kK == 1);
+    constexpr int kX = F::kABytes / 16 / F::kThreads, kW = kBN * kRowBytes / 16 / F::kThreads;
+    const T *px[kX], *px2[kX];
+    int cx[kX];
+#pragma unroll
+    for (int q = 0; q < kX; ++q) {
+      const int place = q * F::kThreads + tid, r = place >> 2;
+      int64_t row = t.lo + (r < count ? r : count - 1);
+      if (a.gather) row = source_row(a, row);
+      row = row < 0 ? 0 : row;
+      cx[q] = ((place & 3) ^ ((r >> 2) & 3)) * kE;
+      px[q] = static_cast<const T *>(a.x) + row * a.ld_x + cx[q];
+      px2[q] = kBack ? static_cast<const T *>(a.x2) + row * a.ld_x2 + cx[q] : nullptr;
+    }
+    u32x4 hx[kX], hw[kW];
+    auto fetch = [&](int step) {
+      const bool second = kBack && step >= each;
+      const int at = (second ? step - each : step) * kStep;
+#pragma unroll
+      for (int q = 0; q < kX; ++q) hx[q] = load_chunk((second ? px2[q] : px[q]) + at, a.k - at - cx[q]);
+#pragma unroll
+      for (int q = 0; q < kW; ++q) {
+        const int place = q * F::kThreads + tid;
+        if constexpr (!kBack) {
+          const int r = place >> 2, c = ((place & 3) ^ ((r >> 2) & 3)) * kE;
+          const bool up = kGated && (r & 32);
+          const int col = kGated ? n0 + (r >> 6) * 32 + (r & 31) : n0 + r;
+          const T *p = up ? w2 + col * a.ld_w2 : w + col * a.ld_w;
+          hw[q] = load_chunk(p + at + c, col < a.n ? a.k - at - c : 0);
+        } else {
+          constexpr int kPlaces = kBN * int(sizeof(T)) / 16;
+          const int r = place / kPlaces, in = place % kPlaces;
+          const int col = n0 + (kBf16 ? tr_run<kBN>(r, in >> 2) * 32 + (in & 3) * 8 : in * 4);
+          const T *p = second ? w2 + (at + r) * a.ld_w2 : w + (at + r) * a.ld_w;
+          hw[q] = load_chunk(p + col, at + r < a.k ? a.n - col : 0);
+        }
+      }
+    };
+    if (steps > 0) fetch(0);
+    with_blocks([&](auto blocks) {
+      u32x4 xf[2][kI], wf[2][2];
 #pragma unroll 1
       for (int s = 0; s < steps; ++s) {
         char *st = smem + (s & 1) * F::kStage;
@@ -461,74 +560,97 @@ void product_kernel(const ProductArgs a) {
         for (int q = 0; q < kW; ++q) *reinterpret_cast<u32x4 *>(st + F::kABytes + (q * F::kThreads + tid) * 16) = hw[q];
         __syncthreads();
         if (s + 1 < steps) fetch(s + 1);
+        if constexpr (decltype(blocks)::value > 0) {
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          read_x(st, kk, xf[kk]);
-          read_w(st, kk, wf[kk]);
-          products(xf[kk], wf[kk]);
+          for (int kk = 0; kk < 2; ++kk) {
+            read_x(st, kk, xf[kk], blocks);
+            read_w(st, kk, wf[kk]);
+            products(xf[kk], wf[kk], blocks);
+          }
         }
       }
-    }
+    });
   }
 
-  // Epilogue: 32 rows of the wave's 64 columns at a time through LDS, so that
-  // a row leaves in runs of eight columns. Accumulator r of a lane is row
-  // 8 (r / 4) + 4 (lane / 32) + r % 4, column lane % 32.
-  __syncthreads();
-  float *buf = reinterpret_cast<float *>(smem) + wave * 32 * kOutPitch;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  if constexpr (F::kK > 1) {
+    // The waves of a sum add up through LDS, a quarter of the rows' columns each
+    // at first: then every wave holds them all again, and stores what is its own.
+    __syncthreads();
+    f32x4v *part = reinterpret_cast<f32x4v *>(smem);
+    static_assert(F::kK == 4 && kI == 1 && F::kWaves * 8192 <= F::kRing * F::kK);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        buf[(8 * (r >> 2) + 4 * fh + (r & 3)) * kOutPitch + 32 * j + fr] = acc[i][j][r];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    constexpr int kRuns = kGated ? 4 : 8;  // of eight columns in a row
+      for (int g = 0; g < 4; ++g)
+        part[((wk * 2 + j) * 4 + g) * 64 + lane] =
+            f32x4v{acc[0][j][4 * g], acc[0][j][4 * g + 1], acc[0][j][4 * g + 2], acc[0][j][4 * g + 3]};
+    __syncthreads();
+    if (wk >= (kGated ? 1 : 2)) return;  // a wave for 32 columns of the output
 #pragma unroll
-    for (int q = 0; q < kRuns / 2; ++q) {
-      const int row = (q * 64 + lane) / kRuns, col = (lane & (kRuns - 1)) * 8;
-      const int at = wm * 128 + i * 32 + row;
-      const int c = n0 + (kGated ? 32 : 64) * wn + col;
-      if (at >= count || c >= a.n) continue;
-      const int64_t s = t.lo + at;
-      const bool there = source_row(a, s) >= 0;
-      float f[8];
+    for (int j = 0; j < 2; ++j) {
+      if (!kGated && j != wk) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = there ? buf[row * kOutPitch + col + e] : 0.f;
-      if constexpr (kGated) {
-        float u[8], h[8];
+      for (int g = 0; g < 4; ++g) {
+        f32x4v v = part[(j * 4 + g) * 64 + lane];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          u[e] = there ? buf[row * kOutPitch + 32 + col + e] : 0.f;
-          float slope;
-          h[e] = act_value(f[e], a.act, slope) * u[e];
-        }
-        store8(static_cast<T *>(a.out) + s * a.ld_out + c, pack8(h, T()), a.n - c);
-        if (a.gate) store8(static_cast<T *>(a.gate) + s * a.ld_gate + c, pack8(f, T()), a.n - c);
-        if (a.up) store8(static_cast<T *>(a.up) + s * a.ld_up + c, pack8(u, T()), a.n - c);
-      } else {
-        const int64_t to = a.scatter ? a.rows[s] : s;
-        if (to >= 0 && to < a.out_rows) store8(static_cast<T *>(a.out) + to * a.ld_out + c, pack8(f, T()), a.n - c);
+        for (int p = 1; p < F::kK; ++p) v += part[((p * 2 + j) * 4 + g) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0][j][4 * g + e] = v[e];
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+  }
+#pragma unroll
+  for (int i = 0; i < kI; ++i) {
+    if (i >= live) break;
+    const int at = (i * F::kWM + wm) * 32 + fr;
+    // the swaps of store_row need both lanes of a row; these have the same row
+    const int64_t s = t.lo + (at < count ? at : count - 1);
+    const bool there = source_row(a, s) >= 0;
+    if constexpr (kGated) {
+      const int c = n0 + 32 * wn;
+      float g[16], u[16], h[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        g[r] = there ? acc[i][0][r] : 0.f;
+        u[r] = there ? acc[i][1][r] : 0.f;
+        float slope;
+        h[r] = act_value(g[r], a.act, slope) * u[r];
+      }
+      const int n = at < count ? a.n - c : 0;
+      store_row(static_cast<T *>(a.out) + s * a.ld_out + c, h, fh, n);
+      if (a.gate) store_row(static_cast<T *>(a.gate) + s * a.ld_gate + c, g, fh, n);
+      if (a.up) store_row(static_cast<T *>(a.up) + s * a.ld_up + c, u, fh, n);
+    } else {
+      const int64_t to = a.scatter ? a.rows[s] : s;
+      const bool put = at < count && to >= 0 && to < a.out_rows;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (F::kK > 1 && j != wk) continue;
+        const int c = n0 + 64 * wn + 32 * j;
+        float f[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) f[r] = there ? acc[i][j][r] : 0.f;
+        store_row(static_cast<T *>(a.out) + (put ? to : 0) * a.ld_out + c, f, fh, put ? a.n - c : 0);
+      }
+    }
   }
 }
 
-template <typename T, int kWM, bool kDirect>
+int64_t row_tiles(const ProductArgs &a, int rows) {  // at most: a group's last one may be a part of a tile
+  return a.slots / rows + std::min<int64_t>(a.offsets ? a.groups : 1, a.slots);
+}
+int tiles_across(const ProductArgs &a, int cols) {
+  const int wide = a.w2 && !a.back ? cols / 2 : cols;
+  return (a.n + wide - 1) / wide;
+}
+
+template <typename T, class F, bool kDirect>
 void tiled(ProductArgs a, hipStream_t s) {
-  using F = Form<kWM>;
-  const int wide = a.w2 && !a.back ? kTileN / 2 : kTileN;
-  a.tiles_n = int32_t((a.n + wide - 1) / wide);
-  // a group's last tile may be a part of one
-  const int64_t rows = a.slots / F::kBM + std::min<int64_t>(a.offsets ? a.groups : 1, a.slots);
-  const int64_t most = 1 << 20, blocks = (rows * a.tiles_n + 7) / 8 * 8;
+  a.tiles_n = tiles_across(a, F::kBN);
+  const int64_t most = 1 << 20, blocks = (row_tiles(a, F::kBM) * a.tiles_n + 7) / 8 * 8;
   const dim3 grid(unsigned(std::min(blocks, most)), unsigned((blocks + most - 1) / most));
-  auto kernel = a.back ? product_kernel<T, kWM, true, false, kDirect>
-                : a.w2 ? product_kernel<T, kWM, false, true, kDirect> : product_kernel<T, kWM, false, false, kDirect>;
+  auto kernel = a.back ? product_kernel<T, F, true, false, kDirect>
+                : a.w2 ? product_kernel<T, F, false, true, kDirect> : product_kernel<T, F, false, false, kDirect>;
   hipLaunchKernelGGL(kernel, grid, dim3(F::kThreads), 0, s, a);
 }
 
@@ -548,12 +670,21 @@ bool direct(const ProductArgs &a, int64_t size) {
 
 template <typename T>
 hipError_t product(const ProductArgs &a, hipStream_t s) {
-  if (!direct(a, sizeof(T)))
-    tiled<T, 1, false>(a, s);
-  else if (a.slots >= 1024 * int64_t(a.offsets ? a.groups : 1))
-    tiled<T, 2, true>(a, s);
+  const int64_t each = a.slots / (a.offsets ? a.groups : 1);
+  const bool lds = direct(a, sizeof(T));
+  const bool few = row_tiles(a, 128) * tiles_across(a, 256) < 512;
+  if (!lds && few)
+    tiled<T, Small, false>(a, s);
+  else if (!lds)
+    tiled<T, Wide, false>(a, s);
+  else if (each <= 16)
+    tiled<T, Thin, true>(a, s);
+  else if (few)
+    tiled<T, Small, true>(a, s);
+  else if (each >= 1024)
+    tiled<T, Large, true>(a, s);
   else
-    tiled<T, 1, true>(a, s);
+    tiled<T, Wide, true>(a, s);
   return hipGetLastError();
 }
 
