@@ -528,7 +528,7 @@ muon_status muon_expert_backward(const muon_mat *dy, const muon_mat *w, int64_t 
  *             (residual NULL-able: 0).
  *   weights   tokens x topk float32, contiguous (NULL-able: 1).
  *   indices   tokens x topk int32, contiguous: a choice below 0 adds nothing,
- *             its row of x is not read (NULL-able: every choice counts).
+ *             whatever its row of x holds (NULL-able: every choice counts).
  *   drop(v)   element i (in row order, columns of the matrix, not its pitch)
  *             is v / (1 - p) where word i mod 4 of Philox4x32-10's block is >=
  *             floor(p 2^32), else 0: counter {i / 4, offset} (64 bits each, the

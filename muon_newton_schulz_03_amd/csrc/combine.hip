@@ -11,7 +11,12 @@
 // counts for nothing, whatever its value.
 //
 // Memory bounds both: each row of x moves once, and dy once for all of a
-// token's slots.
+// token's slots. A thread takes eight columns of a token; the loads of all its
+// rows go out before the generator's words are worked out, and what does not
+// count is masked afterwards: a branch per row would have the loads wait for each
+// other. The last run of a row starts eight columns before its end, whatever the
+// width, so that every run is whole; columns that two threads hold get the same
+// value from both.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -23,7 +28,6 @@ namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAtOnce = 8;  // rows of a token whose loads are under way together
 
 // Four words of one counter block.
 __device__ inline u32x4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
@@ -57,49 +61,88 @@ __device__ inline uint32_t kept8(uint64_t first, uint64_t offset, uint64_t seed,
   return bits >> skip;
 }
 
-// kPerRow threads make a row (of 256; from 64 on whole waves, so that what
-// belongs to a token is scalar), kThreads / kPerRow rows a workgroup.
-template <int kPerRow>
-__device__ inline int64_t first_token() {
-  int64_t t = int64_t(blockIdx.x) * (kThreads / kPerRow) + int(threadIdx.x) / kPerRow;
-  if constexpr (kPerRow >= 64) t = int64_t(blockIdx.x) * (kThreads / kPerRow) + __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kPerRow);
-  return t;
+// A thread's run of columns: kPerRow threads make a row, kThreads / kPerRow rows
+// a workgroup.
+struct Run {
+  int c, own;  // first column; the first of the eight that no earlier run holds
+};
+__device__ inline Run run_at(int c, int cols) {
+  const int last = cols > 8 ? cols - 8 : 0;
+  return {c < last ? c : last, c < last ? 0 : c - last};
+}
+// kTiny: rows of fewer than eight columns.
+template <bool kTiny, typename T>
+__device__ inline Raw8<T> load_run(const T *p, int cols) {
+  return kTiny ? load8(p, cols) : load8(p, 8);
+}
+template <bool kTiny, typename T>
+__device__ inline void store_run(T *p, const float (&f)[8], int cols) {
+  store8(p, pack8(f, T()), kTiny ? cols : 8);
+}
+__device__ inline void keep(Raw8<__bf16> &r, uint32_t mask) { r.v &= mask; }
+__device__ inline void keep(Raw8<float> &r, uint32_t mask) {
+  r.v[0] &= mask;
+  r.v[1] &= mask;
 }
 
-template <typename T, int kPerRow>
+// The slot of a token's choice j (past its last one: that).
+template <int kJ>
+__device__ inline int64_t slot_of(const CombineArgs &a, int64_t t, int j) {
+  return t * a.topk + (kJ == 1 || j < a.topk ? j : a.topk - 1);
+}
+// Weights and indices of kJ choices, all loads of one list out together.
+template <int kJ>
+__device__ inline void choices(const CombineArgs &a, int64_t t, int j0, float (&w)[kJ], int32_t (&idx)[kJ]) {
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
+    w[j] = 1.f;
+    idx[j] = 0;
+  }
+  if (a.weights) {
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) w[j] = a.weights[slot_of<kJ>(a, t, j0 + j)];
+  }
+  if (a.indices) {
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) idx[j] = a.indices[slot_of<kJ>(a, t, j0 + j)];
+  }
+}
+
+// kJ: rows of a token whose loads are under way together.
+template <typename T, int kPerRow, int kJ, bool kTiny>
 __global__ __launch_bounds__(kThreads) void combine_fwd_kernel(const CombineArgs a) {
   const bool drop = a.key != nullptr;
   const uint64_t seed = drop ? a.key[0] : 0, offset = drop ? a.key[1] : 0;
-  for (int64_t t = first_token<kPerRow>(); t < a.tokens; t += int64_t(gridDim.x) * (kThreads / kPerRow)) {
-    for (int c = (int(threadIdx.x) % kPerRow + int(blockIdx.y) * kPerRow) * 8; c < a.cols; c += int(gridDim.y) * kPerRow * 8) {
-      const int left = a.cols - c;
+  constexpr int kRows = kThreads / kPerRow;
+  const T *xs = static_cast<const T *>(a.x);
+  for (int64_t t = int64_t(blockIdx.x) * kRows + int(threadIdx.x) / kPerRow; t < a.tokens; t += int64_t(gridDim.x) * kRows) {
+    for (int c0 = (int(threadIdx.x) % kPerRow + int(blockIdx.y) * kPerRow) * 8; c0 < a.cols; c0 += int(gridDim.y) * kPerRow * 8) {
+      const int c = run_at(c0, a.cols).c;
       Raw8<T> res{};
-      if (a.res) res = load8(static_cast<const T *>(a.res) + t * a.ld_res + c, left);
-      const uint32_t kept = drop ? kept8(uint64_t(t) * uint64_t(a.cols) + c, offset, seed, a.threshold) : 255u;
+      if (a.res) res = load_run<kTiny>(static_cast<const T *>(a.res) + t * a.ld_res + c, a.cols);
       float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int j0 = 0; j0 < a.topk; j0 += kAtOnce) {
-        Raw8<T> x[kAtOnce];
-        float w[kAtOnce];
+      uint32_t kept = 255u;
+      for (int j0 = 0; j0 < a.topk; j0 += kJ) {
+        Raw8<T> x[kJ];
+        float w[kJ];
+        int32_t idx[kJ];
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          const int64_t slot = t * a.topk + j0 + j;
-          const bool there = j0 + j < a.topk && (!a.indices || a.indices[slot] >= 0);
-          x[j] = Raw8<T>{};
-          w[j] = 0.f;
-          if (there) {
-            x[j] = load8(static_cast<const T *>(a.x) + slot * a.ld_x + c, left);
-            w[j] = a.weights ? a.weights[slot] : 1.f;
-          }
-        }
+        for (int j = 0; j < kJ; ++j) x[j] = load_run<kTiny>(xs + slot_of<kJ>(a, t, j0 + j) * a.ld_x + c, a.cols);
+        choices(a, t, j0, w, idx);
+        if (drop && j0 == 0) kept = kept8(uint64_t(t) * uint64_t(a.cols) + c, offset, seed, a.threshold);
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)
+        for (int j = 0; j < kJ; ++j) {
+          const bool there = idx[j] >= 0 && (kJ == 1 || j0 + j < a.topk);
+          keep(x[j], there ? ~0u : 0u);
+          w[j] = there ? w[j] : 0.f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) sum[e] = fmaf(w[j], x[j].get(e), sum[e]);
+        }
       }
       float y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = res.get(e) + (kept >> e & 1 ? sum[e] * a.scale : 0.f);
-      store8(static_cast<T *>(a.out) + t * a.ld_out + c, pack8(y, T()), left);
+      store_run<kTiny>(static_cast<T *>(a.out) + t * a.ld_out + c, y, a.cols);
     }
   }
 }
@@ -113,73 +156,88 @@ __global__ __launch_bounds__(kThreads) void places_kernel(const CombineArgs a) {
   }
 }
 
-template <typename T, int kPerRow>
+template <typename T, int kPerRow, int kJ, bool kTiny>
 __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(const CombineArgs a) {
-  constexpr int kWaves = kPerRow / 64;  // of a row
-  __shared__ float part[kThreads / 64][kAtOnce];
+  constexpr int kWaves = kPerRow / 64, kRows = kThreads / kPerRow;  // waves of a row, rows of a workgroup
+  __shared__ float part[kThreads / 64][kJ];
   const bool drop = a.key != nullptr;
   const uint64_t seed = drop ? a.key[0] : 0, offset = drop ? a.key[1] : 0;
-  const int64_t slots = a.tokens * a.topk, step = int64_t(gridDim.x) * (kThreads / kPerRow);
-  const int64_t own = first_token<kPerRow>();
-  for (int64_t t0 = int64_t(blockIdx.x) * (kThreads / kPerRow); t0 < a.tokens; t0 += step) {  // the workgroup's waves stay together
-    const int64_t t = own + (t0 - int64_t(blockIdx.x) * (kThreads / kPerRow));
-    const bool live = t < a.tokens;
-    for (int j0 = 0; j0 < a.topk; j0 += kAtOnce) {
-      int64_t to[kAtOnce];  // row of dx, -1: none
-      float w[kAtOnce], dot[kAtOnce];
-      bool there[kAtOnce];
+  const int64_t slots = a.tokens * a.topk;
+  const T *xs = static_cast<const T *>(a.x);
+  // the waves of a workgroup stay together; rows past the last repeat it and write nothing
+  for (int64_t t0 = int64_t(blockIdx.x) * kRows; t0 < a.tokens; t0 += int64_t(gridDim.x) * kRows) {
+    const int64_t at = t0 + int(threadIdx.x) / kPerRow;
+    const bool live = at < a.tokens;
+    const int64_t t = live ? at : a.tokens - 1;
+    for (int j0 = 0; j0 < a.topk; j0 += kJ) {
+      // a run's loads go out before what the run before it, or the token's lists, need
+      Raw8<T> dy, x[kJ];
+      auto load = [&](int c0) {
+        const int c = run_at(c0, a.cols).c;
+        dy = load_run<kTiny>(static_cast<const T *>(a.dy) + t * a.ld_dy + c, a.cols);
+        if (a.dweights) {
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int64_t slot = t * a.topk + j0 + j;
-        there[j] = live && j0 + j < a.topk && (!a.indices || a.indices[slot] >= 0);
-        dot[j] = w[j] = 0.f;
-        to[j] = -1;
-        if (there[j]) {
-          w[j] = a.weights ? a.weights[slot] : 1.f;
-          to[j] = slot;
-          if (a.rows) {  // a slot that rows does not hold has found no place: its entry is whatever was there
-            const int32_t p = a.places[slot];
-            to[j] = p >= 0 && p < slots && a.rows[p] == int32_t(slot) ? p : -1;
+          for (int j = 0; j < kJ; ++j) x[j] = load_run<kTiny>(xs + slot_of<kJ>(a, t, j0 + j) * a.ld_x + c, a.cols);
+        }
+      };
+      const int begin = int(threadIdx.x) % kPerRow * 8;
+      load(begin < a.cols ? begin : 0);
+      int32_t to[kJ], idx[kJ];  // row of dx, -1: none
+      float w[kJ], dot[kJ];
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        to[j] = int32_t(slot_of<kJ>(a, t, j0 + j));
+        dot[j] = 0.f;
+      }
+      choices(a, t, j0, w, idx);
+      if (a.rows) {  // a slot that rows does not hold has found no place: its entry is whatever was there
+        int32_t back[kJ];
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) to[j] = a.places[to[j]];
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) back[j] = a.rows[to[j] >= 0 && to[j] < slots ? to[j] : 0];
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+          to[j] = to[j] >= 0 && to[j] < slots && back[j] == int32_t(slot_of<kJ>(a, t, j0 + j)) ? to[j] : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const bool there = live && idx[j] >= 0 && (kJ == 1 || j0 + j < a.topk);
+        idx[j] = there ? 0 : -1;
+        to[j] = there ? to[j] : -1;
+      }
+      for (int c0 = begin; c0 < a.cols; c0 += kPerRow * 8) {
+        const Run run = run_at(c0, a.cols);
+        const uint32_t kept = drop ? kept8(uint64_t(t) * uint64_t(a.cols) + run.c, offset, seed, a.threshold) : 255u;
+        float d[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] = kept >> e & 1 ? dy.get(e) * a.scale : 0.f;
+        if (a.dweights) {
+          const uint32_t counts = kept & 255u << run.own;
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            keep(x[j], idx[j] >= 0 ? ~0u : 0u);
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += counts >> e & 1 ? x[j].get(e) * d[e] : 0.f;
+            dot[j] += s;
           }
         }
-      }
-      if (live) {
-        for (int c = int(threadIdx.x) % kPerRow * 8; c < a.cols; c += kPerRow * 8) {
-          const int left = a.cols - c;
-          const Raw8<T> dy = load8(static_cast<const T *>(a.dy) + t * a.ld_dy + c, left);
-          Raw8<T> x[kAtOnce];
-          if (a.dweights) {
+        if (c0 + kPerRow * 8 < a.cols) load(c0 + kPerRow * 8);
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-              x[j] = Raw8<T>{};
-              if (there[j]) x[j] = load8(static_cast<const T *>(a.x) + (t * a.topk + j0 + j) * a.ld_x + c, left);
-            }
-          }
-          const uint32_t kept = drop ? kept8(uint64_t(t) * uint64_t(a.cols) + c, offset, seed, a.threshold) : 255u;
-          float d[8];
+        for (int j = 0; j < kJ; ++j) {
+          if (to[j] >= 0) {
+            float v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] = kept >> e & 1 ? dy.get(e) * a.scale : 0.f;
-#pragma unroll
-          for (int j = 0; j < kAtOnce; ++j) {
-            if (a.dweights) {
-              float s = 0.f;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) s += kept >> e & 1 ? x[j].get(e) * d[e] : 0.f;
-              dot[j] += s;
-            }
-            if (to[j] >= 0) {
-              float v[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = w[j] * d[e];
-              store8(static_cast<T *>(a.out) + to[j] * a.ld_out + c, pack8(v, T()), left);
-            }
+            for (int e = 0; e < 8; ++e) v[e] = w[j] * d[e];
+            store_run<kTiny>(static_cast<T *>(a.out) + int64_t(to[j]) * a.ld_out + run.c, v, a.cols);
           }
         }
       }
       if (!a.dweights) continue;
       // sums over the row's threads
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
+      for (int j = 0; j < kJ; ++j) {
         if constexpr (kPerRow >= 64) {
           dot[j] = wave_sum(dot[j]);
         } else {
@@ -192,11 +250,11 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(const CombineArgs
         __syncthreads();
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-          for (int j = 0; j < kAtOnce; ++j) part[wave][j] = dot[j];
+          for (int j = 0; j < kJ; ++j) part[wave][j] = dot[j];
         }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
+        for (int j = 0; j < kJ; ++j) {
           dot[j] = 0.f;
 #pragma unroll
           for (int i = 0; i < kWaves; ++i) dot[j] += part[wave / kWaves * kWaves + i][j];
@@ -204,65 +262,61 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(const CombineArgs
       }
       if (live && int(threadIdx.x) % kPerRow == 0) {
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)
-          if (j0 + j < a.topk) a.dweights[t * a.topk + j0 + j] = there[j] ? dot[j] : 0.f;
+        for (int j = 0; j < kJ; ++j)
+          if (j0 + j < a.topk) a.dweights[t * a.topk + j0 + j] = idx[j] >= 0 ? dot[j] : 0.f;
       }
     }
   }
 }
 
-
-template <typename T, int kPerRow>
-void fwd(const CombineArgs &a, hipStream_t s) {
+template <bool kBack, typename T, int kPerRow, int kJ, bool kTiny>
+void go(const CombineArgs &a, hipStream_t s) {
   const int64_t rows = kThreads / kPerRow;
-  const int64_t blocks = std::min<int64_t>((a.tokens + rows - 1) / rows, 1 << 20);
-  const int across = std::min((a.cols + kPerRow * 8 - 1) / (kPerRow * 8), 64);
-  hipLaunchKernelGGL((combine_fwd_kernel<T, kPerRow>), dim3(unsigned(blocks), unsigned(across)), dim3(kThreads), 0, s, a);
+  const unsigned blocks = unsigned(std::min<int64_t>((a.tokens + rows - 1) / rows, 1 << 20));
+  if constexpr (kBack) {
+    hipLaunchKernelGGL((combine_bwd_kernel<T, kPerRow, kJ, kTiny>), dim3(blocks), dim3(kThreads), 0, s, a);
+  } else {
+    const int across = std::min((a.cols + kPerRow * 8 - 1) / (kPerRow * 8), 64);
+    hipLaunchKernelGGL((combine_fwd_kernel<T, kPerRow, kJ, kTiny>), dim3(blocks, unsigned(across)), dim3(kThreads), 0, s, a);
+  }
 }
-
-template <typename T, int kPerRow>
-void bwd(const CombineArgs &a, hipStream_t s) {
-  const int64_t rows = kThreads / kPerRow;
-  const int64_t blocks = std::min<int64_t>((a.tokens + rows - 1) / rows, 1 << 20);
-  hipLaunchKernelGGL((combine_bwd_kernel<T, kPerRow>), dim3(unsigned(blocks)), dim3(kThreads), 0, s, a);
-}
-
-template <typename T>
-hipError_t forward(const CombineArgs &a, hipStream_t s) {
-  if (a.cols <= 64)
-    fwd<T, 8>(a, s);
-  else if (a.cols <= 512)
-    fwd<T, 64>(a, s);
+template <bool kBack, typename T, int kPerRow, bool kTiny>
+void by_topk(const CombineArgs &a, hipStream_t s) {
+  if (a.topk == 1)
+    go<kBack, T, kPerRow, 1, kTiny>(a, s);
+  else if (a.topk <= 4)
+    go<kBack, T, kPerRow, 4, kTiny>(a, s);
   else
-    fwd<T, 256>(a, s);
-  return hipGetLastError();
+    go<kBack, T, kPerRow, 8, kTiny>(a, s);
 }
 
-template <typename T>
-hipError_t backward(const CombineArgs &a, hipStream_t s) {
-  if (a.rows) {
+template <bool kBack, typename T>
+hipError_t combine(const CombineArgs &a, hipStream_t s) {
+  if (kBack && a.rows) {
     const int64_t blocks = std::min<int64_t>((a.tokens * a.topk + kThreads - 1) / kThreads, 4096);
     hipLaunchKernelGGL(places_kernel, dim3(unsigned(blocks)), dim3(kThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.cols <= 64)
-    bwd<T, 8>(a, s);
+  if (a.cols < 8)
+    by_topk<kBack, T, 8, true>(a, s);
+  else if (a.cols <= 64)
+    by_topk<kBack, T, 8, false>(a, s);
   else if (a.cols <= 512)
-    bwd<T, 64>(a, s);
+    by_topk<kBack, T, 64, false>(a, s);
   else
-    bwd<T, 256>(a, s);
+    by_topk<kBack, T, 256, false>(a, s);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_combine_fwd(const CombineArgs &a, bool bf16, hipStream_t s) {
-  return bf16 ? forward<__bf16>(a, s) : forward<float>(a, s);
+  return bf16 ? combine<false, __bf16>(a, s) : combine<false, float>(a, s);
 }
 
 hipError_t launch_combine_bwd(const CombineArgs &a, bool bf16, hipStream_t s) {
-  return bf16 ? backward<__bf16>(a, s) : backward<float>(a, s);
+  return bf16 ? combine<true, __bf16>(a, s) : combine<true, float>(a, s);
 }
 
 }  // namespace muon

@@ -32,27 +32,34 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kRowBytes = 64;      // of a step in LDS: 32 bf16 or 16 float32 of the sum's index
 constexpr int kBand = 8;           // tiles of a group that take turns within one column of tiles
 
+constexpr int kStreamGroups = 1024;  // that a streaming workgroup keeps the tiles of
+
 // A workgroup's tile: kWM x kWN waves of 32 kI x 64 (gated: 32 columns of each
 // product), the 32-row blocks dealt to the wave rows in turn, so that a tile
-// with few rows leaves each of them few. kK > 1: as many waves per part of the
-// tile share its sum, each with an LDS ring of its own, and add up at the end.
-template <int kWM_, int kWN_, int kI_, int kK_, int kStages_>
+// with few rows leaves each of them few. kK > 1: as many waves share a sum, each
+// with an LDS ring of its own, and add up at the end. kStream: a workgroup a CU,
+// which goes from tile to tile and loads the next one's first steps before it
+// stores the last one's sums.
+template <int kWM_, int kWN_, int kI_, int kK_, int kStages_, bool kStream_>
 struct Form {
   static constexpr int kWM = kWM_, kWN = kWN_, kI = kI_, kK = kK_, kStages = kStages_;
+  static constexpr bool kStream = kStream_;
   static constexpr int kWaves = kWM * kWN * kK, kThreads = kWaves * 64;
   static constexpr int kBM = kWM * kI * 32, kBN = kWN * 64;
   static constexpr int kABytes = kBM * kRowBytes;
   static constexpr int kStage = kABytes + kBN * kRowBytes;  // a ring's
   static constexpr int kRing = kStages * kStage;
+  static constexpr int kLds = kRing * kK + (kStream ? (4 * kBM + kStreamGroups) * 4 : 0);
   static constexpr int kLoaders = kK > 1 ? 1 : kWaves < 4 ? kWaves : 4;  // waves that load a ring
   static constexpr int kX = kABytes / 1024 / kLoaders, kW = kBN * kRowBytes / 1024 / kLoaders;  // their loads, a KiB each
   static_assert(kX * kLoaders * 1024 == kABytes && kW * kLoaders * 1024 == kBN * kRowBytes);
-  static constexpr int kPerSimd = kWaves >= 8 ? 2 : kWaves * (kRing * kK > 80 * 1024 ? 1 : 2) / 4;
+  static constexpr int kPerSimd = kWaves >= 8 ? 2 : kWaves * (kLds > 80 * 1024 ? 1 : 2) / 4;
 };
-using Large = Form<2, 4, 4, 1, 5>;  // 256 x 256, 160 KiB of LDS
-using Wide = Form<1, 4, 4, 1, 3>;   // 128 x 256, 72 KiB: two workgroups a CU
-using Small = Form<2, 2, 1, 1, 4>;  // 64 x 128, 48 KiB
-using Thin = Form<1, 1, 1, 4, 3>;   // 32 x 64, four waves to a sum, 72 KiB
+using Large = Form<2, 4, 4, 1, 4, true>;   // 256 x 256, 136 KiB of LDS
+using Wide = Form<1, 4, 4, 1, 3, false>;   // 128 x 256, 72 KiB: two workgroups a CU
+using Small = Form<2, 2, 1, 1, 4, false>;  // 64 x 128, 48 KiB
+using Thin = Form<1, 1, 1, 4, 3, false>;   // 32 x 64, four waves to a sum, 72 KiB
+constexpr int kCus = 256;
 
 __device__ inline float act_value(float g, int act, float &slope) {
   if (act == kActSilu) {
@@ -96,90 +103,140 @@ __device__ inline int slot_bound(const ProductArgs &a, int g) {
   return o < 0 ? 0 : o > int(a.slots) ? int(a.slots) : o;
 }
 
-// The tile of this workgroup, of tiles_n across and `rows` slots each. A
-// group's tiles lie in bands of kBand row tiles; every eighth workgroup runs on
-// one XCD, which gets a contiguous part of them. Each wave counts the tiles of
-// all groups by itself: a lane those of kRun groups, whose offsets it loads at
-// once, again for more groups than 64 kRun.
-__device__ inline Tile find_tile(const ProductArgs &a, int rows, int lane) {
-  constexpr int kRun = 8;
-  const uint32_t b = blockIdx.y * gridDim.x + blockIdx.x;
-  Tile t{-1, 0, 0, 0};
-  uint32_t total = uint32_t((a.slots + rows - 1) / rows);  // row tiles
-  const int run = a.groups >= 64 * kRun ? kRun : (a.groups + 63) / 64;  // groups of a lane
-  int at[kRun + 1], upto = 0, before = 0;
-  auto tiles_of = [&](int r) { return at[r + 1] > at[r] ? (at[r + 1] - at[r] + rows - 1) / rows : 0; };
-  auto scan = [&](int g0) {  // the tiles up to a lane's last group
-#pragma unroll
-    for (int r = 0; r <= kRun; ++r) {
-      const int g = g0 + lane * run + (r < run ? r : run);
-      at[r] = slot_bound(a, g < a.groups ? g : a.groups);
-    }
-    int sum = 0;
-#pragma unroll
-    for (int r = 0; r < kRun; ++r) sum += tiles_of(r);
-    upto = before + wave_scan(sum, lane);
-    before = __builtin_amdgcn_readlane(upto, 63);
-  };
-  if (a.offsets) {
-    for (int g0 = 0; g0 < a.groups; g0 += 64 * run) scan(g0);
-    total = uint32_t(before);
-  }
-  const uint32_t tiles = total * uint32_t(a.tiles_n), per = (tiles + 7) / 8;
-  const uint32_t id = (b & 7) * per + (b >> 3);
-  if ((b >> 3) >= per || id >= tiles) return t;
-  const uint32_t row = id / uint32_t(a.tiles_n);  // in which group's tiles
-  uint32_t first = 0, count = total;              // its row tiles
-  int64_t lo = 0, hi = a.slots;
-  t.group = 0;
-  if (a.offsets) {
-    int g0 = 0;
-    if (a.groups > 64 * run) {
-      before = 0;
-      for (scan(0); uint32_t(before) <= row; scan(g0)) g0 += 64 * run;
-    }
-    const int owner = __builtin_amdgcn_readfirstlane(__builtin_ctzll(__ballot(uint32_t(upto) > row)));
-    int sum = 0;
-#pragma unroll
-    for (int r = 0; r < kRun; ++r) sum += tiles_of(r);
-    first = uint32_t(__builtin_amdgcn_readlane(upto - sum, owner));
-    t.group = g0 + owner * run;
-#pragma unroll
-    for (int r = 0; r < kRun; ++r) {
-      const uint32_t mine = uint32_t(__builtin_amdgcn_readlane(tiles_of(r), owner));
-      if (first <= row && row < first + mine) {
-        t.group = g0 + owner * run + r;
-        count = mine;
-        lo = __builtin_amdgcn_readlane(at[r], owner);
-        hi = __builtin_amdgcn_readlane(at[r + 1], owner);
-        break;
-      }
-      first += mine;
-    }
-  }
+// A group's tiles, tiles_n across and at most `rows` slots each, lie in bands of
+// kBand row tiles, `first` row tiles of other groups before them.
+__device__ __forceinline__ Tile group_tile(const ProductArgs &a, uint32_t id, int group, uint32_t first, uint32_t mine, int64_t lo, int64_t hi) {
+  Tile t{group, 0, 0, 0};
   const uint32_t local = id - first * uint32_t(a.tiles_n);
   const uint32_t band = local / (kBand * uint32_t(a.tiles_n)), in = local - band * kBand * uint32_t(a.tiles_n);
-  const uint32_t wide = count - band * kBand < kBand ? count - band * kBand : kBand;
+  const uint32_t wide = mine - band * kBand < kBand ? mine - band * kBand : kBand;
   t.n = __builtin_amdgcn_readfirstlane(int(in / wide));
   const int m = __builtin_amdgcn_readfirstlane(int(band * kBand + in % wide));
   // the group's 32-row blocks, dealt evenly to its tiles: a tile of few rows
   // would wait for its weights at every step
-  const int each = int((uint32_t(hi - lo + 31) / 32 + count - 1) / count) * 32;
+  const int each = int((uint32_t(hi - lo + 31) / 32 + mine - 1) / mine) * 32;
   t.lo = lo + int64_t(m) * each;
   t.hi = t.lo + each < hi ? t.lo + each : hi;
-  if (t.lo >= t.hi) t.group = -1;
   return t;
 }
 
-// The row of x that slot s reads, -1: none.
-__device__ inline int64_t source_row(const ProductArgs &a, int64_t s) {
-  int64_t r = s;
-  if (a.gather) {
-    const int32_t v = a.rows ? a.rows[s] : int32_t(s);
-    if (v < 0) return -1;
-    r = a.gather == 1 ? v : int32_t(uint32_t(v) / uint32_t(a.gather));
+// The row tiles of a run of groups from g0 on: a lane counts those of `run` of
+// them, whose offsets it loads at once.
+constexpr int kRun = 8;
+struct Count {
+  int at[kRun + 1], upto;  // offsets, and the tiles up to the lane's last group
+};
+__device__ __forceinline__ int tiles_of(const Count &c, int r, int rows) {
+  return c.at[r + 1] > c.at[r] ? (c.at[r + 1] - c.at[r] + rows - 1) / rows : 0;
+}
+__device__ __forceinline__ int count_tiles(Count &c, const ProductArgs &a, int g0, int run, int before, int rows, int lane) {
+#pragma unroll
+  for (int r = 0; r <= kRun; ++r) {
+    const int g = g0 + lane * run + (r < run ? r : run);
+    c.at[r] = slot_bound(a, g < a.groups ? g : a.groups);
   }
+  int sum = 0;
+#pragma unroll
+  for (int r = 0; r < kRun; ++r) sum += tiles_of(c, r, rows);
+  c.upto = before + wave_scan(sum, lane);
+  return __builtin_amdgcn_readlane(c.upto, 63);
+}
+__device__ __forceinline__ int run_of(const ProductArgs &a) { return a.groups >= 64 * kRun ? kRun : (a.groups + 63) / 64; }
+
+// The tiles of XCD x (every eighth workgroup runs on it): a contiguous part.
+struct Part {
+  uint32_t at, end;
+};
+__device__ __forceinline__ Part part_of(const ProductArgs &a, uint32_t total) {
+  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x, tiles = total * uint32_t(a.tiles_n), per = (tiles + 7) / 8;
+  const uint32_t from = (block & 7) * per, to = from + per < tiles ? from + per : tiles;
+  return {from + (block >> 3), to};
+}
+
+// This workgroup's only tile.
+__device__ __forceinline__ Tile find_tile(const ProductArgs &a, int rows, int lane) {
+  uint32_t total = uint32_t((a.slots + rows - 1) / rows);  // row tiles
+  const int run = run_of(a);
+  Count c;
+  if (a.offsets) {
+    int before = 0;
+    for (int g0 = 0; g0 < a.groups; g0 += 64 * run) before = count_tiles(c, a, g0, run, before, rows, lane);
+    total = uint32_t(before);
+  }
+  const Part part = part_of(a, total);
+  if (part.at >= part.end) return Tile{-1, 0, 0, 0};
+  if (!a.offsets) return group_tile(a, part.at, 0, 0, total, 0, a.slots);
+  const uint32_t row = part.at / uint32_t(a.tiles_n);  // in which group's tiles
+  int g0 = 0;
+  if (a.groups > 64 * run)
+    for (int before = count_tiles(c, a, 0, run, 0, rows, lane); uint32_t(before) <= row;) {
+      g0 += 64 * run;
+      before = count_tiles(c, a, g0, run, before, rows, lane);
+    }
+  const int owner = __builtin_amdgcn_readfirstlane(__builtin_ctzll(__ballot(uint32_t(c.upto) > row)));
+  int sum = 0;
+#pragma unroll
+  for (int r = 0; r < kRun; ++r) sum += tiles_of(c, r, rows);
+  uint32_t first = 0, mine = 0, before = uint32_t(__builtin_amdgcn_readlane(c.upto - sum, owner));
+  int group = 0, lo = 0, hi = 0;
+#pragma unroll
+  for (int r = 0; r < kRun; ++r) {
+    const uint32_t n = uint32_t(__builtin_amdgcn_readlane(tiles_of(c, r, rows), owner));
+    const int from = __builtin_amdgcn_readlane(c.at[r], owner), to = __builtin_amdgcn_readlane(c.at[r + 1], owner);
+    const bool here = before <= row && row < before + n;
+    group = here ? g0 + owner * run + r : group;
+    first = here ? before : first;
+    mine = here ? n : mine;
+    lo = here ? from : lo;
+    hi = here ? to : hi;
+    before += n;
+  }
+  return group_tile(a, part.at, group, first, mine, lo, hi);
+}
+
+// A streaming workgroup keeps the tiles up to each group in LDS (`upto`).
+__device__ __forceinline__ void keep_tiles(const ProductArgs &a, int *upto, int rows, int lane) {
+  const int run = run_of(a);
+  int before = 0;
+  for (int g0 = 0; g0 < a.groups; g0 += 64 * run) {
+    Count c;
+    before = count_tiles(c, a, g0, run, before, rows, lane);
+    int sum = c.upto;
+#pragma unroll
+    for (int r = kRun - 1; r >= 0; --r) {
+      const int g = g0 + lane * run + r;
+      if (r < run && g < a.groups) upto[g] = sum;
+      sum -= tiles_of(c, r, rows);
+    }
+  }
+}
+__device__ __forceinline__ Tile kept_tile(const ProductArgs &a, const int *upto, uint32_t id, int rows, int lane) {
+  if (!a.offsets) return group_tile(a, id, 0, 0, uint32_t((a.slots + rows - 1) / rows), 0, a.slots);
+  const int row = int(id / uint32_t(a.tiles_n));
+  int group = 0;
+  for (int g0 = 0; g0 < a.groups; g0 += 64) {
+    const uint64_t past = __ballot(g0 + lane < a.groups && upto[g0 + lane] > row);
+    if (past) {
+      group = __builtin_amdgcn_readfirstlane(g0 + __builtin_ctzll(past));
+      break;
+    }
+  }
+  const int first = group ? upto[group - 1] : 0;
+  return group_tile(a, id, group, uint32_t(__builtin_amdgcn_readfirstlane(first)),
+                    uint32_t(__builtin_amdgcn_readfirstlane(upto[group] - first)), slot_bound(a, group), slot_bound(a, group + 1));
+}
+
+// The entry of a slot's list, and the rows of x and of out that it stands for
+// (-1: none).
+__device__ inline int entry(const ProductArgs &a, int64_t s) { return a.rows ? a.rows[s] : int(s); }
+__device__ inline int source_row(const ProductArgs &a, int64_t s, int v) {
+  if (!a.gather) return s < a.x_rows ? int(s) : -1;
+  if (v < 0) return -1;
+  const int r = a.gather == 1 ? v : int(uint32_t(v) / uint32_t(a.gather));
   return r < a.x_rows ? r : -1;
+}
+__device__ inline int out_row(const ProductArgs &a, int64_t s, int v) {
+  return !a.scatter ? int(s) : v < a.out_rows ? v : -1;  // v < 0 stays below 0
 }
 
 // ---------------------------------------------------------------------------
@@ -251,9 +308,12 @@ __device__ inline u32x4 load_chunk(const T *p, int n) {
 // the gfx9 default format).
 __device__ inline u32x4 whole(const void *p) {
   const uint64_t at = reinterpret_cast<uint64_t>(p);
-  return u32x4{uint32_t(__builtin_amdgcn_readfirstlane(int(at))), uint32_t(__builtin_amdgcn_readfirstlane(int(at >> 32) & 0xffff)),
-               0xffffffffu, 0x00020000u};
+  return u32x4{uint32_t(at), uint32_t(at >> 32) & 0xffffu, 0xffffffffu, 0x00020000u};
 }
+// The same in every lane, said so: an operand of the assembly below has to be
+// in scalar registers.
+__device__ inline uint32_t scalar(uint32_t v) { return uint32_t(__builtin_amdgcn_readfirstlane(int(v))); }
+__device__ inline u32x4 scalar(const u32x4 &v) { return u32x4{scalar(v[0]), scalar(v[1]), 0xffffffffu, 0x00020000u}; }
 // 16 bytes a lane from the buffer straight to LDS (lane l's at lds + 16 l). In
 // assembly, because the compiler would wait for all of these loads before each
 // transposing LDS read; the waits that they need stand at the top of each step.
@@ -262,7 +322,7 @@ __device__ inline u32x4 whole(const void *p) {
 __device__ inline void to_lds(const u32x4 &r, uint32_t lds, uint32_t voff, uint32_t soff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
-               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "s"(scalar(lds)), "v"(voff), "s"(r), "s"(scalar(soff))
                : "memory");
 }
 
@@ -287,34 +347,54 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
   constexpr int kStep = kRowBytes / int(sizeof(T));  // sum indices of a step
   constexpr bool kBf16 = sizeof(T) == 2;
   constexpr int kI = F::kI, kBN = F::kBN;
-  __shared__ __attribute__((aligned(1024))) char smem[F::kRing * F::kK];
+  __shared__ __attribute__((aligned(1024))) char smem[F::kLds];
 
   const int tid = int(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Tile t = find_tile(a, F::kBM, lane);
-  if (t.group < 0) return;
-  const int count = int(t.hi - t.lo);  // slots of the tile
-  const int n0 = t.n * (kGated ? kBN / 2 : kBN);
-  const T *w = static_cast<const T *>(a.w) + t.group * a.w_stride;
-  const T *w2 = static_cast<const T *>(a.w2) + t.group * a.w2_stride;
+  // kStream: rows of x and of out of a tile's slots, for two tiles in turn, and the groups' tiles
+  int *table = reinterpret_cast<int *>(smem + F::kRing * F::kK), *upto = table + 4 * F::kBM;
+  Tile t;
+  Part part{};
+  if constexpr (F::kStream) {
+    uint32_t total = uint32_t((a.slots + F::kBM - 1) / F::kBM);
+    if (a.offsets) {
+      if (wave == 0) keep_tiles(a, upto, F::kBM, lane);
+      __syncthreads();
+      total = uint32_t(__builtin_amdgcn_readfirstlane(upto[a.groups - 1]));
+    }
+    part = part_of(a, total);
+    if (part.at >= part.end) return;
+    t = kept_tile(a, upto, part.at, F::kBM, lane);
+  } else {
+    t = find_tile(a, F::kBM, lane);
+    if (t.group < 0 || t.lo >= t.hi) return;
+  }
 
   const int each = (a.k + kStep - 1) / kStep;  // steps of a part
   const int steps = kBack && a.x2 ? 2 * each : each;
 
   const int wk = F::kK == 1 ? 0 : wave, wm = F::kK > 1 ? 0 : wave / F::kWN, wn = F::kK > 1 ? 0 : wave % F::kWN;
   const int fr = lane & 31, fh = lane >> 5;
-  // the wave's 32-row blocks i kWM + wm that have slots
-  const int live = __builtin_amdgcn_readfirstlane(((count + 31) / 32 - wm + F::kWM - 1) / F::kWM);
   // its steps: all, or those of its part of the sum
   const int share = (steps + F::kK - 1) / F::kK;
   const int first = wk * share, last = first + share < steps ? first + share : steps;
   char *ring = smem + wk * F::kRing;
   f32x16 acc[kI][2];
-#pragma unroll
-  for (int i = 0; i < kI; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  // the tile at hand: its slots (none where the even deal left none), first
+  // column, and the wave's 32-row blocks i kWM + wm that have slots
+  int count = int(t.hi - t.lo);
+  int n0 = t.n * (kGated ? kBN / 2 : kBN);
+  auto blocks_of = [&](int count) {
+    return __builtin_amdgcn_readfirstlane(count > 0 ? ((count + 31) / 32 - wm + F::kWM - 1) / F::kWM : 0);
+  };
+  int live = blocks_of(count);
+  const T *w = static_cast<const T *>(a.w) + t.group * a.w_stride;
+  const T *w2 = static_cast<const T *>(a.w2) + t.group * a.w2_stride;
+  auto list = [&](const Tile &t, int which, int r, int v) __attribute__((always_inline)) {
+    const bool in = t.lo + r < t.hi;
+    table[(2 * which) * F::kBM + r] = in ? source_row(a, t.lo + r, v) : -1;
+    table[(2 * which + 1) * F::kBM + r] = in ? out_row(a, t.lo + r, v) : -1;
+  };
 
   // fragments: 64-byte rows of four chunks, chunk c at place c ^ (row >> 2 & 3)
   const int fa = (wm * 32 + fr) * kRowBytes, fb = F::kABytes + (wn * 64 + fr) * kRowBytes, fx = (fr >> 2) & 3;
@@ -359,6 +439,7 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
   auto cut = [&](int step, int kk, u32x4 (&x)[kI], u32x4 (&v)[2]) {
     const int at = (step >= each ? step - each : step) * kStep;
     if (at + kStep <= a.k) return;
+    asm volatile("");  // a branch: no selects in the other steps
     if (at + (kk * 2 + fh) * kE >= a.k) {
 #pragma unroll
       for (int i = 0; i < kI; ++i) x[i] = u32x4{0u, 0u, 0u, 0u};
@@ -373,7 +454,7 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
       for (int j = 0; j < 2; ++j) multiply(acc[i][j], x[i], v[j], T());
   };
   // f with the number of live blocks as a constant
-  auto with_blocks = [&](auto f) {
+  auto with_blocks = [&](int live, auto f) __attribute__((always_inline)) {
     if (live <= 0)
       f(std::integral_constant<int, 0>());
     else if (kI == 1 || live == 1)
@@ -386,56 +467,115 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
       f(std::integral_constant<int, kI>());
   };
 
+  // The sums of the tile that was, out.
+  auto store = [&](const Tile &t, int count, int n0, int live, int which) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      if (i >= live) break;
+      __builtin_amdgcn_sched_barrier(0);  // one block's values at a time
+      const int at = (i * F::kWM + wm) * 32 + fr;
+      int from, to;
+      if constexpr (F::kStream) {
+        from = table[(2 * which) * F::kBM + at];
+        to = table[(2 * which + 1) * F::kBM + at];
+      } else {
+        const int64_t s = t.lo + (at < count ? at : count - 1);
+        const int v = a.gather || a.scatter ? entry(a, s) : 0;
+        from = source_row(a, s, v);
+        to = at < count ? out_row(a, s, v) : -1;
+      }
+      const bool there = from >= 0;
+      // the swaps of store_row need both lanes of a row: a row that is not stored has no columns
+      const int64_t row = to < 0 ? 0 : to;
+      if constexpr (kGated) {
+        const int c = n0 + 32 * wn, n = to < 0 ? 0 : a.n - c;
+        float g[16], u[16], h[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          g[r] = there ? acc[i][0][r] : 0.f;
+          u[r] = there ? acc[i][1][r] : 0.f;
+          float slope;
+          h[r] = act_value(g[r], a.act, slope) * u[r];
+        }
+        store_row(static_cast<T *>(a.out) + row * a.ld_out + c, h, fh, n);
+        if (a.gate) store_row(static_cast<T *>(a.gate) + row * a.ld_gate + c, g, fh, n);
+        if (a.up) store_row(static_cast<T *>(a.up) + row * a.ld_up + c, u, fh, n);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (F::kK > 1 && j != wk) continue;
+          const int c = n0 + 64 * wn + 32 * j;
+          float f[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) f[r] = there ? acc[i][j][r] : 0.f;
+          store_row(static_cast<T *>(a.out) + row * a.ld_out + c, f, fh, to < 0 ? 0 : a.n - c);
+        }
+      }
+    }
+  };
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kI; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  };
+
   if constexpr (kDirect) {
     constexpr int kX = F::kX, kW = F::kW, kAhead = F::kStages - 1;
     const bool loader = F::kK > 1 || wave < F::kLoaders;
     const int lw = F::kK > 1 ? 0 : wave;
-    const T *xb = static_cast<const T *>(a.x), *xb2 = static_cast<const T *>(a.x2);
-    if (!a.gather) {
-      xb += t.lo * a.ld_x;
-      if (kBack && a.x2) xb2 += t.lo * a.ld_x;
-    }
-    const u32x4 rx = whole(xb), rx2 = whole(kBack && a.x2 ? xb2 : xb);
-    const u32x4 rw = whole(w), rw2 = whole(kGated || (kBack && a.x2) ? w2 : w);
+    u32x4 rx, rx2, rw, rw2;
     uint32_t vx[kX], vw[kW];
-    uint32_t cx[kX], cw[kW];  // the chunk's first sum index within a step
-    if (loader && first < last) {
+    // the lane's chunk of a row (stage rows differ by multiples of 16), and its
+    // first sum index within a step
+    const int chunk = (lane & 3) ^ (lane >> 4);
+    const uint32_t cx = uint32_t(chunk * kE);
+    constexpr int kPlaces = kBN * int(sizeof(T)) / 16;  // chunks of a backward product's stage row
+    auto stage_row = [&](int q) { return uint32_t(((lw * kW + q) * 64 + lane) / kPlaces); };
+    auto cw = [&](int q) { return kBack ? stage_row(q) : cx; };
+    // where the tile's loads are
+    auto aim = [&](int which) __attribute__((always_inline)) {
+      const T *xb = static_cast<const T *>(a.x), *xb2 = static_cast<const T *>(a.x2);
+      if (!a.gather) {
+        xb += t.lo * a.ld_x;
+        if (kBack && a.x2) xb2 += t.lo * a.ld_x;
+      }
+      rx = whole(xb);
+      rx2 = whole(kBack && a.x2 ? xb2 : xb);
+      rw = whole(w);
+      rw2 = whole(kGated || (kBack && a.x2) ? w2 : w);
+      if (!loader || count <= 0) return;
 #pragma unroll
       for (int q = 0; q < kX; ++q) {
         const int r = (lw * kX + q) * 16 + (lane >> 2);
-        const int c = (lane & 3) ^ ((r >> 2) & 3);
-        int64_t row = r < count ? r : count - 1;
+        int row = r < count ? r : count - 1;
         if (a.gather) {
-          row = source_row(a, t.lo + row);
+          row = F::kStream ? table[(2 * which) * F::kBM + row] : source_row(a, t.lo + row, entry(a, t.lo + row));
           row = row < 0 ? 0 : row;
         }
-        cx[q] = uint32_t(c * kE);
-        vx[q] = uint32_t(row * a.ld_x * int64_t(sizeof(T))) + uint32_t(c * 16);
+        vx[q] = uint32_t(row * a.ld_x * int64_t(sizeof(T))) + uint32_t(chunk * 16);
       }
 #pragma unroll
       for (int q = 0; q < kW; ++q) {
         if constexpr (!kBack) {
           const int r = (lw * kW + q) * 16 + (lane >> 2);
-          const int c = (lane & 3) ^ ((r >> 2) & 3);
           int col = kGated ? n0 + (r >> 6) * 32 + (r & 31) : n0 + r;
           col = col < a.n ? col : a.n - 1;
-          cw[q] = uint32_t(c * kE);
-          vw[q] = uint32_t(col * (kGated && (r & 32) ? a.ld_w2 : a.ld_w) * int64_t(sizeof(T))) + uint32_t(c * 16);
+          vw[q] = uint32_t(col * (kGated && (r & 32) ? a.ld_w2 : a.ld_w) * int64_t(sizeof(T))) + uint32_t(chunk * 16);
         } else {
-          const int place = (lw * kW + q) * 64 + lane;  // 16-byte places of the stage
-          constexpr int kPlaces = kBN * int(sizeof(T)) / 16;  // of a row
-          const int r = place / kPlaces, in = place % kPlaces;
+          const int r = int(stage_row(q)), in = ((lw * kW + q) * 64 + lane) % kPlaces;
           int col = kBf16 ? tr_run<kBN>(r, in >> 2) * 32 + (in & 3) * 8 : in * 4;
           col = n0 + col < a.n ? n0 + col : n0;
-          cw[q] = uint32_t(r);
           vw[q] = uint32_t((r * a.ld_w + col) * int64_t(sizeof(T)));
         }
       }
-    }
+    };
     const uint32_t lds = __builtin_amdgcn_readfirstlane(
         int(uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)smem)) + wk * F::kRing));
-    auto load = [&](int step, uint32_t stage) {  // stage: where it begins in the ring
-      if (!loader) return;
+    auto load = [&](int step, uint32_t stage) __attribute__((always_inline)) {  // stage: where it begins in the ring
+      if (!loader || count <= 0) return;
       const uint32_t st = lds + stage;
       const bool second = kBack && step >= each;
       const uint32_t at = uint32_t(second ? step - each : step) * kStep;
@@ -447,23 +587,22 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
 #pragma unroll
       for (int q = 0; q < kW; ++q) ow[q] = vw[q];
       if (at + kStep > uint32_t(a.k)) {  // chunks past the sum's end: the step's first
+        asm volatile("");
 #pragma unroll
-        for (int q = 0; q < kX; ++q) ox[q] -= at + cx[q] >= uint32_t(a.k) ? cx[q] * uint32_t(sizeof(T)) : 0;
+        for (int q = 0; q < kX; ++q) ox[q] -= at + cx >= uint32_t(a.k) ? cx * uint32_t(sizeof(T)) : 0;
 #pragma unroll
         for (int q = 0; q < kW; ++q)
-          ow[q] -= at + cw[q] >= uint32_t(a.k) ? cw[q] * uint32_t(sizeof(T)) * (kBack ? uint32_t(a.ld_w) : 1u) : 0;
+          ow[q] -= at + cw(q) >= uint32_t(a.k) ? cw(q) * uint32_t(sizeof(T)) * (kBack ? uint32_t(a.ld_w) : 1u) : 0;
       }
+      const u32x4 xr = scalar(second ? rx2 : rx), wr = scalar(second ? rw2 : rw), wr2 = kGated ? scalar(rw2) : wr;
 #pragma unroll
-      for (int q = 0; q < kX; ++q) to_lds(second ? rx2 : rx, st + (lw * kX + q) * 1024, ox[q], sx);
+      for (int q = 0; q < kX; ++q) to_lds(xr, st + (lw * kX + q) * 1024, ox[q], sx);
 #pragma unroll
-      for (int q = 0; q < kW; ++q) {
-        // 16 rows a load: of one of the gated block's products
-        const bool other = second || (kGated && ((lw * kW + q) & 2));
-        to_lds(other ? rw2 : rw, st + F::kABytes + (lw * kW + q) * 1024, ow[q], sw);
-      }
+      for (int q = 0; q < kW; ++q)  // 16 rows a load: of one of the gated block's products
+        to_lds(kGated && ((lw * kW + q) & 2) ? wr2 : wr, st + F::kABytes + (lw * kW + q) * 1024, ow[q], sw);
     };
     // s_waitcnt with vmcnt alone constrained: the loads of `n` steps may be under way
-    auto landed = [&](int n) {
+    auto landed = [&](int n) __attribute__((always_inline)) {
       constexpr int kL = kX + kW;
       static_assert(kL * (kAhead - 1) < 64 && kAhead <= 4);
       if (!loader) return;
@@ -480,9 +619,8 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
     // the loads of the steps behind it stay under way; after the barrier, which
     // every wave reaches with its reads of step s - 1 done, the stage of that
     // step takes step s + kStages - 1. A ring of one wave needs no barrier.
-    with_blocks([&](auto blocks) {
+    auto sums = [&](auto blocks) __attribute__((always_inline)) {
       u32x4 xf[2][kI], wf[2][2];
-      for (int s = 0; s < kAhead && first + s < last; ++s) load(first + s, uint32_t(s * F::kStage));
       uint32_t here = 0, there = kAhead * F::kStage;  // the stages of step s and of the step that is loaded
 #pragma unroll 1
       for (int s = first; s < last; ++s) {
@@ -507,7 +645,52 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
       }
       if constexpr (decltype(blocks)::value > 0)
         if (first < last) products(xf[1], wf[1], blocks);
-    });
+    };
+    if constexpr (F::kStream) {
+      // The last half of the waves loads nothing to LDS: it looks up the rows of
+      // the tile after this one, whose entries arrive beside the products.
+      static_assert(F::kThreads / 2 == F::kBM && F::kLoaders * 64 == F::kThreads / 2);
+      const int r = tid - F::kBM;
+      if (r >= 0) list(t, 0, r, t.lo + r < t.hi ? entry(a, t.lo + r) : -1);
+      __syncthreads();
+      int was_n0 = 0, was_live = -1, which = 0;  // of the tile whose sums are to be stored (-1: none yet)
+      for (;;) {
+        const bool more = part.at < part.end;
+        if (more) {
+          n0 = t.n * (kGated ? kBN / 2 : kBN);
+          count = int(t.hi - t.lo);
+          live = blocks_of(count);
+          w = static_cast<const T *>(a.w) + t.group * a.w_stride;
+          w2 = static_cast<const T *>(a.w2) + t.group * a.w2_stride;
+          aim(which);
+          for (int s = 0; s < kAhead && s < steps; ++s) load(s, uint32_t(s * F::kStage));
+        }
+        if (was_live >= 0) store(t, 0, was_n0, was_live, which ^ 1);
+        if (!more) return;
+        part.at += gridDim.x >> 3;
+        Tile next = t;
+        int v = -1;
+        if (part.at < part.end) {
+          next = kept_tile(a, upto, part.at, F::kBM, lane);
+          if (r >= 0 && next.lo + r < next.hi) v = entry(a, next.lo + r);
+        }
+        clear();
+        with_blocks(live, sums);
+        if (r >= 0) list(next, which ^ 1, r, v);
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        was_n0 = n0;
+        was_live = live;
+        t = next;
+        which ^= 1;
+      }
+    } else {
+      aim(0);
+      for (int s = 0; s < kAhead && first + s < last; ++s) load(first + s, uint32_t(s * F::kStage));
+      clear();
+      with_blocks(live, sums);
+    }
   } else {
     // Through registers: any alignment and width.
     static_assert(F::kK == 1);
@@ -517,15 +700,15 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
 #pragma unroll
     for (int q = 0; q < kX; ++q) {
       const int place = q * F::kThreads + tid, r = place >> 2;
-      int64_t row = t.lo + (r < count ? r : count - 1);
-      if (a.gather) row = source_row(a, row);
+      int64_t row = t.lo + (r < count ? r : count > 0 ? count - 1 : 0);
+      if (a.gather) row = source_row(a, row, entry(a, row));
       row = row < 0 ? 0 : row;
       cx[q] = ((place & 3) ^ ((r >> 2) & 3)) * kE;
       px[q] = static_cast<const T *>(a.x) + row * a.ld_x + cx[q];
       px2[q] = kBack ? static_cast<const T *>(a.x2) + row * a.ld_x2 + cx[q] : nullptr;
     }
     u32x4 hx[kX], hw[kW];
-    auto fetch = [&](int step) {
+    auto fetch = [&](int step) __attribute__((always_inline)) {
       const bool second = kBack && step >= each;
       const int at = (second ? step - each : step) * kStep;
 #pragma unroll
@@ -548,11 +731,12 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
         }
       }
     };
-    if (steps > 0) fetch(0);
-    with_blocks([&](auto blocks) {
+    if (steps > 0 && count > 0) fetch(0);
+    clear();
+    with_blocks(live, [&](auto blocks) {
       u32x4 xf[2][kI], wf[2][2];
 #pragma unroll 1
-      for (int s = 0; s < steps; ++s) {
+      for (int s = 0; s < (count > 0 ? steps : 0); ++s) {
         char *st = smem + (s & 1) * F::kStage;
 #pragma unroll
         for (int q = 0; q < kX; ++q) *reinterpret_cast<u32x4 *>(st + (q * F::kThreads + tid) * 16) = hx[q];
@@ -599,41 +783,7 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < kI; ++i) {
-    if (i >= live) break;
-    const int at = (i * F::kWM + wm) * 32 + fr;
-    // the swaps of store_row need both lanes of a row; these have the same row
-    const int64_t s = t.lo + (at < count ? at : count - 1);
-    const bool there = source_row(a, s) >= 0;
-    if constexpr (kGated) {
-      const int c = n0 + 32 * wn;
-      float g[16], u[16], h[16];
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        g[r] = there ? acc[i][0][r] : 0.f;
-        u[r] = there ? acc[i][1][r] : 0.f;
-        float slope;
-        h[r] = act_value(g[r], a.act, slope) * u[r];
-      }
-      const int n = at < count ? a.n - c : 0;
-      store_row(static_cast<T *>(a.out) + s * a.ld_out + c, h, fh, n);
-      if (a.gate) store_row(static_cast<T *>(a.gate) + s * a.ld_gate + c, g, fh, n);
-      if (a.up) store_row(static_cast<T *>(a.up) + s * a.ld_up + c, u, fh, n);
-    } else {
-      const int64_t to = a.scatter ? a.rows[s] : s;
-      const bool put = at < count && to >= 0 && to < a.out_rows;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (F::kK > 1 && j != wk) continue;
-        const int c = n0 + 64 * wn + 32 * j;
-        float f[16];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) f[r] = there ? acc[i][j][r] : 0.f;
-        store_row(static_cast<T *>(a.out) + (put ? to : 0) * a.ld_out + c, f, fh, put ? a.n - c : 0);
-      }
-    }
-  }
+  if constexpr (!F::kStream) store(t, count, n0, live, 0);
 }
 
 int64_t row_tiles(const ProductArgs &a, int rows) {  // at most: a group's last one may be a part of a tile
@@ -647,7 +797,9 @@ int tiles_across(const ProductArgs &a, int cols) {
 template <typename T, class F, bool kDirect>
 void tiled(ProductArgs a, hipStream_t s) {
   a.tiles_n = tiles_across(a, F::kBN);
-  const int64_t most = 1 << 20, blocks = (row_tiles(a, F::kBM) * a.tiles_n + 7) / 8 * 8;
+  const int64_t most = 1 << 20;
+  int64_t blocks = (row_tiles(a, F::kBM) * a.tiles_n + 7) / 8 * 8;
+  if (F::kStream) blocks = std::min<int64_t>(blocks, kCus);
   const dim3 grid(unsigned(std::min(blocks, most)), unsigned((blocks + most - 1) / most));
   auto kernel = a.back ? product_kernel<T, F, true, false, kDirect>
                 : a.w2 ? product_kernel<T, F, false, true, kDirect> : product_kernel<T, F, false, false, kDirect>;
@@ -679,9 +831,9 @@ hipError_t product(const ProductArgs &a, hipStream_t s) {
     tiled<T, Wide, false>(a, s);
   else if (each <= 16)
     tiled<T, Thin, true>(a, s);
-  else if (few)
+  else if (few || a.k == 0)
     tiled<T, Small, true>(a, s);
-  else if (each >= 1024)
+  else if (each >= 1024 && a.groups <= kStreamGroups)
     tiled<T, Large, true>(a, s);
   else
     tiled<T, Wide, true>(a, s);
