@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "lanes.h"
@@ -29,7 +30,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kRowBytes = 64;      // of a step in LDS: 32 bf16 or 16 float32 of the sum's index
 constexpr int kBand = 8;           // tiles of a group that take turns within one column of tiles
 
 constexpr int kStreamGroups = 1024;  // that a streaming workgroup keeps the tiles of
@@ -40,25 +40,30 @@ constexpr int kStreamGroups = 1024;  // that a streaming workgroup keeps the til
 // with an LDS ring of its own, and add up at the end. kStream: a workgroup a CU,
 // which goes from tile to tile and loads the next one's first steps before it
 // stores the last one's sums.
-template <int kWM_, int kWN_, int kI_, int kK_, int kStages_, bool kStream_>
+// kRow: bytes of a row in a step's LDS stage, 32 or 64 bf16 of the sum's index.
+template <int kWM_, int kWN_, int kI_, int kK_, int kStages_, int kRow_, bool kStream_>
 struct Form {
+  static constexpr int kRow = kRow_, kChunks = kRow / 16;  // 16-byte chunks of a row
   static constexpr int kWM = kWM_, kWN = kWN_, kI = kI_, kK = kK_, kStages = kStages_;
   static constexpr bool kStream = kStream_;
   static constexpr int kWaves = kWM * kWN * kK, kThreads = kWaves * 64;
   static constexpr int kBM = kWM * kI * 32, kBN = kWN * 64;
-  static constexpr int kABytes = kBM * kRowBytes;
-  static constexpr int kStage = kABytes + kBN * kRowBytes;  // a ring's
+  static constexpr int kABytes = kBM * kRow;
+  static constexpr int kStage = kABytes + kBN * kRow;  // a ring's
   static constexpr int kRing = kStages * kStage;
   static constexpr int kLds = kRing * kK + (kStream ? (4 * kBM + kStreamGroups) * 4 : 0);
   static constexpr int kLoaders = kK > 1 ? 1 : kWaves < 4 ? kWaves : 4;  // waves that load a ring
-  static constexpr int kX = kABytes / 1024 / kLoaders, kW = kBN * kRowBytes / 1024 / kLoaders;  // their loads, a KiB each
-  static_assert(kX * kLoaders * 1024 == kABytes && kW * kLoaders * 1024 == kBN * kRowBytes);
+  static constexpr int kX = kABytes / 1024 / kLoaders, kW = kBN * kRow / 1024 / kLoaders;  // their loads, a KiB each
+  static_assert(kX * kLoaders * 1024 == kABytes && kW * kLoaders * 1024 == kBN * kRow);
   static constexpr int kPerSimd = kWaves >= 8 ? 2 : kWaves * (kLds > 80 * 1024 ? 1 : 2) / 4;
 };
-using Large = Form<2, 4, 4, 1, 4, true>;   // 256 x 256, 136 KiB of LDS
-using Wide = Form<1, 4, 4, 1, 3, false>;   // 128 x 256, 72 KiB: two workgroups a CU
-using Small = Form<2, 2, 1, 1, 4, false>;  // 64 x 128, 48 KiB
-using Thin = Form<1, 1, 1, 4, 3, false>;   // 32 x 64, four waves to a sum, 72 KiB
+using Large = Form<2, 4, 4, 1, 2, 128, true>;   // 256 x 256, 136 KiB of LDS
+using Wide = Form<1, 4, 4, 1, 3, 64, false>;    // 128 x 256, 72 KiB: two workgroups a CU
+using Small = Form<2, 2, 1, 1, 3, 128, false>;  // 64 x 128, 72 KiB
+// 32 x 64, four waves to a sum. bf16 meets memory's latency: long loads, 144 KiB;
+// float32 the products': 72 KiB, two workgroups a CU.
+template <typename T>
+using Thin = Form<1, 1, 1, 4, 3, sizeof(T) == 2 ? 128 : 64, false>;
 constexpr int kCus = 256;
 
 __device__ inline float act_value(float g, int act, float &slope) {
@@ -326,6 +331,13 @@ __device__ inline void to_lds(const u32x4 &r, uint32_t lds, uint32_t voff, uint3
                : "memory");
 }
 
+// Where chunk c of a stage's row lies: at c ^ swizzle, so that 16 rows' reads of
+// one chunk take all banks.
+template <class F>
+__device__ inline int swizzle(int row) {
+  return F::kRow == 64 ? (row >> 2) & 3 : (row >> 1) & 7;
+}
+
 // Where column col of row r of a backward product's weight tile lies in its
 // stage (bf16): rows of `wide` columns in runs of 32, run i of row r at place
 // i ^ (r & 3) within its four (of two, i ^ (r & 1)), so that a transposing
@@ -344,7 +356,8 @@ __device__ inline int tr_at(int row, int col) {
 template <typename T, class F, bool kBack, bool kGated, bool kDirect>
 __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const ProductArgs a) {
   constexpr int kE = 16 / int(sizeof(T));            // elements of a chunk
-  constexpr int kStep = kRowBytes / int(sizeof(T));  // sum indices of a step
+  constexpr int kStep = F::kRow / int(sizeof(T));  // sum indices of a step
+  constexpr int kParts = F::kRow / 32;              // fragments of a row, two chunks each
   constexpr bool kBf16 = sizeof(T) == 2;
   constexpr int kI = F::kI, kBN = F::kBN;
   __shared__ __attribute__((aligned(1024))) char smem[F::kLds];
@@ -396,8 +409,7 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
     table[(2 * which + 1) * F::kBM + r] = in ? out_row(a, t.lo + r, v) : -1;
   };
 
-  // fragments: 64-byte rows of four chunks, chunk c at place c ^ (row >> 2 & 3)
-  const int fa = (wm * 32 + fr) * kRowBytes, fb = F::kABytes + (wn * 64 + fr) * kRowBytes, fx = (fr >> 2) & 3;
+  const int fa = (wm * 32 + fr) * F::kRow, fb = F::kABytes + (wn * 64 + fr) * F::kRow, fx = swizzle<F>(fr);
   int tr[2] = {0, 0};
   if constexpr (kBack && kBf16) {
     // row 8 (lane / 32) + (lane % 16) / 4 (second read: four rows on), columns
@@ -410,13 +422,13 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
     const int ch = ((kk * 2 + fh) ^ fx) << 4;
 #pragma unroll
     for (int i = 0; i < decltype(blocks)::value; ++i)
-      f[i] = *reinterpret_cast<const u32x4 *>(stage + fa + i * F::kWM * 32 * kRowBytes + ch);
+      f[i] = *reinterpret_cast<const u32x4 *>(stage + fa + i * F::kWM * 32 * F::kRow + ch);
   };
   auto read_w = [&](const char *stage, int kk, u32x4 (&f)[2]) {
     if constexpr (!kBack) {
       const int ch = ((kk * 2 + fh) ^ fx) << 4;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) f[j] = *reinterpret_cast<const u32x4 *>(stage + fb + j * 32 * kRowBytes + ch);
+      for (int j = 0; j < 2; ++j) f[j] = *reinterpret_cast<const u32x4 *>(stage + fb + j * 32 * F::kRow + ch);
     } else if constexpr (kBf16) {
       typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
 #pragma unroll
@@ -528,13 +540,13 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
     const int lw = F::kK > 1 ? 0 : wave;
     u32x4 rx, rx2, rw, rw2;
     uint32_t vx[kX], vw[kW];
-    // the lane's chunk of a row (stage rows differ by multiples of 16), and its
-    // first sum index within a step
-    const int chunk = (lane & 3) ^ (lane >> 4);
-    const uint32_t cx = uint32_t(chunk * kE);
+    // load l of a stage: its row in this lane, and the chunk that belongs in the lane's place
+    auto load_row = [&](int l) { return l * (64 / F::kChunks) + lane / F::kChunks; };
+    auto chunk = [&](int l) { return (lane & (F::kChunks - 1)) ^ swizzle<F>(load_row(l)); };
+    auto cx = [&](int l) { return uint32_t(chunk(l) * kE); };  // its first sum index within a step
     constexpr int kPlaces = kBN * int(sizeof(T)) / 16;  // chunks of a backward product's stage row
     auto stage_row = [&](int q) { return uint32_t(((lw * kW + q) * 64 + lane) / kPlaces); };
-    auto cw = [&](int q) { return kBack ? stage_row(q) : cx; };
+    auto cw = [&](int q) { return kBack ? stage_row(q) : cx(lw * kW + q); };
     // where the tile's loads are
     auto aim = [&](int which) __attribute__((always_inline)) {
       const T *xb = static_cast<const T *>(a.x), *xb2 = static_cast<const T *>(a.x2);
@@ -549,21 +561,21 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
       if (!loader || count <= 0) return;
 #pragma unroll
       for (int q = 0; q < kX; ++q) {
-        const int r = (lw * kX + q) * 16 + (lane >> 2);
+        const int r = load_row(lw * kX + q);
         int row = r < count ? r : count - 1;
         if (a.gather) {
           row = F::kStream ? table[(2 * which) * F::kBM + row] : source_row(a, t.lo + row, entry(a, t.lo + row));
           row = row < 0 ? 0 : row;
         }
-        vx[q] = uint32_t(row * a.ld_x * int64_t(sizeof(T))) + uint32_t(chunk * 16);
+        vx[q] = uint32_t(row * a.ld_x * int64_t(sizeof(T))) + uint32_t(chunk(lw * kX + q) * 16);
       }
 #pragma unroll
       for (int q = 0; q < kW; ++q) {
         if constexpr (!kBack) {
-          const int r = (lw * kW + q) * 16 + (lane >> 2);
+          const int r = load_row(lw * kW + q);
           int col = kGated ? n0 + (r >> 6) * 32 + (r & 31) : n0 + r;
           col = col < a.n ? col : a.n - 1;
-          vw[q] = uint32_t(col * (kGated && (r & 32) ? a.ld_w2 : a.ld_w) * int64_t(sizeof(T))) + uint32_t(chunk * 16);
+          vw[q] = uint32_t(col * (kGated && (r & 32) ? a.ld_w2 : a.ld_w) * int64_t(sizeof(T))) + uint32_t(chunk(lw * kW + q) * 16);
         } else {
           const int r = int(stage_row(q)), in = ((lw * kW + q) * 64 + lane) % kPlaces;
           int col = kBf16 ? tr_run<kBN>(r, in >> 2) * 32 + (in & 3) * 8 : in * 4;
@@ -589,7 +601,7 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
       if (at + kStep > uint32_t(a.k)) {  // chunks past the sum's end: the step's first
         asm volatile("");
 #pragma unroll
-        for (int q = 0; q < kX; ++q) ox[q] -= at + cx >= uint32_t(a.k) ? cx * uint32_t(sizeof(T)) : 0;
+        for (int q = 0; q < kX; ++q) ox[q] -= at + cx(lw * kX + q) >= uint32_t(a.k) ? cx(lw * kX + q) * uint32_t(sizeof(T)) : 0;
 #pragma unroll
         for (int q = 0; q < kW; ++q)
           ow[q] -= at + cw(q) >= uint32_t(a.k) ? cw(q) * uint32_t(sizeof(T)) * (kBack ? uint32_t(a.ld_w) : 1u) : 0;
@@ -598,19 +610,19 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
 #pragma unroll
       for (int q = 0; q < kX; ++q) to_lds(xr, st + (lw * kX + q) * 1024, ox[q], sx);
 #pragma unroll
-      for (int q = 0; q < kW; ++q)  // 16 rows a load: of one of the gated block's products
-        to_lds(kGated && ((lw * kW + q) & 2) ? wr2 : wr, st + F::kABytes + (lw * kW + q) * 1024, ow[q], sw);
+      for (int q = 0; q < kW; ++q)  // a load's rows are of one of the gated block's products
+        to_lds(kGated && ((lw * kW + q) * (64 / F::kChunks) & 32) ? wr2 : wr, st + F::kABytes + (lw * kW + q) * 1024, ow[q], sw);
     };
     // s_waitcnt with vmcnt alone constrained: the loads of `n` steps may be under way
     auto landed = [&](int n) __attribute__((always_inline)) {
       constexpr int kL = kX + kW;
-      static_assert(kL * (kAhead - 1) < 64 && kAhead <= 4);
+      static_assert(kL * (kAhead - 1) < 64 && kAhead <= 4 && kParts % 2 == 0);
       if (!loader) return;
       if (n >= 3 && kAhead > 3)
         __builtin_amdgcn_s_waitcnt((3 * kL & 15) | (3 * kL >> 4) << 14 | 0x0F70);
       else if (n >= 2 && kAhead > 2)
         __builtin_amdgcn_s_waitcnt((2 * kL & 15) | (2 * kL >> 4) << 14 | 0x0F70);
-      else if (n >= 1)
+      else if (n >= 1 && kAhead > 1)
         __builtin_amdgcn_s_waitcnt((kL & 15) | (kL >> 4) << 14 | 0x0F70);
       else
         __builtin_amdgcn_s_waitcnt(0x0F70);
@@ -633,14 +645,14 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
         there = here;
         here = here == (F::kStages - 1) * F::kStage ? 0 : here + F::kStage;
         if constexpr (decltype(blocks)::value > 0) {
-          read_x(st, 0, xf[0], blocks);
-          read_w(st, 0, wf[0]);
-          if (s > first) products(xf[1], wf[1], blocks);
-          read_x(st, 1, xf[1], blocks);
-          read_w(st, 1, wf[1]);
-          cut(s, 0, xf[0], wf[0]);
-          products(xf[0], wf[0], blocks);
-          cut(s, 1, xf[1], wf[1]);
+#pragma unroll
+          for (int kk = 0; kk < kParts; ++kk) {
+            read_x(st, kk, xf[kk & 1], blocks);
+            read_w(st, kk, wf[kk & 1]);
+            if (kk) cut(s, kk - 1, xf[~kk & 1], wf[~kk & 1]);
+            if (kk || s > first) products(xf[~kk & 1], wf[~kk & 1], blocks);
+          }
+          cut(s, kParts - 1, xf[1], wf[1]);
         }
       }
       if constexpr (decltype(blocks)::value > 0)
@@ -694,16 +706,17 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
   } else {
     // Through registers: any alignment and width.
     static_assert(F::kK == 1);
-    constexpr int kX = F::kABytes / 16 / F::kThreads, kW = kBN * kRowBytes / 16 / F::kThreads;
+    constexpr int kX = F::kABytes / 16 / F::kThreads, kW = kBN * F::kRow / 16 / F::kThreads;
+    auto chunk = [&](int place) { return (place & (F::kChunks - 1)) ^ swizzle<F>(place / F::kChunks); };
     const T *px[kX], *px2[kX];
     int cx[kX];
 #pragma unroll
     for (int q = 0; q < kX; ++q) {
-      const int place = q * F::kThreads + tid, r = place >> 2;
+      const int place = q * F::kThreads + tid, r = place / F::kChunks;
       int64_t row = t.lo + (r < count ? r : count > 0 ? count - 1 : 0);
       if (a.gather) row = source_row(a, row, entry(a, row));
       row = row < 0 ? 0 : row;
-      cx[q] = ((place & 3) ^ ((r >> 2) & 3)) * kE;
+      cx[q] = chunk(place) * kE;
       px[q] = static_cast<const T *>(a.x) + row * a.ld_x + cx[q];
       px2[q] = kBack ? static_cast<const T *>(a.x2) + row * a.ld_x2 + cx[q] : nullptr;
     }
@@ -717,7 +730,7 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
       for (int q = 0; q < kW; ++q) {
         const int place = q * F::kThreads + tid;
         if constexpr (!kBack) {
-          const int r = place >> 2, c = ((place & 3) ^ ((r >> 2) & 3)) * kE;
+          const int r = place / F::kChunks, c = chunk(place) * kE;
           const bool up = kGated && (r & 32);
           const int col = kGated ? n0 + (r >> 6) * 32 + (r & 31) : n0 + r;
           const T *p = up ? w2 + col * a.ld_w2 : w + col * a.ld_w;
@@ -746,10 +759,10 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
         if (s + 1 < steps) fetch(s + 1);
         if constexpr (decltype(blocks)::value > 0) {
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {
-            read_x(st, kk, xf[kk], blocks);
-            read_w(st, kk, wf[kk]);
-            products(xf[kk], wf[kk], blocks);
+          for (int kk = 0; kk < kParts; ++kk) {
+            read_x(st, kk, xf[kk & 1], blocks);
+            read_w(st, kk, wf[kk & 1]);
+            products(xf[kk & 1], wf[kk & 1], blocks);
           }
         }
       }
@@ -820,23 +833,54 @@ bool direct(const ProductArgs &a, int64_t size) {
   return true;
 }
 
+// The form with the least time by this estimate: us for 64 bytes of the sum's
+// index when a CU has c tiles, measured (at 2 GHz, the rate the power cap
+// leaves) as
+//              256 x 256        128 x 256       64 x 128          32 x 64
+//   bf16       0.85 c           0.62, 0.5 c     0.22, 0.17 c      0.127, 0.09 c
+//   float32    3.7 c            2.08, 1.85 c    0.62, 0.5 c       0.2, 0.155 c
+// the first figure that of a single tile. A 256 x 256 tile skips 32-row blocks
+// without slots, down to half the time (float32 0.3). What it chose against the
+// best of the four, us:
+//   one token, 8 of 128 experts 768x2048, gated     32 x 64   14.7    (64 x 128: 21)
+//   64 tokens, 18432x7168, gated                    64 x 128  133     (32 x 64: 150, 128 x 256: 151)
+//   1024 tokens, 2048x2048                          64 x 128  17      (32 x 64: 26, 128 x 256: 38)
+//   2048 tokens, 4096x4096                          128 x 256 86      (64 x 128: 98, 256 x 256: 106)
+//   4096 tokens, 8 of 128 experts 768x2048, gated   256 x 256 280     (128 x 256: 309)
+//   float32, 1024 tokens, 1024x2048                 32 x 64   40      (64 x 128: 79)
+//   float32, 4096 tokens, 2048x4096                 64 x 128  518     (128 x 256: 534)
+// and where it missed: 512 tokens, 8 of 128, gated: 64 x 128 160, 256 x 256 158.
+enum { kLarge, kWide, kSmall, kThin };
+int form_of(const ProductArgs &a, bool bf16, bool lds) {
+  const double groups = double(std::min<int64_t>(a.offsets ? a.groups : 1, a.slots)), slots = double(a.slots);
+  // a group's last tile is half a one on average
+  auto row_tiles = [&](int rows) { return a.offsets ? std::max(groups, slots / rows + groups / 2) : std::ceil(slots / rows); };
+  auto per_cu = [&](int rows, int cols) { return std::max(1., row_tiles(rows) * tiles_across(a, cols) / kCus); };
+  const double fill = std::min(1., slots / row_tiles(256) / 256), wide = std::ceil(per_cu(128, 256));
+  double us[4];
+  us[kLarge] = (bf16 ? 0.85 : 3.7) * std::ceil(per_cu(256, 256)) * std::max(bf16 ? 0.5 : 0.3, fill);
+  us[kWide] = bf16 ? std::max(0.62, wide > 1 ? 0.5 * wide : 0.) : std::max(2.08, wide > 1 ? 1.85 * wide : 0.);
+  us[kSmall] = bf16 ? std::max(0.22, 0.17 * per_cu(64, 128)) : std::max(0.62, 0.5 * per_cu(64, 128));
+  us[kThin] = bf16 ? std::max(0.127, 0.09 * per_cu(32, 64)) : std::max(0.2, 0.155 * per_cu(32, 64));
+  if (!lds) return us[kSmall] <= us[kWide] ? kSmall : kWide;
+  if (a.k == 0 || (a.offsets && a.groups > kStreamGroups)) us[kLarge] = 1e30;
+  return int(std::min_element(us, us + 4) - us);
+}
+
 template <typename T>
 hipError_t product(const ProductArgs &a, hipStream_t s) {
-  const int64_t each = a.slots / (a.offsets ? a.groups : 1);
   const bool lds = direct(a, sizeof(T));
-  const bool few = row_tiles(a, 128) * tiles_across(a, 256) < 512;
-  if (!lds && few)
-    tiled<T, Small, false>(a, s);
-  else if (!lds)
-    tiled<T, Wide, false>(a, s);
-  else if (each <= 16)
-    tiled<T, Thin, true>(a, s);
-  else if (few || a.k == 0)
-    tiled<T, Small, true>(a, s);
-  else if (each >= 1024 && a.groups <= kStreamGroups)
+  const int form = form_of(a, sizeof(T) == 2, lds);
+  if (!lds)
+    form == kSmall ? tiled<T, Small, false>(a, s) : tiled<T, Wide, false>(a, s);
+  else if (form == kLarge)
     tiled<T, Large, true>(a, s);
-  else
+  else if (form == kWide)
     tiled<T, Wide, true>(a, s);
+  else if (form == kSmall)
+    tiled<T, Small, true>(a, s);
+  else
+    tiled<T, Thin<T>, true>(a, s);
   return hipGetLastError();
 }
 
