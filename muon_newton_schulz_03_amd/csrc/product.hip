@@ -36,8 +36,8 @@ constexpr int kStreamGroups = 1024;  // that a streaming workgroup keeps the til
 
 // A workgroup's tile: kWM x kWN waves of 32 kI x 64 (gated: 32 columns of each
 // product), the 32-row blocks dealt to the wave rows in turn, so that a tile
-// with few rows leaves each of them few. kK > 1: as many waves share a sum, each
-// with an LDS ring of its own, and add up at the end. kStream: a workgroup a CU,
+// with few rows leaves each of them few. kK > 1: as many such sets of waves share
+// the sums, each with an LDS ring of its own, and add up at the end. kStream: a workgroup a CU,
 // which goes from tile to tile and loads the next one's first steps before it
 // stores the last one's sums.
 // kRow: bytes of a row in a step's LDS stage, 32 or 64 bf16 of the sum's index.
@@ -52,14 +52,17 @@ struct Form {
   static constexpr int kStage = kABytes + kBN * kRow;  // a ring's
   static constexpr int kRing = kStages * kStage;
   static constexpr int kLds = kRing * kK + (kStream ? (4 * kBM + kStreamGroups) * 4 : 0);
-  static constexpr int kLoaders = kK > 1 ? 1 : kWaves < 4 ? kWaves : 4;  // waves that load a ring
+  static constexpr int kOfRing = kWM * kWN;                         // waves of a ring
+  static constexpr int kLoaders = kOfRing < 4 ? kOfRing : 4;        // that load it
   static constexpr int kX = kABytes / 1024 / kLoaders, kW = kBN * kRow / 1024 / kLoaders;  // their loads, a KiB each
   static_assert(kX * kLoaders * 1024 == kABytes && kW * kLoaders * 1024 == kBN * kRow);
   static constexpr int kPerSimd = kWaves >= 8 ? 2 : kWaves * (kLds > 80 * 1024 ? 1 : 2) / 4;
 };
-using Large = Form<2, 4, 4, 1, 2, 128, true>;   // 256 x 256, 136 KiB of LDS
-using Wide = Form<1, 4, 4, 1, 3, 64, false>;    // 128 x 256, 72 KiB: two workgroups a CU
-using Small = Form<2, 2, 1, 1, 3, 128, false>;  // 64 x 128, 72 KiB
+using Large = Form<2, 4, 4, 1, 2, 128, true>;    // 256 x 256, 136 KiB of LDS
+using LargeAny = Form<2, 4, 4, 1, 2, 128, false>;  // the same, for operands that go through registers
+using Wide = Form<1, 4, 4, 1, 3, 64, false>;     // 128 x 256, 72 KiB: two workgroups a CU
+using Small = Form<2, 2, 1, 1, 3, 128, false>;   // 64 x 128, 72 KiB
+using Mid = Form<2, 1, 1, 2, 3, 64, false>;      // 64 x 64, two sets of waves to a sum, 48 KiB
 // 32 x 64, four waves to a sum. bf16 meets memory's latency: long loads, 144 KiB;
 // float32 the products': 72 KiB, two workgroups a CU.
 template <typename T>
@@ -292,6 +295,11 @@ __device__ inline void store_row(float *p, const float (&f)[16], int fh, int n) 
   }
 }
 
+// 16 bytes at any address of global memory.
+template <typename T>
+__device__ inline u32x4 load_whole(const T *p) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) u32x4_any *>((const __attribute__((address_space(1))) char *)(p));
+}
 // The first min(n, 16 / sizeof(T)) elements at p, zeros behind them.
 template <typename T>
 __device__ inline u32x4 load_chunk(const T *p, int n) {
@@ -385,7 +393,8 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
   const int each = (a.k + kStep - 1) / kStep;  // steps of a part
   const int steps = kBack && a.x2 ? 2 * each : each;
 
-  const int wk = F::kK == 1 ? 0 : wave, wm = F::kK > 1 ? 0 : wave / F::kWN, wn = F::kK > 1 ? 0 : wave % F::kWN;
+  // its place in the ring's waves, and which ring
+  const int lw = wave % F::kOfRing, wk = wave / F::kOfRing, wm = lw / F::kWN, wn = lw % F::kWN;
   const int fr = lane & 31, fh = lane >> 5;
   // its steps: all, or those of its part of the sum
   const int share = (steps + F::kK - 1) / F::kK;
@@ -536,8 +545,7 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
 
   if constexpr (kDirect) {
     constexpr int kX = F::kX, kW = F::kW, kAhead = F::kStages - 1;
-    const bool loader = F::kK > 1 || wave < F::kLoaders;
-    const int lw = F::kK > 1 ? 0 : wave;
+    const bool loader = lw < F::kLoaders;
     u32x4 rx, rx2, rw, rw2;
     uint32_t vx[kX], vw[kW];
     // load l of a stage: its row in this lane, and the chunk that belongs in the lane's place
@@ -635,11 +643,12 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
       u32x4 xf[2][kI], wf[2][2];
       uint32_t here = 0, there = kAhead * F::kStage;  // the stages of step s and of the step that is loaded
 #pragma unroll 1
-      for (int s = first; s < last; ++s) {
+      for (int s = first; s < (F::kOfRing > 1 ? first + share : last); ++s) {  // the rings' waves keep step
         landed(last - 1 - s);
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-        if constexpr (F::kK == 1) __builtin_amdgcn_s_barrier();
+        if constexpr (F::kOfRing > 1) __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
+        if (F::kK > 1 && F::kOfRing > 1 && s >= last) continue;
         if (s + kAhead < last) load(s + kAhead, there);
         const char *st = ring + here;
         there = here;
@@ -704,59 +713,89 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
       with_blocks(live, sums);
     }
   } else {
-    // Through registers: any alignment and width.
-    static_assert(F::kK == 1);
-    constexpr int kX = F::kABytes / 16 / F::kThreads, kW = kBN * F::kRow / 16 / F::kThreads;
+    // Through registers: any alignment and width. A step is loaded kDeep steps
+    // ahead in whole 16-byte chunks at whatever address, which stay inside the
+    // operands but for a part's last step: that one goes by elements.
+    constexpr int kRt = F::kOfRing * 64, kX = F::kABytes / 16 / kRt, kW = kBN * F::kRow / 16 / kRt, kDeep = kI == 1 ? 2 : 1;
+    const int rt = tid % kRt;  // the ring's threads
     auto chunk = [&](int place) { return (place & (F::kChunks - 1)) ^ swizzle<F>(place / F::kChunks); };
-    const T *px[kX], *px2[kX];
-    int cx[kX];
+    constexpr int kPlaces = kBN * int(sizeof(T)) / 16;  // of a backward product's stage row
+    const T *px[kX], *px2[kX], *pw[kW], *pw2[kW];
+    int cx[kX], cw[kW];  // the chunk's first sum index in a step
+    int nw[kW];          // columns from the chunk on
 #pragma unroll
     for (int q = 0; q < kX; ++q) {
-      const int place = q * F::kThreads + tid, r = place / F::kChunks;
-      int64_t row = t.lo + (r < count ? r : count > 0 ? count - 1 : 0);
+      const int place = q * kRt + rt, r = place / F::kChunks;
+      int64_t row = t.lo + (r < count ? r : count - 1);
       if (a.gather) row = source_row(a, row, entry(a, row));
       row = row < 0 ? 0 : row;
       cx[q] = chunk(place) * kE;
       px[q] = static_cast<const T *>(a.x) + row * a.ld_x + cx[q];
       px2[q] = kBack ? static_cast<const T *>(a.x2) + row * a.ld_x2 + cx[q] : nullptr;
     }
-    u32x4 hx[kX], hw[kW];
-    auto fetch = [&](int step) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < kW; ++q) {
+      const int place = q * kRt + rt;
+      if constexpr (!kBack) {
+        const int r = place / F::kChunks;
+        int col = kGated ? n0 + (r >> 6) * 32 + (r & 31) : n0 + r;
+        col = col < a.n ? col : a.n - 1;
+        cw[q] = chunk(place) * kE;
+        pw[q] = (kGated && (r & 32) ? w2 + col * a.ld_w2 : w + col * a.ld_w) + cw[q];
+        pw2[q] = nullptr;
+        nw[q] = 0;
+      } else {
+        const int in = place % kPlaces;
+        int col = n0 + (kBf16 ? tr_run<kBN>(place / kPlaces, in >> 2) * 32 + (in & 3) * 8 : in * 4);
+        col = col < a.n ? col : n0;
+        cw[q] = place / kPlaces;
+        pw[q] = w + cw[q] * a.ld_w + col;
+        pw2[q] = w2 + cw[q] * a.ld_w2 + col;
+        nw[q] = a.n - col;
+      }
+    }
+    struct Held {
+      u32x4 x[kX], w[kW];
+    };
+    // rows that are shorter than a chunk would be read past by more than the one behind them
+    const bool whole_chunks = !kBack || (a.ld_w >= kE && (!a.x2 || a.ld_w2 >= kE));
+    auto fetch = [&](int step, Held &h) __attribute__((always_inline)) {
+      if (step >= last) return;
       const bool second = kBack && step >= each;
       const int at = (second ? step - each : step) * kStep;
+      if (whole_chunks && at + kStep < a.k) {
 #pragma unroll
-      for (int q = 0; q < kX; ++q) hx[q] = load_chunk((second ? px2[q] : px[q]) + at, a.k - at - cx[q]);
+        for (int q = 0; q < kX; ++q) h.x[q] = load_whole((second ? px2[q] : px[q]) + at);
 #pragma unroll
-      for (int q = 0; q < kW; ++q) {
-        const int place = q * F::kThreads + tid;
-        if constexpr (!kBack) {
-          const int r = place / F::kChunks, c = chunk(place) * kE;
-          const bool up = kGated && (r & 32);
-          const int col = kGated ? n0 + (r >> 6) * 32 + (r & 31) : n0 + r;
-          const T *p = up ? w2 + col * a.ld_w2 : w + col * a.ld_w;
-          hw[q] = load_chunk(p + at + c, col < a.n ? a.k - at - c : 0);
-        } else {
-          constexpr int kPlaces = kBN * int(sizeof(T)) / 16;
-          const int r = place / kPlaces, in = place % kPlaces;
-          const int col = n0 + (kBf16 ? tr_run<kBN>(r, in >> 2) * 32 + (in & 3) * 8 : in * 4);
-          const T *p = second ? w2 + (at + r) * a.ld_w2 : w + (at + r) * a.ld_w;
-          hw[q] = load_chunk(p + col, at + r < a.k ? a.n - col : 0);
+        for (int q = 0; q < kW; ++q) h.w[q] = load_whole(kBack ? (second ? pw2[q] + at * a.ld_w2 : pw[q] + at * a.ld_w) : pw[q] + at);
+      } else {
+#pragma unroll
+        for (int q = 0; q < kX; ++q) h.x[q] = load_chunk((second ? px2[q] : px[q]) + at, a.k - at - cx[q]);
+#pragma unroll
+        for (int q = 0; q < kW; ++q) {
+          if constexpr (!kBack)
+            h.w[q] = load_chunk(pw[q] + at, a.k - at - cw[q]);
+          else
+            h.w[q] = load_chunk(second ? pw2[q] + at * a.ld_w2 : pw[q] + at * a.ld_w, at + cw[q] < a.k ? nw[q] : 0);
         }
       }
     };
-    if (steps > 0 && count > 0) fetch(0);
     clear();
-    with_blocks(live, [&](auto blocks) {
+    with_blocks(live, [&](auto blocks) __attribute__((always_inline)) {
       u32x4 xf[2][kI], wf[2][2];
-#pragma unroll 1
-      for (int s = 0; s < (count > 0 ? steps : 0); ++s) {
-        char *st = smem + (s & 1) * F::kStage;
+      Held held[kDeep];
+      // the stage that a step writes was last read two steps before, ahead of the barrier between
+      auto pass = [&](int s, Held &h) __attribute__((always_inline)) {
+        char *st = ring + ((s - first) & 1) * F::kStage;
 #pragma unroll
-        for (int q = 0; q < kX; ++q) *reinterpret_cast<u32x4 *>(st + (q * F::kThreads + tid) * 16) = hx[q];
+        for (int q = 0; q < kX; ++q) *reinterpret_cast<u32x4 *>(st + (q * kRt + rt) * 16) = h.x[q];
 #pragma unroll
-        for (int q = 0; q < kW; ++q) *reinterpret_cast<u32x4 *>(st + F::kABytes + (q * F::kThreads + tid) * 16) = hw[q];
-        __syncthreads();
-        if (s + 1 < steps) fetch(s + 1);
+        for (int q = 0; q < kW; ++q) *reinterpret_cast<u32x4 *>(st + F::kABytes + (q * kRt + rt) * 16) = h.w[q];
+        fetch(s + kDeep, h);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (F::kK > 1 && s >= last) return;  // this part of the sum has fewer steps
         if constexpr (decltype(blocks)::value > 0) {
 #pragma unroll
           for (int kk = 0; kk < kParts; ++kk) {
@@ -765,32 +804,40 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
             products(xf[kk & 1], wf[kk & 1], blocks);
           }
         }
+      };
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) fetch(first + d, held[d]);
+#pragma unroll 1
+      for (int s = first; s < first + share; s += kDeep) {
+        pass(s, held[0]);
+        if constexpr (kDeep > 1)
+          if (s + 1 < first + share) pass(s + 1, held[kDeep - 1]);
       }
     });
   }
 
   if constexpr (F::kK > 1) {
-    // The waves of a sum add up through LDS, a quarter of the rows' columns each
-    // at first: then every wave holds them all again, and stores what is its own.
+    // The waves of a sum add up through LDS: the first (of two 32-column outputs,
+    // the first two, one each) takes the others' sums to its own, in order.
     __syncthreads();
     f32x4v *part = reinterpret_cast<f32x4v *>(smem);
-    static_assert(F::kK == 4 && kI == 1 && F::kWaves * 8192 <= F::kRing * F::kK);
+    static_assert(kI == 1 && F::kWaves * 8192 <= F::kRing * F::kK);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int g = 0; g < 4; ++g)
-        part[((wk * 2 + j) * 4 + g) * 64 + lane] =
+        part[((wave * 2 + j) * 4 + g) * 64 + lane] =
             f32x4v{acc[0][j][4 * g], acc[0][j][4 * g + 1], acc[0][j][4 * g + 2], acc[0][j][4 * g + 3]};
     __syncthreads();
-    if (wk >= (kGated ? 1 : 2)) return;  // a wave for 32 columns of the output
+    if (wk >= (kGated ? 1 : 2)) return;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (!kGated && j != wk) continue;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        f32x4v v = part[(j * 4 + g) * 64 + lane];
+        f32x4v v = part[((lw * 2 + j) * 4 + g) * 64 + lane];
 #pragma unroll
-        for (int p = 1; p < F::kK; ++p) v += part[((p * 2 + j) * 4 + g) * 64 + lane];
+        for (int p = 1; p < F::kK; ++p) v += part[(((p * F::kOfRing + lw) * 2 + j) * 4 + g) * 64 + lane];
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[0][j][4 * g + e] = v[e];
       }
@@ -834,53 +881,54 @@ bool direct(const ProductArgs &a, int64_t size) {
 }
 
 // The form with the least time by this estimate: us for 64 bytes of the sum's
-// index when a CU has c tiles, measured (at 2 GHz, the rate the power cap
-// leaves) as
-//              256 x 256        128 x 256       64 x 128          32 x 64
-//   bf16       0.85 c           0.62, 0.5 c     0.22, 0.17 c      0.127, 0.09 c
-//   float32    3.7 c            2.08, 1.85 c    0.62, 0.5 c       0.2, 0.155 c
+// index when the CUs have up to c tiles each, measured (at 2 GHz, the rate the
+// power cap leaves) as
+//              256 x 256   128 x 256       64 x 128        64 x 64        32 x 64
+//   bf16       0.85 c      0.62, 0.5 c     0.22, 0.17 c    0.2, 0.13 c    0.127, 0.09 c
+//   float32    3.7 c       2.08, 1.85 c    0.62, 0.5 c     0.37, 0.3 c    0.2, 0.17 c
 // the first figure that of a single tile. A 256 x 256 tile skips 32-row blocks
-// without slots, down to half the time (float32 0.3). What it chose against the
-// best of the four, us:
+// without slots, down to 0.55 of its time (float32 0.3); through registers it takes
+// a tenth more. What it chose against the next best, us:
 //   one token, 8 of 128 experts 768x2048, gated     32 x 64   14.7    (64 x 128: 21)
-//   64 tokens, 18432x7168, gated                    64 x 128  133     (32 x 64: 150, 128 x 256: 151)
-//   1024 tokens, 2048x2048                          64 x 128  17      (32 x 64: 26, 128 x 256: 38)
-//   2048 tokens, 4096x4096                          128 x 256 86      (64 x 128: 98, 256 x 256: 106)
+//   64 tokens, 18432x7168, gated                    64 x 128  133     (64 x 64: 149)
+//   1024 tokens, 2048x2048                          64 x 128  17      (64 x 64: 21)
+//   2048 tokens, 4096x4096                          128 x 256 86      (64 x 128: 98)
 //   4096 tokens, 8 of 128 experts 768x2048, gated   256 x 256 280     (128 x 256: 309)
-//   float32, 1024 tokens, 1024x2048                 32 x 64   40      (64 x 128: 79)
+//   8192 tokens, 4095x2047 (registers)              256 x 256 203     (128 x 256: 222)
+//   float32, 1024 tokens, 1024x2048                 32 x 64   40      (64 x 64: 47)
+//   float32, 777 tokens, 3 of 12, 532x1024, gated   64 x 64   57      (32 x 64: 71)
 //   float32, 4096 tokens, 2048x4096                 64 x 128  518     (128 x 256: 534)
-// and where it missed: 512 tokens, 8 of 128, gated: 64 x 128 160, 256 x 256 158.
-enum { kLarge, kWide, kSmall, kThin };
+// and where it missed: 512 tokens, 1 of 1, 768x2048, gated: 32 x 64 15.3, 64 x 64 13.5.
+enum { kLarge, kWide, kSmall, kMid, kThin, kForms };
 int form_of(const ProductArgs &a, bool bf16, bool lds) {
   const double groups = double(std::min<int64_t>(a.offsets ? a.groups : 1, a.slots)), slots = double(a.slots);
   // a group's last tile is half a one on average
   auto row_tiles = [&](int rows) { return a.offsets ? std::max(groups, slots / rows + groups / 2) : std::ceil(slots / rows); };
-  auto per_cu = [&](int rows, int cols) { return std::max(1., row_tiles(rows) * tiles_across(a, cols) / kCus); };
-  const double fill = std::min(1., slots / row_tiles(256) / 256), wide = std::ceil(per_cu(128, 256));
-  double us[4];
-  us[kLarge] = (bf16 ? 0.85 : 3.7) * std::ceil(per_cu(256, 256)) * std::max(bf16 ? 0.5 : 0.3, fill);
-  us[kWide] = bf16 ? std::max(0.62, wide > 1 ? 0.5 * wide : 0.) : std::max(2.08, wide > 1 ? 1.85 * wide : 0.);
-  us[kSmall] = bf16 ? std::max(0.22, 0.17 * per_cu(64, 128)) : std::max(0.62, 0.5 * per_cu(64, 128));
-  us[kThin] = bf16 ? std::max(0.127, 0.09 * per_cu(32, 64)) : std::max(0.2, 0.155 * per_cu(32, 64));
-  if (!lds) return us[kSmall] <= us[kWide] ? kSmall : kWide;
-  if (a.k == 0 || (a.offsets && a.groups > kStreamGroups)) us[kLarge] = 1e30;
-  return int(std::min_element(us, us + 4) - us);
+  auto per_cu = [&](int rows, int cols) { return std::ceil(row_tiles(rows) * tiles_across(a, cols) / kCus); };
+  auto us_of = [](double one, double each, double c) { return c > 1 ? std::max(one, each * c) : one; };
+  const double fill = std::min(1., slots / row_tiles(256) / 256);
+  double us[kForms];
+  us[kLarge] = (bf16 ? 0.85 : 3.7) * (lds ? 1 : 1.1) * per_cu(256, 256) * std::max(bf16 ? 0.55 : 0.3, fill);
+  us[kWide] = bf16 ? us_of(0.62, 0.5, per_cu(128, 256)) : us_of(2.08, 1.85, per_cu(128, 256));
+  us[kSmall] = bf16 ? us_of(0.22, 0.17, per_cu(64, 128)) : us_of(0.62, 0.5, per_cu(64, 128));
+  us[kMid] = bf16 ? us_of(0.2, 0.13, per_cu(64, 64)) : us_of(0.37, 0.3, per_cu(64, 64));
+  us[kThin] = bf16 ? us_of(0.127, 0.09, per_cu(32, 64)) : us_of(0.2, 0.17, per_cu(32, 64));
+  // a streaming workgroup needs a step between two tiles, and room for the groups
+  if (lds && (a.k == 0 || (a.offsets && a.groups > kStreamGroups))) us[kLarge] = 1e30;
+  return int(std::min_element(us, us + kForms) - us);
 }
 
 template <typename T>
 hipError_t product(const ProductArgs &a, hipStream_t s) {
   const bool lds = direct(a, sizeof(T));
   const int form = form_of(a, sizeof(T) == 2, lds);
-  if (!lds)
-    form == kSmall ? tiled<T, Small, false>(a, s) : tiled<T, Wide, false>(a, s);
-  else if (form == kLarge)
-    tiled<T, Large, true>(a, s);
-  else if (form == kWide)
-    tiled<T, Wide, true>(a, s);
-  else if (form == kSmall)
-    tiled<T, Small, true>(a, s);
-  else
-    tiled<T, Thin<T>, true>(a, s);
+  switch (form) {
+    case kLarge: lds ? tiled<T, Large, true>(a, s) : tiled<T, LargeAny, false>(a, s); break;
+    case kWide: lds ? tiled<T, Wide, true>(a, s) : tiled<T, Wide, false>(a, s); break;
+    case kSmall: lds ? tiled<T, Small, true>(a, s) : tiled<T, Small, false>(a, s); break;
+    case kMid: lds ? tiled<T, Mid, true>(a, s) : tiled<T, Mid, false>(a, s); break;
+    default: lds ? tiled<T, Thin<T>, true>(a, s) : tiled<T, Thin<T>, false>(a, s);
+  }
   return hipGetLastError();
 }
 

@@ -372,3 +372,106 @@ def test_dropped_values_do_not_count(gpu_lib):
     good = mat(randn(g, rows, cols), F32)
     mu.muon_combine_backward(good, x, dx, dw, weights=torch.ones((rows, 1), device="cuda"), p=p, key=key)
     assert bool(torch.isfinite(dw).all())
+
+
+# ---------------------------------------------------------------------------
+# sizes that take every form of tile, against 64-bit products on the GPU
+# ---------------------------------------------------------------------------
+
+def grouped64(x, w, offsets, source, back):
+    """(products, magnitudes) in slot order, in 64 bits on the GPU."""
+    cols = w.shape[2] if back else w.shape[1]
+    y = torch.zeros((len(source), cols), dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(y)
+    for g, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        if hi > lo:
+            m = w[g].double() if back else w[g].double().t().contiguous()
+            rows = x[source[lo:hi].clamp(min=0)].double() * (source[lo:hi] >= 0)[:, None]
+            y[lo:hi], mag[lo:hi] = rows @ m, rows.abs() @ m.abs()
+    return y, mag
+
+
+def near(got, ref, tol, what):
+    bad = ~((got.double() - ref).abs() <= tol)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} off, worst {float(((got.double() - ref).abs() / tol.clamp(min=1e-300)).max()):.3g} of the tolerance"
+
+
+# tokens, topk, experts, n, k: streams of several tiles a workgroup (with one group and with many), two row halves, tiles of
+# every size; the same with rows that start on no 16-byte boundary
+SIZES = [(9000, 1, 1, 2304, 128), (5000, 4, 40, 640, 192), (4000, 2, 600, 264, 64), (900, 8, 128, 256, 64), (2300, 1, 1, 2048, 64),
+         (700, 1, 1, 1024, 256), (513, 3, 16, 200, 512), (60, 4, 64, 512, 320), (2, 1, 1, 4096, 1024), (9, 2, 35, 72, 2048),
+         (8000, 1, 1, 2303, 127), (5000, 4, 40, 639, 191), (2300, 1, 1, 2047, 63), (1000, 2, 30, 201, 333), (3, 2, 9, 515, 1031)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tokens,topk,experts,n,k", SIZES)
+def test_products_of_every_size(gpu_lib, tokens, topk, experts, n, k, dtype):
+    mu, g = gpu_lib, gen(tokens + experts + n)
+    slots = tokens * topk
+    # uneven groups, some of them empty, some slots behind the last
+    share = torch.rand(experts, generator=g, device="cuda") ** 2 * (torch.rand(experts, generator=g, device="cuda") < 0.9)
+    ends = (share.cumsum(0) / share.sum().clamp(min=1e-3) * (slots - slots // 50)).long() if experts > 1 else torch.tensor([slots], device="cuda")
+    offsets = torch.cat([ends.new_zeros(1), ends]).to(torch.int32)
+    rows = torch.randperm(slots, generator=g, device="cuda").to(torch.int32)
+    rows[::97] = -1
+    off = offsets.tolist()
+    used = torch.arange(slots, device="cuda") < off[-1]
+    token = torch.where(rows < 0, -1, rows // topk).long()
+    x, wg, wu = mat(randn(g, tokens, k), dtype), stack(g, experts, n, k, dtype), stack(g, experts, n, k, dtype)
+    h, gate, up = (out_mat(slots, n, dtype) for _ in range(3))
+    mu.muon_gated_forward(x, wg, wu, h, gate, up, offsets, rows, topk)
+    rg, mg = grouped64(x, wg, off, token, False)
+    ru, mu_ = grouped64(x, wu, off, token, False)
+    u = (2 * k + 2) * U
+    near(gate[used], rg[used], (HALF[dtype] * rg.abs() + u * mg)[used], "gate")
+    near(up[used], ru[used], (HALF[dtype] * ru.abs() + u * mu_)[used], "up")
+    v = rg * torch.sigmoid(rg)
+    near(h[used], (v * ru)[used], (HALF[dtype] * (v * ru).abs() + 1.2 * u * mg * (ru.abs() + u * mu_) + v.abs() * u * mu_ +
+                                   16 * U * (rg * ru).abs())[used], "h")
+    assert bool((h[~used] == MARK).all() and (gate[~used] == MARK).all() and (up[~used] == MARK).all())
+    del rg, mg, ru, mu_, v
+    dh, dgate, dup = mat(randn(g, slots, n), dtype), out_mat(slots, n, dtype), out_mat(slots, n, dtype)
+    dx = out_mat(slots, k, dtype)
+    mu.muon_gated_backward(dh, gate, up, wg, wu, dgate, dup, dx, offsets, rows)
+    own = torch.arange(slots, device="cuda")
+    a, ma = grouped64(dgate, wg, off, own, True)
+    b, mb = grouped64(dup, wu, off, own, True)
+    put = used & (rows >= 0)
+    near(dx[rows[put].long()], (a + b)[put], (HALF[dtype] * (a + b).abs() + (4 * n + 2) * U * (ma + mb))[put], "dx")
+    other = torch.ones(slots, dtype=torch.bool, device="cuda")
+    other[rows[put].long()] = False
+    assert bool((dx[other] == MARK).all())
+    del a, b, ma, mb
+    for back in (False, True):
+        xs = mat(randn(g, slots, n if back else k), dtype)
+        y = out_mat(slots, k if back else n, dtype)
+        (mu.muon_expert_backward if back else mu.muon_expert_forward)(xs, wg, y, offsets)
+        r, m = grouped64(xs, wg, off, own, back)
+        near(y[used], r[used], (HALF[dtype] * r.abs() + (2 * xs.shape[1] + 2) * U * m)[used], "backward" if back else "forward")
+        assert bool((y[~used] == MARK).all())
+
+
+@pytest.mark.parametrize("k", [33, 40, 63, 64, 65, 72, 96, 120, 129, 200])
+def test_products_whose_sum_ends_anywhere_in_a_step(gpu_lib, k):
+    """The operands lie in buffers of NaN: nothing behind a sum's end takes part. Tiles that stream (enough rows for them),
+    small ones and those of registers."""
+    mu, g = gpu_lib, gen(k)
+    for rows, n in ((70000, 264), (130, 264), (20, 24)):
+        for dtype in (BF, F32):
+            wide = torch.full((rows + 2, 256), float("nan"), dtype=dtype, device="cuda")
+            x = wide[1:-1, :k]
+            x.copy_(randn(g, rows, k))
+            wbuf = torch.full((n + 2, 256), float("nan"), dtype=dtype, device="cuda")
+            w = wbuf[1:-1, :k]
+            w.copy_(randn(g, n, k, scale=k ** -0.5))
+            y = out_mat(rows, n, dtype)
+            mu.muon_expert_forward(x, w, y)
+            r, m = grouped64(x, w[None], [0, rows], torch.arange(rows, device="cuda"), False)
+            near(y, r, HALF[dtype] * r.abs() + (2 * k + 2) * U * m, f"forward {rows} {dtype}")
+            # backward: the sum's index is the weights' row
+            wt = torch.full((k + 2, 320), float("nan"), dtype=dtype, device="cuda")
+            v = wt[1:-1, :n]
+            v.copy_(w.t())
+            z = out_mat(rows, n, dtype)
+            mu.muon_expert_backward(x, v, z)
+            near(z, r, HALF[dtype] * r.abs() + (2 * k + 2) * U * m, f"backward {rows} {dtype}")
