@@ -63,10 +63,8 @@ using LargeAny = Form<2, 4, 4, 1, 2, 128, false>;  // the same, for operands tha
 using Wide = Form<1, 4, 4, 1, 3, 64, false>;     // 128 x 256, 72 KiB: two workgroups a CU
 using Small = Form<2, 2, 1, 1, 3, 128, false>;   // 64 x 128, 72 KiB
 using Mid = Form<2, 1, 1, 2, 3, 64, false>;      // 64 x 64, two sets of waves to a sum, 48 KiB
-// 32 x 64, four waves to a sum. bf16 meets memory's latency: long loads, 144 KiB;
-// float32 the products': 72 KiB, two workgroups a CU.
-template <typename T>
-using Thin = Form<1, 1, 1, 4, 3, sizeof(T) == 2 ? 128 : 64, false>;
+using Thin = Form<1, 1, 1, 4, 3, 128, false>;    // 32 x 64, four waves to a sum, 144 KiB
+using Thin2 = Form<1, 1, 1, 4, 3, 64, false>;    // the same in 72 KiB: two workgroups a CU
 constexpr int kCus = 256;
 
 __device__ inline float act_value(float g, int act, float &slope) {
@@ -300,11 +298,23 @@ template <typename T>
 __device__ inline u32x4 load_whole(const T *p) {
   return *reinterpret_cast<const __attribute__((address_space(1))) u32x4_any *>((const __attribute__((address_space(1))) char *)(p));
 }
-// The first min(n, 16 / sizeof(T)) elements at p, zeros behind them.
-template <typename T>
+// The first min(n, 16 / sizeof(T)) elements at p, zeros behind them. kRoom: at
+// least 16 bytes of the operand end at p + n; they are read whole and moved down.
+template <bool kRoom, typename T>
 __device__ inline u32x4 load_chunk(const T *p, int n) {
   constexpr int kE = 16 / int(sizeof(T));
-  if (n >= kE) return *reinterpret_cast<const u32x4_any *>(p);
+  if constexpr (kRoom) {
+    const int short_by = n < kE ? kE - n : 0;
+    u32x4 v = load_whole(p - short_by);
+    // by a chunk (all of it zeros), or 8, 4, 2 bytes
+    const uint32_t by = uint32_t(short_by < kE ? short_by : kE) * uint32_t(sizeof(T));
+    if (by & 16) v = u32x4{0u, 0u, 0u, 0u};
+    if (by & 8) v = u32x4{v[2], v[3], 0u, 0u};
+    if (by & 4) v = u32x4{v[1], v[2], v[3], 0u};
+    if (sizeof(T) == 2 && (by & 2)) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+    return v;
+  }
+  if (n >= kE) return load_whole(p);
   u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int e = 0; e < kE - 1; ++e)
@@ -757,27 +767,37 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
     struct Held {
       u32x4 x[kX], w[kW];
     };
-    // rows that are shorter than a chunk would be read past by more than the one behind them
-    const bool whole_chunks = !kBack || (a.ld_w >= kE && (!a.x2 || a.ld_w2 >= kE));
+    // rows shorter than a chunk go by elements throughout
+    const bool room = a.k >= kE && (!kBack || a.n >= kE);
+    auto part_of_step = [&](int at, bool second, Held &h, auto has_room) __attribute__((always_inline)) {
+      constexpr bool kRoom = decltype(has_room)::value;
+#pragma unroll
+      for (int q = 0; q < kX; ++q) h.x[q] = load_chunk<kRoom>((second ? px2[q] : px[q]) + at, a.k - at - cx[q]);
+#pragma unroll
+      for (int q = 0; q < kW; ++q) {
+        if constexpr (!kBack) {
+          h.w[q] = load_chunk<kRoom>(pw[q] + at, a.k - at - cw[q]);
+        } else {  // rows past the sum's end: the last one's place, zeros
+          const int past = at + cw[q] - (a.k - 1);
+          const T *p = second ? pw2[q] + (at - (past > 0 ? past : 0)) * a.ld_w2 : pw[q] + (at - (past > 0 ? past : 0)) * a.ld_w;
+          const u32x4 v = load_chunk<kRoom>(p, nw[q]);
+          h.w[q] = past > 0 ? u32x4{0u, 0u, 0u, 0u} : v;
+        }
+      }
+    };
     auto fetch = [&](int step, Held &h) __attribute__((always_inline)) {
       if (step >= last) return;
       const bool second = kBack && step >= each;
       const int at = (second ? step - each : step) * kStep;
-      if (whole_chunks && at + kStep < a.k) {
+      if (!room) {
+        part_of_step(at, second, h, std::false_type());
+      } else if (at + kStep >= a.k) {
+        part_of_step(at, second, h, std::true_type());
+      } else {
 #pragma unroll
         for (int q = 0; q < kX; ++q) h.x[q] = load_whole((second ? px2[q] : px[q]) + at);
 #pragma unroll
         for (int q = 0; q < kW; ++q) h.w[q] = load_whole(kBack ? (second ? pw2[q] + at * a.ld_w2 : pw[q] + at * a.ld_w) : pw[q] + at);
-      } else {
-#pragma unroll
-        for (int q = 0; q < kX; ++q) h.x[q] = load_chunk((second ? px2[q] : px[q]) + at, a.k - at - cx[q]);
-#pragma unroll
-        for (int q = 0; q < kW; ++q) {
-          if constexpr (!kBack)
-            h.w[q] = load_chunk(pw[q] + at, a.k - at - cw[q]);
-          else
-            h.w[q] = load_chunk(second ? pw2[q] + at * a.ld_w2 : pw[q] + at * a.ld_w, at + cw[q] < a.k ? nw[q] : 0);
-        }
       }
     };
     clear();
@@ -899,7 +919,7 @@ bool direct(const ProductArgs &a, int64_t size) {
 //   float32, 777 tokens, 3 of 12, 532x1024, gated   64 x 64   57      (32 x 64: 71)
 //   float32, 4096 tokens, 2048x4096                 64 x 128  518     (128 x 256: 534)
 // and where it missed: 512 tokens, 1 of 1, 768x2048, gated: 32 x 64 15.3, 64 x 64 13.5.
-enum { kLarge, kWide, kSmall, kMid, kThin, kForms };
+enum { kLarge, kWide, kSmall, kMid, kThin, kForms, kThin2 = kForms };
 int form_of(const ProductArgs &a, bool bf16, bool lds) {
   const double groups = double(std::min<int64_t>(a.offsets ? a.groups : 1, a.slots)), slots = double(a.slots);
   // a group's last tile is half a one on average
@@ -915,7 +935,10 @@ int form_of(const ProductArgs &a, bool bf16, bool lds) {
   us[kThin] = bf16 ? us_of(0.127, 0.09, per_cu(32, 64)) : us_of(0.2, 0.17, per_cu(32, 64));
   // a streaming workgroup needs a step between two tiles, and room for the groups
   if (lds && (a.k == 0 || (a.offsets && a.groups > kStreamGroups))) us[kLarge] = 1e30;
-  return int(std::min_element(us, us + kForms) - us);
+  const int best = int(std::min_element(us, us + kForms) - us);
+  // memory's latency asks for long loads, float32 products for two workgroups a CU:
+  // 1024 tokens, 1024x2048, 40 us against 46; 64 tokens, 4096x4096, gated, 52 against 48
+  return best == kThin && !bf16 && per_cu(32, 64) > 1 ? kThin2 : best;
 }
 
 template <typename T>
@@ -927,7 +950,8 @@ hipError_t product(const ProductArgs &a, hipStream_t s) {
     case kWide: lds ? tiled<T, Wide, true>(a, s) : tiled<T, Wide, false>(a, s); break;
     case kSmall: lds ? tiled<T, Small, true>(a, s) : tiled<T, Small, false>(a, s); break;
     case kMid: lds ? tiled<T, Mid, true>(a, s) : tiled<T, Mid, false>(a, s); break;
-    default: lds ? tiled<T, Thin<T>, true>(a, s) : tiled<T, Thin<T>, false>(a, s);
+    case kThin: lds ? tiled<T, Thin, true>(a, s) : tiled<T, Thin, false>(a, s); break;
+    default: lds ? tiled<T, Thin2, true>(a, s) : tiled<T, Thin2, false>(a, s);
   }
   return hipGetLastError();
 }
