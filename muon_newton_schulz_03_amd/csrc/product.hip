@@ -901,16 +901,18 @@ bool direct(const ProductArgs &a, int64_t size) {
 }
 
 // The form with the least time by this estimate: us for 64 bytes of the sum's
-// index when the CUs have up to c tiles each, measured (at 2 GHz, the rate the
-// power cap leaves) as
+// index when the CUs have up to c tiles each, and us a tile besides, measured (at
+// 2 GHz, the rate the power cap leaves) as
 //              256 x 256   128 x 256       64 x 128        64 x 64        32 x 64
 //   bf16       0.85 c      0.62, 0.5 c     0.22, 0.17 c    0.2, 0.13 c    0.127, 0.09 c
 //   float32    3.7 c       2.08, 1.85 c    0.62, 0.5 c     0.37, 0.3 c    0.2, 0.17 c
+//   a tile     3           1.2             1.8             1.3            3
 // the first figure that of a single tile. A 256 x 256 tile skips 32-row blocks
-// without slots, down to 0.55 of its time (float32 0.3); through registers it takes
+// without slots, down to half its time; through registers it takes
 // a tenth more. What it chose against the next best, us:
-//   one token, 8 of 128 experts 768x2048, gated     32 x 64   14.7    (64 x 128: 21)
+//   one token, 8 of 128 experts 768x2048, gated     32 x 64   14.7    (64 x 64: 19)
 //   64 tokens, 18432x7168, gated                    64 x 128  133     (64 x 64: 149)
+//   80 tokens, 8 of 89, 418x135, gated              128 x 256 13.7    (64 x 128: 18, 32 x 64: 40)
 //   1024 tokens, 2048x2048                          64 x 128  17      (64 x 64: 21)
 //   2048 tokens, 4096x4096                          128 x 256 86      (64 x 128: 98)
 //   4096 tokens, 8 of 128 experts 768x2048, gated   256 x 256 280     (128 x 256: 309)
@@ -918,21 +920,24 @@ bool direct(const ProductArgs &a, int64_t size) {
 //   float32, 1024 tokens, 1024x2048                 32 x 64   40      (64 x 64: 47)
 //   float32, 777 tokens, 3 of 12, 532x1024, gated   64 x 64   57      (32 x 64: 71)
 //   float32, 4096 tokens, 2048x4096                 64 x 128  518     (128 x 256: 534)
-// and where it missed: 512 tokens, 1 of 1, 768x2048, gated: 32 x 64 15.3, 64 x 64 13.5.
 enum { kLarge, kWide, kSmall, kMid, kThin, kForms, kThin2 = kForms };
 int form_of(const ProductArgs &a, bool bf16, bool lds) {
   const double groups = double(std::min<int64_t>(a.offsets ? a.groups : 1, a.slots)), slots = double(a.slots);
+  const double steps = double(a.k) * (bf16 ? 2 : 4) * (a.back && a.x2 ? 2 : 1) / 64;
   // a group's last tile is half a one on average
   auto row_tiles = [&](int rows) { return a.offsets ? std::max(groups, slots / rows + groups / 2) : std::ceil(slots / rows); };
   auto per_cu = [&](int rows, int cols) { return std::ceil(row_tiles(rows) * tiles_across(a, cols) / kCus); };
-  auto us_of = [](double one, double each, double c) { return c > 1 ? std::max(one, each * c) : one; };
-  const double fill = std::min(1., slots / row_tiles(256) / 256);
+  auto us_of = [&](int rows, int cols, double one, double each, double besides) {
+    const double c = per_cu(rows, cols);
+    return steps * (c > 1 ? std::max(one, each * c) : one) + besides * c;
+  };
+  const double fill = std::max(bf16 ? 0.55 : 0.5, std::min(1., slots / row_tiles(256) / 256)) * (lds ? 1 : 1.1);
   double us[kForms];
-  us[kLarge] = (bf16 ? 0.85 : 3.7) * (lds ? 1 : 1.1) * per_cu(256, 256) * std::max(bf16 ? 0.55 : 0.3, fill);
-  us[kWide] = bf16 ? us_of(0.62, 0.5, per_cu(128, 256)) : us_of(2.08, 1.85, per_cu(128, 256));
-  us[kSmall] = bf16 ? us_of(0.22, 0.17, per_cu(64, 128)) : us_of(0.62, 0.5, per_cu(64, 128));
-  us[kMid] = bf16 ? us_of(0.2, 0.13, per_cu(64, 64)) : us_of(0.37, 0.3, per_cu(64, 64));
-  us[kThin] = bf16 ? us_of(0.127, 0.09, per_cu(32, 64)) : us_of(0.2, 0.17, per_cu(32, 64));
+  us[kLarge] = bf16 ? us_of(256, 256, 0.85 * fill, 0.85 * fill, 3) : us_of(256, 256, 3.7 * fill, 3.7 * fill, 3);
+  us[kWide] = bf16 ? us_of(128, 256, 0.62, 0.5, 1.2) : us_of(128, 256, 2.08, 1.85, 1.2);
+  us[kSmall] = bf16 ? us_of(64, 128, 0.22, 0.17, 1.8) : us_of(64, 128, 0.62, 0.5, 1.8);
+  us[kMid] = bf16 ? us_of(64, 64, 0.2, 0.13, 1.3) : us_of(64, 64, 0.37, 0.3, 1.3);
+  us[kThin] = bf16 ? us_of(32, 64, 0.127, 0.09, 3) : us_of(32, 64, 0.2, 0.17, 3);
   // a streaming workgroup needs a step between two tiles, and room for the groups
   if (lds && (a.k == 0 || (a.offsets && a.groups > kStreamGroups))) us[kLarge] = 1e30;
   const int best = int(std::min_element(us, us + kForms) - us);
