@@ -482,7 +482,8 @@ muon_status muon_route_backward(const muon_mat *logits, int32_t topk, int32_t re
  *   x            tokens x k;  wgate, wup  n x k;  h  slots x n.
  *   gate, up     slots x n, receive the two products (NULL-able): what
  *                muon_gated_backward reads.
- * A slot whose token lies outside x gets zeros.
+ * A slot whose token lies outside x gets zeros. Workspace:
+ * muon_gated_workspace_size.
  */
 muon_status muon_gated_forward(const muon_mat *x, const muon_mat *wgate, int64_t gate_stride, const muon_mat *wup,
                                int64_t up_stride, int32_t n_groups, const int32_t *offsets, const int32_t *rows,
@@ -496,12 +497,18 @@ muon_status muon_gated_forward(const muon_mat *x, const muon_mat *wgate, int64_t
  * dx has k columns and, without rows, a row for each slot; NULL: not computed,
  * wgate and wup are then not read. The entries of rows are distinct; a row that
  * rows does not name, or that lies outside dx, is not written. The weights'
- * gradients are muon_ckpt_weight_grad of dgate and dup.
+ * gradients are muon_ckpt_weight_grad of dgate and dup. Workspace (for dx):
+ * muon_gated_workspace_size.
  */
 muon_status muon_gated_backward(const muon_mat *dh, const muon_mat *gate, const muon_mat *up, const muon_mat *wgate,
                                 int64_t gate_stride, const muon_mat *wup, int64_t up_stride, int32_t n_groups,
                                 const int32_t *offsets, const int32_t *rows, int32_t activation, const muon_mat *dgate,
                                 const muon_mat *dup, const muon_mat *dx);
+
+/* Bytes for both (backward 0 or 1), of `slots` slots and n x k weights in
+ * `groups` groups: 0 unless a long sum with few outputs is shared out. */
+muon_status muon_gated_workspace_size(int32_t dtype, int64_t slots, int64_t n, int64_t k, int64_t groups, int32_t backward,
+                                      size_t *bytes);
 
 /*
  * Products of a group of expert layers: y[p(s)] = x[q(s)] w_g^T, w n x k, for
@@ -510,6 +517,8 @@ muon_status muon_gated_backward(const muon_mat *dh, const muon_mat *gate, const 
  *            gather (a slot whose row lies outside x gets zeros).
  *   scatter  0: p(s) = s, y has a row for each slot;  1: p(s) = rows[s] (as
  *            for dx of muon_gated_backward).
+ * Workspace: muon_expert_workspace_size (n x k: the weights; backward as for
+ * muon_gated_workspace_size).
  */
 muon_status muon_expert_forward(const muon_mat *x, const muon_mat *w, int64_t group_stride, int32_t n_groups, int64_t slots,
                                 const int32_t *offsets, const int32_t *rows, int32_t gather, int32_t scatter,
@@ -520,6 +529,9 @@ muon_status muon_expert_forward(const muon_mat *x, const muon_mat *w, int64_t gr
 muon_status muon_expert_backward(const muon_mat *dy, const muon_mat *w, int64_t group_stride, int32_t n_groups, int64_t slots,
                                  const int32_t *offsets, const int32_t *rows, int32_t gather, int32_t scatter,
                                  const muon_mat *dx);
+
+muon_status muon_expert_workspace_size(int32_t dtype, int64_t slots, int64_t n, int64_t k, int64_t groups, int32_t backward,
+                                       size_t *bytes);
 
 /*
  * The sum over a token's experts, dropout and residual:

@@ -53,6 +53,7 @@ EXPORTED = (
     "muon_ckpt_save", "muon_ckpt_load", "muon_ckpt_weight_grad", "muon_ckpt_weight_grad_workspace_size",
     "muon_route_forward", "muon_route_backward", "muon_route_workspace_size",
     "muon_gated_forward", "muon_gated_backward", "muon_expert_forward", "muon_expert_backward",
+    "muon_gated_workspace_size", "muon_expert_workspace_size",
     "muon_combine_forward", "muon_combine_backward", "muon_combine_workspace_size",
     "muon_dropout_forward", "muon_dropout_backward",
 )
@@ -146,6 +147,8 @@ def load_library(path=LIB_PATH):
         "muon_gated_backward": [p, p, p, p, i64, p, i64, i32, p, p, i32, p, p, p],
         "muon_expert_forward": [p, p, i64, i32, i64, p, p, i32, i32, p],
         "muon_expert_backward": [p, p, i64, i32, i64, p, p, i32, i32, p],
+        "muon_gated_workspace_size": [i32, i64, i64, i64, i64, i32, sz],
+        "muon_expert_workspace_size": [i32, i64, i64, i64, i64, i32, sz],
         "muon_combine_forward": [p, i32, p, p, p, f, p, p],
         "muon_combine_backward": [p, p, i32, p, p, p, f, p, p, p],
         "muon_combine_workspace_size": [i64, i32, sz],
@@ -706,28 +709,43 @@ def _slots(offsets, rows, groups, slots, device):
             _vec("rows", rows, _torch.int32, (slots,), device))
 
 
+@functools.lru_cache(256)
+def muon_gated_workspace_size(dtype, slots, n, k, groups=1, backward=0):
+    return _size(lib().muon_gated_workspace_size, dtype, slots, n, k, groups, backward)
+
+
+@functools.lru_cache(256)
+def muon_expert_workspace_size(dtype, slots, n, k, groups=1, backward=0):
+    return _size(lib().muon_expert_workspace_size, dtype, slots, n, k, groups, backward)
+
+
 def muon_gated_forward(x, wgate, wup, h, gate=None, up=None, offsets=None, rows=None, rows_per_token=1,
-                       activation="silu"):
+                       activation="silu", workspace=None):
     """h = act(x wgate^T) * (x wup^T), one kernel (see muon.h). x: tokens x k;
     wgate, wup: groups x n x k (or n x k: one group); h, and where given gate
     and up (what the backward pass reads): slots x n; offsets (groups + 1) and
     rows (slots): int32, as muon_route_forward writes them with rows_per_token
-    = topk. Rows of the outputs behind the last group are left as they were."""
+    = topk. Rows of the outputs behind the last group are left as they were.
+    workspace: a uint8 tensor of muon_gated_workspace_size bytes (default: a
+    temporary one)."""
     d = _enter(x)
     g, g_stride, groups = _stack("wgate", wgate, d)
     u, u_stride, groups_u = _stack("wup", wup, d)
     if groups != groups_u:
         raise ValueError("wgate and wup differ in their number of groups")
     h_mat = _mat("h", h, d)
-    _check(_lib.muon_gated_forward(
-        _mat("x", x, d), g, g_stride, u, u_stride, groups, *_slots(offsets, rows, groups, h.shape[0], d), rows_per_token,
-        _activation(activation), h_mat, _mat("gate", gate, d), _mat("up", up, d)))
+    args = (_mat("x", x, d), g, g_stride, u, u_stride, groups, *_slots(offsets, rows, groups, h.shape[0], d), rows_per_token,
+            _activation(activation), h_mat, _mat("gate", gate, d), _mat("up", up, d))
+    need = muon_gated_workspace_size(_codes[x.dtype], h.shape[0], wgate.shape[-2], wgate.shape[-1], groups)
+    _with_scratch(need, workspace, d, _lib.muon_gated_forward, *args)
 
 
-def muon_gated_backward(dh, gate, up, wgate, wup, dgate, dup, dx=None, offsets=None, rows=None, activation="silu"):
+def muon_gated_backward(dh, gate, up, wgate, wup, dgate, dup, dx=None, offsets=None, rows=None, activation="silu",
+                        workspace=None):
     """dgate, dup (slots x n) and, where given, dx of the gated block (see
     muon.h): dx[rows[s]] = dgate[s] wgate + dup[s] wup (without rows: dx[s]).
-    wgate and wup may be None without dx, if there is one group."""
+    wgate and wup may be None without dx. workspace: a uint8 tensor of
+    muon_gated_workspace_size bytes (default: a temporary one)."""
     d = _enter(dh)
     g = u = None
     g_stride = u_stride = 0
@@ -740,32 +758,35 @@ def muon_gated_backward(dh, gate, up, wgate, wup, dgate, dup, dx=None, offsets=N
         if groups != groups_u:
             raise ValueError("wgate and wup differ in their number of groups")
     dh_mat = _mat("dh", dh, d)
-    _check(_lib.muon_gated_backward(
-        dh_mat, _mat("gate", gate, d), _mat("up", up, d), g, g_stride, u, u_stride, groups,
-        *_slots(offsets, rows, groups, dh.shape[0], d), _activation(activation), _mat("dgate", dgate, d),
-        _mat("dup", dup, d), _mat("dx", dx, d)))
+    args = (dh_mat, _mat("gate", gate, d), _mat("up", up, d), g, g_stride, u, u_stride, groups,
+            *_slots(offsets, rows, groups, dh.shape[0], d), _activation(activation), _mat("dgate", dgate, d),
+            _mat("dup", dup, d), _mat("dx", dx, d))
+    need = 0 if dx is None else muon_gated_workspace_size(_codes[dh.dtype], dh.shape[0], wgate.shape[-2], wgate.shape[-1], groups, 1)
+    _with_scratch(need, workspace, d, _lib.muon_gated_backward, *args)
 
 
-def _expert(fn, x, w, y, offsets, rows, gather, scatter):
+def _expert(fn, back, x, w, y, offsets, rows, gather, scatter, workspace):
     d = _enter(x)
     w_mat, stride, groups = _stack("w", w, d)
     x_mat, y_mat = _mat("x", x, d), _mat("y", y, d)
     slots = x.shape[0] if not gather else y.shape[0] if not scatter else rows.shape[0] if rows is not None else 0
-    _check(fn(x_mat, w_mat, stride, groups, slots, *_slots(offsets, rows, groups, slots, d), int(gather), int(scatter), y_mat))
+    args = (x_mat, w_mat, stride, groups, slots, *_slots(offsets, rows, groups, slots, d), int(gather), int(scatter), y_mat)
+    _with_scratch(muon_expert_workspace_size(_codes[x.dtype], slots, w.shape[-2], w.shape[-1], groups, back), workspace, d, fn, *args)
 
 
-def muon_expert_forward(x, w, y, offsets=None, rows=None, gather=0, scatter=False):
+def muon_expert_forward(x, w, y, offsets=None, rows=None, gather=0, scatter=False, workspace=None):
     """y[p(s)] = x[q(s)] w_g^T over the slots of each group g (see muon.h). w:
     groups x n x k (or n x k: one group). gather: 0 (row s of x) or the rows
     per token (row rows[s] // gather); scatter: whether slot s writes row
-    rows[s] of y instead of row s."""
-    _expert((_lib or lib()).muon_expert_forward, x, w, y, offsets, rows, gather, scatter)
+    rows[s] of y instead of row s. workspace: a uint8 tensor of
+    muon_expert_workspace_size bytes (default: a temporary one)."""
+    _expert((_lib or lib()).muon_expert_forward, 0, x, w, y, offsets, rows, gather, scatter, workspace)
 
 
-def muon_expert_backward(dy, w, dx, offsets=None, rows=None, gather=0, scatter=False):
+def muon_expert_backward(dy, w, dx, offsets=None, rows=None, gather=0, scatter=False, workspace=None):
     """dx[p(s)] = dy[q(s)] w_g (see muon.h); the arguments are those of
     muon_expert_forward."""
-    _expert((_lib or lib()).muon_expert_backward, dy, w, dx, offsets, rows, gather, scatter)
+    _expert((_lib or lib()).muon_expert_backward, 1, dy, w, dx, offsets, rows, gather, scatter, workspace)
 
 
 @functools.lru_cache(256)

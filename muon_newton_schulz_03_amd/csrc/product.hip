@@ -154,13 +154,13 @@ struct Part {
   uint32_t at, end;
 };
 __device__ __forceinline__ Part part_of(const ProductArgs &a, uint32_t total) {
-  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x, tiles = total * uint32_t(a.tiles_n), per = (tiles + 7) / 8;
+  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x, tiles = total * uint32_t(a.tiles_n * a.splits), per = (tiles + 7) / 8;
   const uint32_t from = (block & 7) * per, to = from + per < tiles ? from + per : tiles;
   return {from + (block >> 3), to};
 }
 
-// This workgroup's only tile.
-__device__ __forceinline__ Tile find_tile(const ProductArgs &a, int rows, int lane) {
+// This workgroup's only tile, and which part of its sum.
+__device__ __forceinline__ Tile find_tile(const ProductArgs &a, int rows, int lane, int &split) {
   uint32_t total = uint32_t((a.slots + rows - 1) / rows);  // row tiles
   const int run = run_of(a);
   Count c;
@@ -170,9 +170,12 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs &a, int rows, int la
     total = uint32_t(before);
   }
   const Part part = part_of(a, total);
+  split = 0;
   if (part.at >= part.end) return Tile{-1, 0, 0, 0};
-  if (!a.offsets) return group_tile(a, part.at, 0, 0, total, 0, a.slots);
-  const uint32_t row = part.at / uint32_t(a.tiles_n);  // in which group's tiles
+  const uint32_t id = part.at / uint32_t(a.splits);
+  split = __builtin_amdgcn_readfirstlane(int(part.at - id * uint32_t(a.splits)));
+  if (!a.offsets) return group_tile(a, id, 0, 0, total, 0, a.slots);
+  const uint32_t row = id / uint32_t(a.tiles_n);  // in which group's tiles
   int g0 = 0;
   if (a.groups > 64 * run)
     for (int before = count_tiles(c, a, 0, run, 0, rows, lane); uint32_t(before) <= row;) {
@@ -197,7 +200,7 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs &a, int rows, int la
     hi = here ? to : hi;
     before += n;
   }
-  return group_tile(a, part.at, group, first, mine, lo, hi);
+  return group_tile(a, id, group, first, mine, lo, hi);
 }
 
 // A streaming workgroup keeps the tiles up to each group in LDS (`upto`).
@@ -371,7 +374,9 @@ __device__ inline int tr_at(int row, int col) {
 
 // kDirect: 16-byte loads straight to LDS. Needs operands whose rows start on
 // 16-byte boundaries, whole chunks in each row, and byte offsets below 2^32.
-template <typename T, class F, bool kBack, bool kGated, bool kDirect>
+// kPart: the tile's part of a sum that several workgroups share goes to a.part, in
+// slot order.
+template <typename T, class F, bool kBack, bool kGated, bool kDirect, bool kPart>
 __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const ProductArgs a) {
   constexpr int kE = 16 / int(sizeof(T));            // elements of a chunk
   constexpr int kStep = F::kRow / int(sizeof(T));  // sum indices of a step
@@ -385,6 +390,7 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
   int *table = reinterpret_cast<int *>(smem + F::kRing * F::kK), *upto = table + 4 * F::kBM;
   Tile t;
   Part part{};
+  int split = 0;
   if constexpr (F::kStream) {
     uint32_t total = uint32_t((a.slots + F::kBM - 1) / F::kBM);
     if (a.offsets) {
@@ -396,7 +402,7 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
     if (part.at >= part.end) return;
     t = kept_tile(a, upto, part.at, F::kBM, lane);
   } else {
-    t = find_tile(a, F::kBM, lane);
+    t = find_tile(a, F::kBM, lane, split);
     if (t.group < 0 || t.lo >= t.hi) return;
   }
 
@@ -406,9 +412,11 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
   // its place in the ring's waves, and which ring
   const int lw = wave % F::kOfRing, wk = wave / F::kOfRing, wm = lw / F::kWN, wn = lw % F::kWN;
   const int fr = lane & 31, fh = lane >> 5;
-  // its steps: all, or those of its part of the sum
-  const int share = (steps + F::kK - 1) / F::kK;
-  const int first = wk * share, last = first + share < steps ? first + share : steps;
+  // its steps: all, or those of the workgroup's part of the sum, and of its ring's part of that
+  const int of_split = kPart ? (steps + a.splits - 1) / a.splits : steps, from = split * of_split;
+  const int upto_step = from + of_split < steps ? from + of_split : steps;
+  const int share = upto_step > from ? (upto_step - from + F::kK - 1) / F::kK : 0;
+  const int first = from + wk * share, last = first + share < upto_step ? first + share : upto_step;
   char *ring = smem + wk * F::kRing;
   f32x16 acc[kI][2];
 
@@ -516,6 +524,19 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
         to = at < count ? out_row(a, s, v) : -1;
       }
       const bool there = from >= 0;
+      if constexpr (kPart) {
+        const int64_t slot = t.lo + (at < count ? at : count - 1);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (F::kK > 1 && !kGated && j != wk) continue;
+          const int c = n0 + (kGated ? 32 * wn : 64 * wn + 32 * j), wide = kGated ? 2 * a.n : a.n;
+          float f[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) f[r] = acc[i][j][r];
+          store_row(a.part + (split * a.slots + slot) * wide + (kGated ? j * a.n : 0) + c, f, fh, at < count ? a.n - c : 0);
+        }
+        continue;
+      }
       // the swaps of store_row need both lanes of a row: a row that is not stored has no columns
       const int64_t row = to < 0 ? 0 : to;
       if constexpr (kGated) {
@@ -866,6 +887,55 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
   if constexpr (!F::kStream) store(t, count, n0, live, 0);
 }
 
+// Adds the parts of the sums in order and makes of them what the tiled kernel
+// would have: a thread takes eight columns of a slot.
+template <typename T, bool kGated>
+__global__ __launch_bounds__(256) void join_kernel(const ProductArgs a) {
+  int64_t lo = 0, hi = a.slots;
+  if (a.offsets) {
+    lo = slot_bound(a, 0);
+    hi = slot_bound(a, a.groups);
+  }
+  const int64_t runs = (a.n + 7) / 8, wide = kGated ? 2 * a.n : a.n, step = a.slots * wide;
+  for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < (hi - lo) * runs; u += int64_t(gridDim.x) * 256) {
+    const int64_t s = lo + u / runs;
+    const int c = int(u % runs) * 8, left = a.n - c;
+    const float *p = a.part + s * wide + c;
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int i = 0; i < a.splits; ++i) {
+      const Raw8<float> r = load8(p + i * step, left);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] += r.get(e);
+      if constexpr (kGated) {
+        const Raw8<float> q = load8(p + i * step + a.n, left);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] += q.get(e);
+      }
+    }
+    const int v = a.gather || a.scatter ? entry(a, s) : 0;
+    const bool there = source_row(a, s, v) >= 0;
+    const int to = out_row(a, s, v);
+    if (to < 0) continue;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = there ? f[e] : 0.f;
+    if constexpr (kGated) {
+      float h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        g[e] = there ? g[e] : 0.f;
+        float slope;
+        h[e] = act_value(f[e], a.act, slope) * g[e];
+      }
+      store8(static_cast<T *>(a.out) + to * a.ld_out + c, pack8(h, T()), left);
+      if (a.gate) store8(static_cast<T *>(a.gate) + to * a.ld_gate + c, pack8(f, T()), left);
+      if (a.up) store8(static_cast<T *>(a.up) + to * a.ld_up + c, pack8(g, T()), left);
+    } else {
+      store8(static_cast<T *>(a.out) + to * a.ld_out + c, pack8(f, T()), left);
+    }
+  }
+}
+
 int64_t row_tiles(const ProductArgs &a, int rows) {  // at most: a group's last one may be a part of a tile
   return a.slots / rows + std::min<int64_t>(a.offsets ? a.groups : 1, a.slots);
 }
@@ -874,15 +944,15 @@ int tiles_across(const ProductArgs &a, int cols) {
   return (a.n + wide - 1) / wide;
 }
 
-template <typename T, class F, bool kDirect>
+template <typename T, class F, bool kDirect, bool kPart = false>
 void tiled(ProductArgs a, hipStream_t s) {
   a.tiles_n = tiles_across(a, F::kBN);
   const int64_t most = 1 << 20;
-  int64_t blocks = (row_tiles(a, F::kBM) * a.tiles_n + 7) / 8 * 8;
+  int64_t blocks = (row_tiles(a, F::kBM) * a.tiles_n * a.splits + 7) / 8 * 8;
   if (F::kStream) blocks = std::min<int64_t>(blocks, kCus);
   const dim3 grid(unsigned(std::min(blocks, most)), unsigned((blocks + most - 1) / most));
-  auto kernel = a.back ? product_kernel<T, F, true, false, kDirect>
-                : a.w2 ? product_kernel<T, F, false, true, kDirect> : product_kernel<T, F, false, false, kDirect>;
+  auto kernel = a.back ? product_kernel<T, F, true, false, kDirect, kPart>
+                : a.w2 ? product_kernel<T, F, false, true, kDirect, kPart> : product_kernel<T, F, false, false, kDirect, kPart>;
   hipLaunchKernelGGL(kernel, grid, dim3(F::kThreads), 0, s, a);
 }
 
@@ -906,7 +976,7 @@ bool direct(const ProductArgs &a, int64_t size) {
 //              256 x 256   128 x 256       64 x 128        64 x 64        32 x 64
 //   bf16       0.85 c      0.62, 0.5 c     0.22, 0.17 c    0.2, 0.13 c    0.127, 0.09 c
 //   float32    3.7 c       2.08, 1.85 c    0.62, 0.5 c     0.37, 0.3 c    0.2, 0.17 c
-//   a tile     3           1.2             1.8             1.3            3
+//   a tile     3           1.2             1.8             1.3            3 (float32: 1.5)
 // the first figure that of a single tile. A 256 x 256 tile skips 32-row blocks
 // without slots, down to half its time; through registers it takes
 // a tenth more. What it chose against the next best, us:
@@ -917,39 +987,57 @@ bool direct(const ProductArgs &a, int64_t size) {
 //   2048 tokens, 4096x4096                          128 x 256 86      (64 x 128: 98)
 //   4096 tokens, 8 of 128 experts 768x2048, gated   256 x 256 280     (128 x 256: 309)
 //   8192 tokens, 4095x2047 (registers)              256 x 256 203     (128 x 256: 222)
-//   float32, 1024 tokens, 1024x2048                 32 x 64   40      (64 x 64: 47)
-//   float32, 777 tokens, 3 of 12, 532x1024, gated   64 x 64   57      (32 x 64: 71)
+//   float32, 1024 tokens, 1024x2048                 32 x 64   39      (64 x 64: 47)
+//   float32, 777 tokens, 3 of 12, 532x1024, gated   64 x 64   56      (32 x 64: 72)
 //   float32, 4096 tokens, 2048x4096                 64 x 128  518     (128 x 256: 534)
 enum { kLarge, kWide, kSmall, kMid, kThin, kForms, kThin2 = kForms };
-int form_of(const ProductArgs &a, bool bf16, bool lds) {
-  const double groups = double(std::min<int64_t>(a.offsets ? a.groups : 1, a.slots)), slots = double(a.slots);
+struct Estimate {
+  double us[kForms], steps, mid_tiles;
+  bool thin2;
+};
+Estimate estimate(const ProductArgs &a, bool bf16, bool lds) {
+  const double groups = double(std::min<int64_t>(a.groups, a.slots)), slots = double(a.slots);
   const double steps = double(a.k) * (bf16 ? 2 : 4) * (a.back && a.x2 ? 2 : 1) / 64;
   // a group's last tile is half a one on average
-  auto row_tiles = [&](int rows) { return a.offsets ? std::max(groups, slots / rows + groups / 2) : std::ceil(slots / rows); };
-  auto per_cu = [&](int rows, int cols) { return std::ceil(row_tiles(rows) * tiles_across(a, cols) / kCus); };
+  auto tiles = [&](int rows, int cols) {
+    return (a.groups > 1 ? std::max(groups, slots / rows + groups / 2) : std::ceil(slots / rows)) * tiles_across(a, cols);
+  };
   auto us_of = [&](int rows, int cols, double one, double each, double besides) {
-    const double c = per_cu(rows, cols);
+    const double c = std::ceil(tiles(rows, cols) / kCus);
     return steps * (c > 1 ? std::max(one, each * c) : one) + besides * c;
   };
-  const double fill = std::max(bf16 ? 0.55 : 0.5, std::min(1., slots / row_tiles(256) / 256)) * (lds ? 1 : 1.1);
-  double us[kForms];
-  us[kLarge] = bf16 ? us_of(256, 256, 0.85 * fill, 0.85 * fill, 3) : us_of(256, 256, 3.7 * fill, 3.7 * fill, 3);
-  us[kWide] = bf16 ? us_of(128, 256, 0.62, 0.5, 1.2) : us_of(128, 256, 2.08, 1.85, 1.2);
-  us[kSmall] = bf16 ? us_of(64, 128, 0.22, 0.17, 1.8) : us_of(64, 128, 0.62, 0.5, 1.8);
-  us[kMid] = bf16 ? us_of(64, 64, 0.2, 0.13, 1.3) : us_of(64, 64, 0.37, 0.3, 1.3);
-  us[kThin] = bf16 ? us_of(32, 64, 0.127, 0.09, 3) : us_of(32, 64, 0.2, 0.17, 3);
+  const double fill = std::max(bf16 ? 0.55 : 0.5, std::min(1., slots * tiles_across(a, 256) / tiles(256, 256) / 256)) * (lds ? 1 : 1.1);
+  Estimate e;
+  e.us[kLarge] = bf16 ? us_of(256, 256, 0.85 * fill, 0.85 * fill, 3) : us_of(256, 256, 3.7 * fill, 3.7 * fill, 3);
+  e.us[kWide] = bf16 ? us_of(128, 256, 0.62, 0.5, 1.2) : us_of(128, 256, 2.08, 1.85, 1.2);
+  e.us[kSmall] = bf16 ? us_of(64, 128, 0.22, 0.17, 1.8) : us_of(64, 128, 0.62, 0.5, 1.8);
+  e.us[kMid] = bf16 ? us_of(64, 64, 0.2, 0.13, 1.3) : us_of(64, 64, 0.37, 0.3, 1.3);
+  e.us[kThin] = bf16 ? us_of(32, 64, 0.127, 0.09, 3) : us_of(32, 64, 0.2, 0.17, 1.5);
   // a streaming workgroup needs a step between two tiles, and room for the groups
-  if (lds && (a.k == 0 || (a.offsets && a.groups > kStreamGroups))) us[kLarge] = 1e30;
-  const int best = int(std::min_element(us, us + kForms) - us);
+  if (lds && (a.k == 0 || (a.offsets && a.groups > kStreamGroups))) e.us[kLarge] = 1e30;
   // memory's latency asks for long loads, float32 products for two workgroups a CU:
   // 1024 tokens, 1024x2048, 40 us against 46; 64 tokens, 4096x4096, gated, 52 against 48
-  return best == kThin && !bf16 && per_cu(32, 64) > 1 ? kThin2 : best;
+  e.thin2 = !bf16 && tiles(32, 64) > kCus;
+  e.steps = steps;
+  e.mid_tiles = tiles(64, 64);
+  return e;
 }
 
 template <typename T>
 hipError_t product(const ProductArgs &a, hipStream_t s) {
   const bool lds = direct(a, sizeof(T));
-  const int form = form_of(a, sizeof(T) == 2, lds);
+  if (a.splits > 1) {
+    lds ? tiled<T, Mid, true, true>(a, s) : tiled<T, Mid, false, true>(a, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t blocks = std::min<int64_t>((a.slots * ((a.n + 7) / 8) + 255) / 256, 4096);
+    auto kernel = a.w2 && !a.back ? join_kernel<T, true> : join_kernel<T, false>;
+    hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  const Estimate e = estimate(a, sizeof(T) == 2, lds);
+  int form = int(std::min_element(e.us, e.us + kForms) - e.us);
+  if (form == kThin && e.thin2) form = kThin2;
   switch (form) {
     case kLarge: lds ? tiled<T, Large, true>(a, s) : tiled<T, LargeAny, false>(a, s); break;
     case kWide: lds ? tiled<T, Wide, true>(a, s) : tiled<T, Wide, false>(a, s); break;
@@ -1004,6 +1092,29 @@ hipError_t gated_grad(const GatedGradArgs &a, hipStream_t s) {
 }
 
 }  // namespace
+
+// A long sum with few tiles is shared out to several workgroups a tile, whose
+// parts a second launch adds: 8 bytes a part and value, and what the launch costs.
+// 64 tokens, 1024x8192: float32 82 -> 20 us, bf16 19 -> 13; 1 token, 2048x2304:
+// float32 26 -> 14, bf16 stays at 8, two launches take 12.
+void product_plan(ProductArgs &a, bool bf16) {
+  a.splits = 1;
+  if (a.slots == 0 || a.groups == 0) return;
+  const Estimate e = estimate(a, bf16, true);
+  const double values = double(a.slots) * a.n * (a.w2 && !a.back ? 2 : 1);
+  double best = *std::min_element(e.us, e.us + kForms) - (bf16 ? 9 : 5);
+  for (int n = 2; n <= 16 && 8 * n <= e.steps; ++n) {
+    const double c = std::ceil(e.mid_tiles * n / kCus), one = bf16 ? 0.2 : 0.37, each = bf16 ? 0.13 : 0.3;
+    const double us = std::ceil(e.steps / n) * std::max(one, each * c) + 1.3 * c + n * values * 8 / 5e6;
+    if (us >= best) continue;
+    best = us;
+    a.splits = n;
+  }
+}
+
+size_t product_part_bytes(const ProductArgs &a) {
+  return a.splits > 1 ? size_t(a.splits) * size_t(a.slots) * size_t(a.n) * (a.w2 && !a.back ? 2 : 1) * sizeof(float) : 0;
+}
 
 hipError_t launch_product(const ProductArgs &a, bool bf16, hipStream_t s) {
   return bf16 ? product<__bf16>(a, s) : product<float>(a, s);

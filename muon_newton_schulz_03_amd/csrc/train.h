@@ -134,6 +134,8 @@ struct ProductArgs {
   int64_t out_rows;
   int32_t act;             // Activation
   int32_t tiles_n;
+  int32_t splits;          // workgroups that share a tile's sums
+  float *part;             // their parts when there are several
 };
 
 struct GatedGradArgs {
@@ -180,6 +182,10 @@ hipError_t launch_wgrad(const WgradArgs &a, bool bf16, hipStream_t s);
 void route_plan(RouteFwdArgs &a);
 hipError_t launch_route_fwd(const RouteFwdArgs &a, bool bf16, hipStream_t s);
 hipError_t launch_route_bwd(const RouteBwdArgs &a, bool bf16, hipStream_t s);
+// Fills splits of a (from its sizes, groups and the kind of product: back, and
+// whether x2 and w2 are set); the parts take product_part_bytes.
+void product_plan(ProductArgs &a, bool bf16);
+size_t product_part_bytes(const ProductArgs &a);
 hipError_t launch_product(const ProductArgs &a, bool bf16, hipStream_t s);
 hipError_t launch_gated_grad(const GatedGradArgs &a, bool bf16, hipStream_t s);
 hipError_t launch_combine_fwd(const CombineArgs &a, bool bf16, hipStream_t s);

@@ -216,6 +216,33 @@ void sizes(ProductArgs &a, int64_t n, int64_t k) {
   a.k = a.x_rows > 0 ? int32_t(k) : 0;  // no row of x: every sum is empty
 }
 
+// The workspace of a product, whose kind back, x2 and w2 have been set for, and its check with the call's buffers.
+void parts(const State &st, ProductArgs &a, Buffers &b, bool bf16) {
+  product_plan(a, bf16);
+  a.part = reinterpret_cast<float *>(workspace(st, product_part_bytes(a), b));
+  b.check();
+}
+
+// What the workspace of a product of these sizes is: weights n x k.
+size_t product_workspace(int32_t dtype, int64_t slots, int64_t n, int64_t k, int64_t groups, int32_t backward, bool gated) {
+  if (dtype != MUON_F32 && dtype != MUON_BF16) refuse(MUON_ERR_DTYPE, "unknown dtype");
+  if (backward != 0 && backward != 1) refuse(MUON_ERR_INVALID_ARG, "backward must be 0 or 1");
+  if (groups < 0 || groups > 65536) refuse(MUON_ERR_INVALID_ARG, "groups must lie in [0, 65536]");
+  if (n < 1 || k < 1) refuse(MUON_ERR_SHAPE, "n and k must lie in [1, 2^30)");
+  ProductArgs a{};
+  Buffers b;
+  slots_of(a, b, slots, 0, nullptr, nullptr);
+  a.groups = int32_t(groups);
+  a.x_rows = 1;
+  sizes(a, backward ? k : n, backward ? n : k);
+  a.back = backward;
+  const void *some = &a;  // only whether there is one counts
+  a.w2 = gated ? some : nullptr;
+  a.x2 = gated && backward ? some : nullptr;
+  product_plan(a, dtype == MUON_BF16);
+  return product_part_bytes(a);
+}
+
 void activation_of(int32_t activation) {
   if (activation != MUON_ACT_SILU && activation != MUON_ACT_GELU)
     refuse(MUON_ERR_INVALID_ARG, "activation must be MUON_ACT_SILU or MUON_ACT_GELU");
@@ -242,7 +269,8 @@ void expert_product(State &st, const muon_mat *x, const muon_mat *w, int64_t gro
   add(b, x, false, "x");
   weights(b, w, "w", group_stride, n_groups, x->dtype, false);
   add(b, y, true, "y");
-  b.check();
+  a.back = back;
+  parts(st, a, b, x->dtype == MUON_BF16);
   if (n_groups == 0 || slots == 0) return;
   a.x = x->data;
   a.ld_x = x->ld;
@@ -251,7 +279,6 @@ void expert_product(State &st, const muon_mat *x, const muon_mat *w, int64_t gro
   a.w_stride = n_groups > 1 ? group_stride : 0;
   a.gather = gather;
   a.scatter = scatter;
-  a.back = back;
   a.out = y->data;
   a.ld_out = y->ld;
   a.out_rows = y->rows;
@@ -696,14 +723,14 @@ muon_status muon_gated_forward(const muon_mat *x, const muon_mat *wgate, int64_t
     add(b, h, true, "h");
     add(b, gate, true, "gate");
     add(b, up, true, "up");
-    b.check();
+    a.w2 = wup->data;
+    parts(st, a, b, x->dtype == MUON_BF16);
     if (n_groups == 0 || h->rows == 0) return;
     a.x = x->data;
     a.ld_x = x->ld;
     a.w = wgate->data;
     a.ld_w = wgate->ld;
     a.w_stride = n_groups > 1 ? gate_stride : 0;
-    a.w2 = wup->data;
     a.ld_w2 = wup->ld;
     a.w2_stride = n_groups > 1 ? up_stride : 0;
     a.gather = rows || rows_per_token > 1 ? rows_per_token : 0;
@@ -747,10 +774,16 @@ muon_status muon_gated_backward(const muon_mat *dh, const muon_mat *gate, const 
       weights(b, wgate, "wgate", gate_stride, n_groups, dh->dtype, false);
       weights(b, wup, "wup", up_stride, n_groups, dh->dtype, false);
       add(b, dx, true, "dx");
+      a.back = 1;
+      a.x2 = dup->data;
+      a.w2 = wup->data;
     }
-    b.check();
-    if (n_groups == 0 || dh->rows == 0) return;
     const bool bf16 = dh->dtype == MUON_BF16;
+    if (dx)
+      parts(st, a, b, bf16);
+    else
+      b.check();
+    if (n_groups == 0 || dh->rows == 0) return;
     GatedGradArgs g{};
     g.dh = dh->data;
     g.ld_dh = dh->ld;
@@ -771,16 +804,13 @@ muon_status muon_gated_backward(const muon_mat *dh, const muon_mat *gate, const 
     if (!dx) return;
     a.x = dgate->data;
     a.ld_x = dgate->ld;
-    a.x2 = dup->data;
     a.ld_x2 = dup->ld;
     a.w = wgate->data;
     a.ld_w = wgate->ld;
     a.w_stride = n_groups > 1 ? gate_stride : 0;
-    a.w2 = wup->data;
     a.ld_w2 = wup->ld;
     a.w2_stride = n_groups > 1 ? up_stride : 0;
     a.scatter = rows != nullptr;
-    a.back = 1;
     a.out = dx->data;
     a.ld_out = dx->ld;
     a.out_rows = dx->rows;
@@ -798,6 +828,22 @@ muon_status muon_expert_backward(const muon_mat *dy, const muon_mat *w, int64_t 
                                  const int32_t *offsets, const int32_t *rows, int32_t gather, int32_t scatter,
                                  const muon_mat *dx) {
   return entry([&](State &st) { expert_product(st, dy, w, group_stride, n_groups, slots, offsets, rows, gather, scatter, dx, true); });
+}
+
+muon_status muon_gated_workspace_size(int32_t dtype, int64_t slots, int64_t n, int64_t k, int64_t groups, int32_t backward,
+                                      size_t *bytes) {
+  return entry([&](State &) {
+    need(bytes, "bytes");
+    *bytes = product_workspace(dtype, slots, n, k, groups, backward, true);
+  });
+}
+
+muon_status muon_expert_workspace_size(int32_t dtype, int64_t slots, int64_t n, int64_t k, int64_t groups, int32_t backward,
+                                       size_t *bytes) {
+  return entry([&](State &) {
+    need(bytes, "bytes");
+    *bytes = product_workspace(dtype, slots, n, k, groups, backward, false);
+  });
 }
 
 muon_status muon_combine_forward(const muon_mat *x, int32_t topk, const float *weights, const int32_t *indices,

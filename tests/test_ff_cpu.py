@@ -121,6 +121,29 @@ def test_expert_refusals(back):
     assert f(x=m(1, 3), y=m(5, 99, 6), slots=0, gather=2, scatter=1) == mu.MUON_OK
 
 
+@pytest.mark.parametrize("gated_", [False, True])
+def test_product_workspace(gated_):
+    """Sizes, their refusals, and calls without the workspace or with one in the way."""
+    f = mu.muon_gated_workspace_size if gated_ else mu.muon_expert_workspace_size
+    for args in ((2, 4, 5, 6), (F32, -1, 5, 6), (F32, MOST + 1, 5, 6), (F32, 4, 0, 6), (F32, 4, 5, 0), (F32, 4, 1 << 30, 6),
+                 (F32, 4, 5, 1 << 30), (F32, 4, 5, 6, -1), (F32, 4, 5, 6, 65537), (F32, 4, 5, 6, 1, 2), (F32, 4, 5, 6, 1, -1)):
+        with pytest.raises(mu.MuonError):
+            f(*args)
+    assert f(BF, 12, 6, 8, 2) == f(F32, 0, 6, 1 << 20) == f(F32, 5, 6, 1 << 20, 0) == f(BF, 8192, 768, 2048, 128) == 0
+    size = f(F32, 12, 6, 1 << 14, 2)
+    assert size > 0 and size % (12 * 6 * 4) == 0 and f(F32, 12, 1 << 14, 6, 2, 1) > 0
+    x, w, y = m(1, 12, 1 << 14, F32), m(2, 6, 1 << 14, F32), m(6, 12, 6, F32)
+    gs = 6 << 14
+    run = lambda **kw: (gated(x=x, wg=w, wu=m(3, 6, 1 << 14, F32), gs=gs, us=gs, rows=None, per=1, h=y, gate=None, up=None, **kw)  # noqa: E731
+                        if gated_ else expert("muon_expert_forward", x=x, w=w, gs=gs, y=y, **kw))
+    assert run() == WORK
+    mu.muon_set_workspace(A * 9, size - 4)
+    assert run() == WORK
+    for at in (1, 2, 4, 6):
+        mu.muon_set_workspace(A * at, size)
+        assert run() == ALIAS, at
+
+
 def comb(x=m(1, 12), topk=3, w=A * 2, idx=A * 3, res=m(4, 4), p=0.1, key=A * 5, y=m(6, 4)):
     return call("muon_combine_forward", x, topk, w, idx, res, p, key, y)
 

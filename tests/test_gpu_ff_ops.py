@@ -475,3 +475,119 @@ def test_products_whose_sum_ends_anywhere_in_a_step(gpu_lib, k):
             z = out_mat(rows, n, dtype)
             mu.muon_expert_backward(x, v, z)
             near(z, r, HALF[dtype] * r.abs() + (2 * k + 2) * U * m, f"backward {rows} {dtype}")
+
+
+# tokens, topk, experts, width, length of the sum: few outputs of long sums, which several workgroups share
+LONG = [(1, 1, 1, 5, 8192), (64, 1, 1, 520, 8192), (100, 3, 4, 129, 4095), (40, 1, 3, 72, 6001), (33, 2, 9, 64, 12288)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tokens,topk,experts,n,k", LONG)
+def test_long_sums_shared_out(gpu_lib, tokens, topk, experts, n, k, dtype):
+    """The parts go to a workspace of exactly the size asked for, full of NaN; slots of no group or token; an infinity in one
+    slot; the same bits twice; too little workspace is refused."""
+    mu, g = gpu_lib, gen(tokens + n + k)
+    code = mu.MUON_BF16 if dtype == BF else mu.MUON_F32
+    slots = tokens * topk
+    ends = torch.arange(experts + 1, device="cuda") * (slots - (2 if experts > 1 else 0)) // experts
+    ends[0] = 1 if experts > 1 else 0
+    offsets, off = ends.to(torch.int32), ends.tolist()
+    rows = torch.randperm(slots, generator=g, device="cuda").to(torch.int32)
+    if experts > 1:
+        rows[5::11] = -1
+    token = torch.where(rows < 0, -1, rows // topk).long()
+    own = torch.arange(slots, device="cuda")
+    used = (own >= off[0]) & (own < off[-1])
+
+    def twice(size, fn, *outs):
+        assert size > 0
+        buf = torch.full((size + 4096,), 255, dtype=torch.uint8, device="cuda")
+        ws = buf[:size]
+        fn(ws)
+        first = [o.clone() for o in outs]
+        ws.fill_(255)
+        fn(ws)
+        for a, b in zip(first, outs):
+            assert torch.equal(a.nan_to_num(), b.nan_to_num())
+        with pytest.raises(mu.MuonError, match="workspace"):
+            fn(ws[:size - 4])
+        assert bool((buf[size:] == 255).all())
+
+    # forward, gated: sums of k
+    x, wg, wu = mat(randn(g, tokens, k), dtype), stack(g, experts, n, k, dtype), stack(g, experts, n, k, dtype)
+    h, gate, up = (out_mat(slots, n, dtype) for _ in range(3))
+    twice(mu.muon_gated_workspace_size(code, slots, n, k, experts), lambda ws: mu.muon_gated_forward(
+        x, wg, wu, h, gate, up, offsets, rows, topk, workspace=ws), h, gate, up)
+    rg, mg = grouped64(x, wg, off, token, False)
+    ru, mu_ = grouped64(x, wu, off, token, False)
+    u = (2 * k + 2) * U
+    near(gate[used], rg[used], (HALF[dtype] * rg.abs() + u * mg)[used], "gate")
+    near(up[used], ru[used], (HALF[dtype] * ru.abs() + u * mu_)[used], "up")
+    v = rg * torch.sigmoid(rg)
+    near(h[used], (v * ru)[used], (HALF[dtype] * (v * ru).abs() + 1.2 * u * mg * (ru.abs() + u * mu_) + v.abs() * u * mu_ +
+                                   16 * U * (rg * ru).abs())[used], "h")
+    assert bool((h[~used] == MARK).all() and (gate[~used] == MARK).all() and (up[~used] == MARK).all())
+    only = out_mat(slots, n, dtype)
+    mu.muon_gated_forward(x, wg, wu, only, offsets=offsets, rows=rows, rows_per_token=topk)  # a workspace of the binding's
+    assert torch.equal(only, h)
+    # forward, scattered; an infinity stays in its slot
+    xs, y = mat(randn(g, slots, k), dtype), out_mat(slots, n, dtype)
+    at = off[0] + (off[-1] - off[0]) // 2
+    xs[at, 7] = float("inf")
+    twice(mu.muon_expert_workspace_size(code, slots, n, k, experts), lambda ws: mu.muon_expert_forward(
+        xs, wg, y, offsets, rows, scatter=True, workspace=ws), y)
+    r, m = grouped64(xs, wg, off, own, False)
+    put = used & (rows >= 0)
+    to = rows[put].long()
+    if int(rows[at]) >= 0:
+        assert not bool(torch.isfinite(y[int(rows[at])]).any())
+    put[at] = False
+    near(y[rows[put].long()], r[put], (HALF[dtype] * r.abs() + u * m)[put], "scattered")
+    other = torch.ones(slots, dtype=torch.bool, device="cuda")
+    other[to] = False
+    assert bool((y[other] == MARK).all())
+    # backward: the weights' rows are summed over
+    wd, we = stack(g, experts, k, n, dtype), stack(g, experts, k, n, dtype)
+    xs = mat(randn(g, slots, k), dtype)
+    y = out_mat(slots, n, dtype)
+    twice(mu.muon_expert_workspace_size(code, slots, k, n, experts, 1), lambda ws: mu.muon_expert_backward(
+        xs, wd, y, offsets, workspace=ws), y)
+    r, m = grouped64(xs, wd, off, own, True)
+    near(y[used], r[used], (HALF[dtype] * r.abs() + u * m)[used], "backward")
+    assert bool((y[~used] == MARK).all())
+    # both products' gradient of x, one sum
+    gate, up, dh = (mat(randn(g, slots, k), dtype) for _ in range(3))
+    dgate, dup, dx = out_mat(slots, k, dtype), out_mat(slots, k, dtype), out_mat(slots, n, dtype)
+    twice(mu.muon_gated_workspace_size(code, slots, k, n, experts, 1), lambda ws: mu.muon_gated_backward(
+        dh, gate, up, wd, we, dgate, dup, dx, offsets, rows, workspace=ws), dx)
+    a, ma = grouped64(dgate, wd, off, own, True)
+    b, mb = grouped64(dup, we, off, own, True)
+    put = used & (rows >= 0)
+    near(dx[rows[put].long()], (a + b)[put], (HALF[dtype] * (a + b).abs() + (4 * k + 2) * U * (ma + mb))[put], "dx")
+    assert bool((dx[other] == MARK).all())
+
+
+def test_long_sums_captured(gpu_lib):
+    """Two graphs whose parts lie in one workspace, replayed in turn on new inputs, as eager calls."""
+    mu, g, n, k = gpu_lib, gen(3), 72, 8192
+    ws = torch.empty(mu.muon_gated_workspace_size(mu.MUON_F32, 40, n, k), dtype=torch.uint8, device="cuda")
+    sets = []
+    for i in range(2):
+        x, wg, wu, h = mat(randn(g, 40, k), F32), stack(g, 1, n, k, F32)[0], stack(g, 1, n, k, F32)[0], out_mat(40, n, F32)
+        mu.muon_gated_forward(x, wg, wu, h, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mu.muon_gated_forward(x, wg, wu, h, workspace=ws)
+        sets.append((graph, x, wg, wu, h))
+    for _ in range(3):
+        for graph, x, wg, wu, h in sets:
+            x.copy_(randn(g, 40, k))
+            h.fill_(MARK)
+            graph.replay()
+            want = out_mat(40, n, F32)
+            mu.muon_set_stream(torch.cuda.current_stream().cuda_stream)
+            mu.muon_gated_forward(x, wg, wu, want)
+            torch.cuda.synchronize()
+            assert torch.equal(h, want)
+    mu.muon_set_stream(None)
