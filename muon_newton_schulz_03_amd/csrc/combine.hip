@@ -17,9 +17,10 @@
 // other. The last run of a row starts eight columns before its end, whatever the
 // width, so that every run is whole; columns that two threads hold get the same
 // value from both. 16384 x 2048 bf16, 8 experts: forward 124 us (5.4 TB/s; a plain
-// copy reaches 5.0-5.2), backward 231 us (4.9 TB/s, 4 of them for the slots'
-// places); dropout of 8192 x 7168 bf16 79 us, of 333 x 2047 float32 5.6 us with
-// its call. Sums are float32 and each result is rounded once.
+// copy reaches 5.0-5.2), backward 226-233 us (4.9 TB/s, 4 of them for the slots'
+// places); dropout of 8192 x 7168 float32 91 us (5.2 TB/s), bf16 60 us, where the
+// generator's instructions count (38 without them); of 333 x 2047 float32 5.4 us
+// with its call. Sums are float32 and each result is rounded once.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -33,15 +34,16 @@ namespace {
 constexpr int kThreads = 256;
 
 // Four words of one counter block.
+// The 64-bit products and the three-way exclusive ors are one instruction each.
 __device__ inline u32x4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
   uint32_t c0 = uint32_t(block), c1 = uint32_t(block >> 32), c2 = uint32_t(offset), c3 = uint32_t(offset >> 32);
   uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t p = uint64_t(0xD2511F53u) * c0, q = uint64_t(0xCD9E8D57u) * c2;
-    c0 = uint32_t(q >> 32) ^ c1 ^ k0;
+    c0 = __builtin_amdgcn_bitop3_b32(uint32_t(q >> 32), c1, k0, 0x96);  // the exclusive or of the three
     c1 = uint32_t(q);
-    c2 = uint32_t(p >> 32) ^ c3 ^ k1;
+    c2 = __builtin_amdgcn_bitop3_b32(uint32_t(p >> 32), c3, k1, 0x96);
     c3 = uint32_t(p);
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
@@ -49,19 +51,21 @@ __device__ inline u32x4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
   return u32x4{c0, c1, c2, c3};
 }
 
-// Which of the eight elements from `first` on are kept, a bit each.
-__device__ inline uint32_t kept8(uint64_t first, uint64_t offset, uint64_t seed, uint32_t threshold) {
+// Which of the eight elements from `first` on are kept.
+__device__ inline void kept8(uint64_t first, uint64_t offset, uint64_t seed, uint32_t threshold, bool (&k)[8]) {
   const uint64_t block = first >> 2;
+  const u32x4 w0 = philox(block, offset, seed), w1 = philox(block + 1, offset, seed);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) k[e] = (e < 4 ? w0[e] : w1[e - 4]) >= threshold;
   const int skip = int(first & 3);
+  if (__ballot(skip != 0) == 0) return;  // of the whole wave, as in rows of a multiple of four
+  asm volatile("");  // a branch: no third block otherwise
+  const u32x4 w2 = philox(block + 2, offset, seed);
   uint32_t bits = 0;
 #pragma unroll
-  for (int b = 0; b < 3; ++b) {
-    if (b == 2 && skip == 0) break;
-    const u32x4 w = philox(block + b, offset, seed);
+  for (int e = 0; e < 12; ++e) bits |= (e < 8 ? k[e < 8 ? e : 0] : w2[e & 3] >= threshold) ? 1u << e : 0u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bits |= (w[e] >= threshold ? 1u : 0u) << (4 * b + e);
-  }
-  return bits >> skip;
+  for (int e = 0; e < 8; ++e) k[e] = bits >> (skip + e) & 1;
 }
 
 // A thread's run of columns: kPerRow threads make a row, kThreads / kPerRow rows
@@ -126,7 +130,7 @@ __global__ __launch_bounds__(kThreads) void combine_fwd_kernel(const CombineArgs
       Raw8<T> res{};
       if (a.res) res = load_run<kTiny>(static_cast<const T *>(a.res) + t * a.ld_res + c, a.cols);
       float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      uint32_t kept = 255u;
+      bool kept[8] = {true, true, true, true, true, true, true, true};
       for (int j0 = 0; j0 < a.topk; j0 += kJ) {
         Raw8<T> x[kJ];
         float w[kJ];
@@ -134,7 +138,10 @@ __global__ __launch_bounds__(kThreads) void combine_fwd_kernel(const CombineArgs
 #pragma unroll
         for (int j = 0; j < kJ; ++j) x[j] = load_run<kTiny>(xs + slot_of<kJ>(a, t, j0 + j) * a.ld_x + c, a.cols);
         choices(a, t, j0, w, idx);
-        if (drop && j0 == 0) kept = kept8(uint64_t(t) * uint64_t(a.cols) + c, offset, seed, a.threshold);
+        if (drop && j0 == 0) {
+          asm volatile("");  // a branch: no words where nothing is dropped
+          kept8(uint64_t(t) * uint64_t(a.cols) + c, offset, seed, a.threshold, kept);
+        }
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
           const bool there = idx[j] >= 0 && (kJ == 1 || j0 + j < a.topk);
@@ -146,7 +153,7 @@ __global__ __launch_bounds__(kThreads) void combine_fwd_kernel(const CombineArgs
       }
       float y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = res.get(e) + (kept >> e & 1 ? sum[e] * a.scale : 0.f);
+      for (int e = 0; e < 8; ++e) y[e] = res.get(e) + (kept[e] ? sum[e] * a.scale : 0.f);
       store_run<kTiny>(static_cast<T *>(a.out) + t * a.ld_out + c, y, a.cols);
     }
   }
@@ -213,18 +220,23 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(const CombineArgs
       }
       for (int c0 = begin; c0 < a.cols; c0 += kPerRow * 8) {
         const Run run = run_at(c0, a.cols);
-        const uint32_t kept = drop ? kept8(uint64_t(t) * uint64_t(a.cols) + run.c, offset, seed, a.threshold) : 255u;
+        bool kept[8] = {true, true, true, true, true, true, true, true};
+        if (drop) {
+          asm volatile("");
+          kept8(uint64_t(t) * uint64_t(a.cols) + run.c, offset, seed, a.threshold, kept);
+        }
         float d[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = kept >> e & 1 ? dy.get(e) * a.scale : 0.f;
+        for (int e = 0; e < 8; ++e) d[e] = kept[e] ? dy.get(e) * a.scale : 0.f;
         if (a.dweights) {
-          const uint32_t counts = kept & 255u << run.own;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) kept[e] = kept[e] && e >= run.own;
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
             keep(x[j], idx[j] >= 0 ? ~0u : 0u);
             float s = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += counts >> e & 1 ? x[j].get(e) * d[e] : 0.f;
+            for (int e = 0; e < 8; ++e) s += kept[e] ? x[j].get(e) * d[e] : 0.f;
             dot[j] += s;
           }
         }

@@ -68,13 +68,17 @@ __device__ inline Raw8<float> load8(const float *p, int n) {
   return r;
 }
 
+// Two values of a word, one instruction.
+__device__ inline uint32_t pack2(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
 __device__ inline Raw8<__bf16> pack8(const float (&f)[8], __bf16) {
   Raw8<__bf16> r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = __builtin_bit_cast(uint16_t, __bf16(f[2 * i]));
-    const uint32_t hi = __builtin_bit_cast(uint16_t, __bf16(f[2 * i + 1]));
-    r.v[i] = lo | hi << 16;
+    r.v[i] = pack2(f[2 * i], f[2 * i + 1]);
   }
   return r;
 }

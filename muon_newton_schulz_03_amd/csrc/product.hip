@@ -280,10 +280,7 @@ __device__ inline void multiply(f32x16 &acc, const u32x4 &x, const u32x4 &w, flo
 __device__ inline void store_row(__bf16 *p, const float (&f)[16], int fh, int n) {
   uint32_t d[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t lo = __builtin_bit_cast(uint16_t, __bf16(f[2 * i])), hi = __builtin_bit_cast(uint16_t, __bf16(f[2 * i + 1]));
-    d[i] = lo | hi << 16;
-  }
+  for (int i = 0; i < 8; ++i) d[i] = pack2(f[2 * i], f[2 * i + 1]);
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     // the lower lane takes the first of two runs of eight columns, the upper one the second
