@@ -477,6 +477,34 @@ def test_products_whose_sum_ends_anywhere_in_a_step(gpu_lib, k):
             near(z, r, HALF[dtype] * r.abs() + (2 * k + 2) * U * m, f"backward {rows} {dtype}")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tokens,n,k", [(40, 24, 40), (700, 130, 65), (21, 16, 8200)])
+def test_lists_without_groups(gpu_lib, tokens, n, k, dtype):
+    """One matrix of weights, no offsets: rows alone gather, scatter and do both; a longer list of a token's entries than one."""
+    mu, g, topk = gpu_lib, gen(tokens + k), 2
+    slots = tokens * topk
+    rows = torch.randperm(slots, generator=g, device="cuda").to(torch.int32)
+    rows[3::17] = -1
+    there = rows >= 0
+    x, w = mat(randn(g, tokens, k), dtype), mat(randn(g, n, k, scale=k ** -0.5), dtype)
+    r, m = grouped64(x, w[None], [0, slots], torch.where(there, rows // topk, -1).long(), False)
+    tol = HALF[dtype] * r.abs() + (2 * k + 2) * U * m
+    y = out_mat(slots, n, dtype)
+    mu.muon_expert_forward(x, w, y, rows=rows, gather=topk)
+    near(y, r, tol, "gathered")
+    z = out_mat(slots, n, dtype)
+    mu.muon_expert_forward(x, w, z, rows=rows, gather=topk, scatter=True)
+    assert torch.equal(z[rows[there].long()], y[there])
+    other = torch.ones(slots, dtype=torch.bool, device="cuda")
+    other[rows[there].long()] = False
+    assert bool((z[other] == MARK).all())
+    h, one = out_mat(slots, n, dtype), mat(randn(g, n, k, scale=k ** -0.5), dtype)
+    mu.muon_gated_forward(x, w, one, h, rows=rows, rows_per_token=topk)
+    u, mu_ = grouped64(x, one[None], [0, slots], torch.where(there, rows // topk, -1).long(), False)
+    v, e, eu = r * torch.sigmoid(r), (2 * k + 2) * U * m, (2 * k + 2) * U * mu_
+    near(h, v * u, HALF[dtype] * (v * u).abs() + 1.2 * e * (u.abs() + eu) + v.abs() * eu + 16 * U * (r * u).abs(), "gated")
+
+
 # tokens, topk, experts, width, length of the sum: few outputs of long sums, which several workgroups share
 LONG = [(1, 1, 1, 5, 8192), (64, 1, 1, 520, 8192), (100, 3, 4, 129, 4095), (40, 1, 3, 72, 6001), (33, 2, 9, 64, 12288)]
 
