@@ -595,6 +595,22 @@ def test_long_sums_shared_out(gpu_lib, tokens, topk, experts, n, k, dtype):
     assert bool((dx[other] == MARK).all())
 
 
+# tokens, width, length of the sum: one group's tiles that go round the CUs once and a little more. Swapped for the backward
+# products. The last with rows that start on no 16-byte boundary.
+LEFT_OVER = [(33, 17000, 640, F32), (500, 2060, 1024, F32), (33, 17000, 3686, BF), (33, 17000, 7168, BF),
+             (33, 17003, 643, F32), (33, 17005, 3689, BF)]
+
+
+@pytest.mark.parametrize("swapped", [False, True])
+@pytest.mark.parametrize("tokens,n,k,dtype", LEFT_OVER)
+def test_columns_left_over_are_shared_out(gpu_lib, tokens, n, k, dtype, swapped):
+    mu, code = gpu_lib, gpu_lib.MUON_BF16 if dtype == BF else gpu_lib.MUON_F32
+    w = (k, n) if swapped else (n, k)
+    sizes = [f(code, tokens, *w, 1, int(swapped)) / (tokens * n * 4) for f in (mu.muon_gated_workspace_size, mu.muon_expert_workspace_size)]
+    assert any(size % 1 for size in sizes), sizes  # parts of some of the columns
+    test_products_of_every_size(mu, tokens, 1, 1, *w, dtype)
+
+
 def test_long_sums_captured(gpu_lib):
     """Two graphs whose parts lie in one workspace, replayed in turn on new inputs, as eager calls."""
     mu, g, n, k = gpu_lib, gen(3), 72, 8192
