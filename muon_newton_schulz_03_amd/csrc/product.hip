@@ -1004,8 +1004,8 @@ bool direct(const ProductArgs &a, int64_t size) {
 enum { kLarge, kWide, kSmall, kMid, kThin, kForms, kThin2 = kForms };
 struct Estimate {
   double us[kForms], shared_us;
-  int splits;  // of 64 x 64 tiles whose sums are shared out; 1 where the sum is too short, shared_us is without the second launch
-  bool thin2;
+  int splits;  // workgroups to a tile whose sums are shared out; 1 where the sum is too short, shared_us is without the second launch
+  bool thin2, thin_parts;
   double least() const { return *std::min_element(us, us + kForms); }
 };
 Estimate estimate(const ProductArgs &a, bool bf16, bool lds) {
@@ -1040,14 +1040,21 @@ Estimate estimate(const ProductArgs &a, bool bf16, bool lds) {
   e.thin2 = !bf16 && tiles(32, 64) > kCus;
   e.shared_us = 1e30;
   e.splits = 1;
-  const double values = slots * a.n * (a.w2 && !a.back ? 2 : 1), one = bf16 ? 0.2 : 0.37, each = bf16 ? 0.13 : 0.3;
-  for (int n = 2; n <= 16 && 8 * n <= steps; ++n) {
-    const double c = std::ceil(tiles(64, 64) * n / kCus);
-    const double us = std::max(std::ceil(steps / n) * std::max(one, each * c), cold(64, 64, c, 37) / n) + 1.3 * c + n * values * 8 / 5e6;
-    if (us >= e.shared_us) continue;
-    e.shared_us = us;
-    e.splits = n;
-  }
+  const double values = slots * a.n * (a.w2 && !a.back ? 2 : 1);
+  auto share = [&](int rows, bool thin, double one, double each, double besides, double rate) {
+    for (int n = 2; n <= 16 && 8 * n <= steps; ++n) {
+      const double c = std::ceil(tiles(rows, 64) * n / kCus);
+      const double us = std::max(std::ceil(steps / n) * std::max(one, each * c), cold(rows, 64, c, rate) / n) + besides * c + n * values * 8 / 5e6;
+      if (us >= e.shared_us) continue;
+      e.shared_us = us;
+      e.splits = n;
+      e.thin_parts = thin;
+    }
+  };
+  e.thin_parts = false;
+  share(64, false, bf16 ? 0.2 : 0.37, bf16 ? 0.13 : 0.3, 1.3, 37);
+  // half of a 64-row tile's waves have nothing to do for up to 32 rows
+  if (slots <= 32) share(32, true, bf16 ? 0.085 : 0.2, bf16 ? 0.09 : 0.17, bf16 ? 3 : 1.5, 52);
   return e;
 }
 
@@ -1084,7 +1091,10 @@ hipError_t product(const ProductArgs &all, hipStream_t s) {
   a.out = static_cast<T *>(a.out) + from;
   a.gate = a.gate ? static_cast<T *>(a.gate) + from : nullptr;
   a.up = a.up ? static_cast<T *>(a.up) + from : nullptr;
-  lds ? tiled<T, Mid, true, true>(a, s) : tiled<T, Mid, false, true>(a, s);
+  if (a.thin_parts)
+    lds ? tiled<T, Thin2, true, true>(a, s) : tiled<T, Thin2, false, true>(a, s);
+  else
+    lds ? tiled<T, Mid, true, true>(a, s) : tiled<T, Mid, false, true>(a, s);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t blocks = std::min<int64_t>((a.slots * ((a.n + 7) / 8) + 255) / 256, 4096);
@@ -1146,7 +1156,8 @@ hipError_t gated_grad(const GatedGradArgs &a, hipStream_t s) {
 // A long sum with few tiles is shared out to several workgroups a tile, whose
 // parts a second launch adds: 8 bytes a part and value, and what the launch costs.
 // 64 tokens, 1024x8192: float32 82 -> 20 us, bf16 19 -> 13; 1 token, 2048x2304:
-// float32 26 -> 14, bf16 stays at 8, two launches take 12. Of one group's tiles
+// float32 26 -> 13, bf16 stays at 8, two launches take 12. Up to 32 rows in 32-row
+// tiles: 16 tokens, 7168x18432, float32, 146 -> 123; 5 tokens, 7168x5408, 50 -> 43. Of one group's tiles
 // that go round the CUs more than a whole number of times, those left over are
 // shared out, two launches of their own: 64 tokens, 18432x7168, gated, 288 tiles
 // of 64 x 64 (256 of them take 92), 133 -> 107-112 us; float32, 348 tokens, 3686x4512,
@@ -1154,6 +1165,7 @@ hipError_t gated_grad(const GatedGradArgs &a, hipStream_t s) {
 void product_plan(ProductArgs &a, bool bf16) {
   a.splits = 1;
   a.whole = 0;
+  a.thin_parts = 0;
   if (a.slots == 0 || a.groups == 0) return;
   const Estimate e = estimate(a, bf16, true);
   double best = e.least();
@@ -1161,6 +1173,7 @@ void product_plan(ProductArgs &a, bool bf16) {
   if (shared < best) {
     best = shared;
     a.splits = e.splits;
+    a.thin_parts = e.thin_parts;
   }
   if (a.groups > 1) return;
   const int forms[][2] = {{256, 256}, {128, 256}, {64, 128}, {64, 64}, {32, 64}};
@@ -1176,6 +1189,7 @@ void product_plan(ProductArgs &a, bool bf16) {
     if (us >= best) continue;
     best = us;
     a.splits = rest.splits;
+    a.thin_parts = rest.thin_parts;
     a.whole = w.n;
   }
 }

@@ -135,6 +135,7 @@ struct ProductArgs {
   int32_t act;             // Activation
   int32_t tiles_n;
   int32_t splits;          // workgroups that share a tile's sums
+  int32_t thin_parts;      // whether those tiles have 32 rows instead of 64
   int32_t whole;           // of one group: the first columns whose tiles are not shared
   float *part;             // their parts when there are several
 };
@@ -183,7 +184,7 @@ hipError_t launch_wgrad(const WgradArgs &a, bool bf16, hipStream_t s);
 void route_plan(RouteFwdArgs &a);
 hipError_t launch_route_fwd(const RouteFwdArgs &a, bool bf16, hipStream_t s);
 hipError_t launch_route_bwd(const RouteBwdArgs &a, bool bf16, hipStream_t s);
-// Fills splits and whole of a (from its sizes, groups and the kind of product: back, and
+// Fills splits, thin_parts and whole of a (from its sizes, groups and the kind of product: back, and
 // whether x2 and w2 are set); the parts take product_part_bytes.
 void product_plan(ProductArgs &a, bool bf16);
 size_t product_part_bytes(const ProductArgs &a);

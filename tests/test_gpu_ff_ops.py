@@ -506,7 +506,8 @@ def test_lists_without_groups(gpu_lib, tokens, n, k, dtype):
 
 
 # tokens, topk, experts, width, length of the sum: few outputs of long sums, which several workgroups share
-LONG = [(1, 1, 1, 5, 8192), (64, 1, 1, 520, 8192), (100, 3, 4, 129, 4095), (40, 1, 3, 72, 6001), (33, 2, 9, 64, 12288)]
+LONG = [(1, 1, 1, 5, 8192), (64, 1, 1, 520, 8192), (100, 3, 4, 129, 4095), (40, 1, 3, 72, 6001), (33, 2, 9, 64, 12288),
+        (12, 2, 5, 72, 8001), (16, 2, 3, 264, 9000)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
