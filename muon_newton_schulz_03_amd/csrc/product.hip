@@ -1033,8 +1033,9 @@ Estimate estimate(const ProductArgs &a, bool bf16, bool lds) {
   e.us[kSmall] = bf16 ? us_of(64, 128, 0.22, 0.17, 1.8) : us_of(64, 128, 0.62, 0.5, 1.8);
   e.us[kMid] = bf16 ? us_of(64, 64, 0.2, 0.13, 1.3, 37) : us_of(64, 64, 0.37, 0.3, 1.3, 37);
   e.us[kThin] = bf16 ? us_of(32, 64, 0.085, 0.09, 3, 52) : us_of(32, 64, 0.2, 0.17, 1.5, 52);
-  // a streaming workgroup needs a step between two tiles, and room for the groups
-  if (lds && (a.k == 0 || (a.offsets && a.groups > kStreamGroups))) e.us[kLarge] = 1e30;
+  // a streaming workgroup needs a step between two tiles, and room for the groups;
+  // from sizes alone, as the workspace is asked for without the lists
+  if (lds && (a.k == 0 || a.groups > kStreamGroups)) e.us[kLarge] = 1e30;
   // memory's latency asks for long loads, float32 products for two workgroups a CU:
   // 1024 tokens, 1024x2048, 40 us against 46; 64 tokens, 4096x4096, gated, 52 against 48
   e.thin2 = !bf16 && tiles(32, 64) > kCus;
