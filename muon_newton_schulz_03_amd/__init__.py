@@ -766,10 +766,12 @@ def muon_gated_backward(dh, gate, up, wgate, wup, dgate, dup, dx=None, offsets=N
 
 
 def _expert(fn, back, x, w, y, offsets, rows, gather, scatter, workspace):
+    if gather and scatter and rows is None:
+        raise ValueError("rows: needed with gather and scatter, whose slots they count")
     d = _enter(x)
     w_mat, stride, groups = _stack("w", w, d)
     x_mat, y_mat = _mat("x", x, d), _mat("y", y, d)
-    slots = x.shape[0] if not gather else y.shape[0] if not scatter else rows.shape[0] if rows is not None else 0
+    slots = x.shape[0] if not gather else y.shape[0] if not scatter else rows.shape[0]
     args = (x_mat, w_mat, stride, groups, slots, *_slots(offsets, rows, groups, slots, d), int(gather), int(scatter), y_mat)
     _with_scratch(muon_expert_workspace_size(_codes[x.dtype], slots, w.shape[-2], w.shape[-1], groups, back), workspace, d, fn, *args)
 
