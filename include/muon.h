@@ -396,7 +396,7 @@ muon_status muon_ckpt_load(const muon_ckpt *ckpt, const muon_mat *out);
  *   x         tokens x k.
  *   grads     descriptor of the first group's n x k gradient, dy's dtype;
  *             group g's lies g * group_stride elements further. Overwritten;
- *             zeros for an empty group.
+ *             zeros for an empty group. Its data may be NULL with no groups.
  *   offsets   device, n_groups + 1 ascending int32 (NULL with one group: every
  *             slot). Values outside [0, slots] count as the nearest bound.
  *   rows      device, int32 per slot (NULL: rows[s] = s). A slot whose token
@@ -463,7 +463,7 @@ muon_status muon_route_backward(const muon_mat *logits, int32_t topk, int32_t re
  * with one group: every slot) and rows (device, an int32 per slot) are what
  * muon_route_forward writes. Offsets outside [0, slots] count as the nearest
  * bound. Rows of an output that belong to no group are left as they were; with
- * no groups or no slots nothing is written.
+ * no groups (the weights' data may then be NULL) or no slots nothing is written.
  *
  * Weights: the first group's matrix, the others' `stride` elements further
  * each; all operands of a call but offsets, rows, weights, indices and

@@ -117,14 +117,15 @@ void need(const void *p, const char *name) {
   if (!p) refuse(MUON_ERR_INVALID_ARG, "%s must not be NULL", name);
 }
 
-// A matrix operand: dtype, shape, pitch, alignment. rows may be 0 (no data).
-void matrix(const muon_mat *m, const char *name, int64_t max_cols) {
+// A matrix operand: dtype, shape, pitch, alignment. Without rows, or as the first
+// of none (`none`), it needs no data.
+void matrix(const muon_mat *m, const char *name, int64_t max_cols, bool none = false) {
   need(m, name);
   if (m->dtype != MUON_F32 && m->dtype != MUON_BF16) refuse(MUON_ERR_DTYPE, "%s: unknown dtype", name);
   if (m->rows < 0 || m->rows > kMaxIndex || m->cols <= 0 || m->cols > max_cols)
     refuse(MUON_ERR_SHAPE, "%s: rows must lie in [0, 2^31), cols in [1, %lld]", name, (long long)max_cols);
   if (m->ld < m->cols || !fits(m->rows, m->ld)) refuse(MUON_ERR_SHAPE, "%s: ld < cols, or rows * ld > 2^60", name);
-  if (m->rows > 0 && !m->data) refuse(MUON_ERR_INVALID_ARG, "%s: NULL data", name);
+  if (m->rows > 0 && !m->data && !none) refuse(MUON_ERR_INVALID_ARG, "%s: NULL data", name);
   if (reinterpret_cast<uintptr_t>(m->data) % esize(m->dtype))
     refuse(MUON_ERR_ALIGN, "%s: data not aligned to its element size", name);
 }
@@ -251,7 +252,7 @@ void activation_of(int32_t activation) {
 void expert_product(State &st, const muon_mat *x, const muon_mat *w, int64_t group_stride, int32_t n_groups, int64_t slots,
                     const int32_t *offsets, const int32_t *rows, int32_t gather, int32_t scatter, const muon_mat *y, bool back) {
   matrix(x, "x", kMaxIndex / 2);
-  matrix(w, "w", kMaxIndex / 2);
+  matrix(w, "w", kMaxIndex / 2, n_groups == 0);
   matrix(y, "y", kMaxIndex / 2);
   if (y->dtype != x->dtype) refuse(MUON_ERR_DTYPE, "x and y differ in dtype");
   if (gather < 0) refuse(MUON_ERR_INVALID_ARG, "gather must be >= 0");
@@ -533,7 +534,7 @@ muon_status muon_ckpt_weight_grad(const muon_mat *dy, const muon_ckpt *x, const 
     matrix(dy, "dy", kMaxIndex / 2);
     WgradArgs a{};
     a.x = checkpoint(x, "x");
-    matrix(grads, "grads", kMaxIndex / 2);
+    matrix(grads, "grads", kMaxIndex / 2, n_groups == 0);
     if (grads->rows < 1) refuse(MUON_ERR_SHAPE, "grads: no rows");
     if (grads->dtype != dy->dtype) refuse(MUON_ERR_DTYPE, "dy and grads differ in dtype");
     if (grads->rows != dy->cols || grads->cols != x->cols) refuse(MUON_ERR_SHAPE, "a gradient is dy's columns x x's columns");
@@ -695,8 +696,8 @@ muon_status muon_gated_forward(const muon_mat *x, const muon_mat *wgate, int64_t
                                const muon_mat *up) {
   return entry([&](State &st) {
     matrix(x, "x", kMaxIndex / 2);
-    matrix(wgate, "wgate", kMaxIndex / 2);
-    matrix(wup, "wup", kMaxIndex / 2);
+    matrix(wgate, "wgate", kMaxIndex / 2, n_groups == 0);
+    matrix(wup, "wup", kMaxIndex / 2, n_groups == 0);
     matrix(h, "h", kMaxIndex / 2);
     const muon_mat *saved[2] = {gate, up};
     const char *names[2] = {"gate", "up"};
@@ -762,8 +763,8 @@ muon_status muon_gated_backward(const muon_mat *dh, const muon_mat *gate, const 
     ProductArgs a{};
     slots_of(a, b, dh->rows, n_groups, offsets, rows);
     if (dx) {
-      matrix(wgate, "wgate", kMaxIndex / 2);
-      matrix(wup, "wup", kMaxIndex / 2);
+      matrix(wgate, "wgate", kMaxIndex / 2, n_groups == 0);
+      matrix(wup, "wup", kMaxIndex / 2, n_groups == 0);
       matrix(dx, "dx", kMaxIndex / 2);
       same(wup, "wup", wgate, "wgate");
       if (dx->dtype != dh->dtype) refuse(MUON_ERR_DTYPE, "dh and dx differ in dtype");
