@@ -769,7 +769,7 @@ muon_status muon_gated_backward(const muon_mat *dh, const muon_mat *gate, const 
       same(wup, "wup", wgate, "wgate");
       if (dx->dtype != dh->dtype) refuse(MUON_ERR_DTYPE, "dh and dx differ in dtype");
       if (wgate->rows != dh->cols || wgate->cols != dx->cols) refuse(MUON_ERR_SHAPE, "weights are dh's columns x dx's columns");
-      if (!rows && dx->rows != dh->rows) refuse(MUON_ERR_SHAPE, "without rows, dx has a row for each slot");
+      if (!rows && dh->rows > 0 && dx->rows != dh->rows) refuse(MUON_ERR_SHAPE, "without rows, dx has a row for each slot");
       a.x_rows = dh->rows;
       sizes(a, dx->cols, dh->cols);
       weights(b, wgate, "wgate", gate_stride, n_groups, dh->dtype, false);

@@ -42,3 +42,13 @@ def test_weights_of_no_groups_have_no_data():
                 call("muon_ckpt_weight_grad", h, ckpt, w, 48, groups, A * 9, None, 1)]
     assert calls(0) == [mu.MUON_OK] * 5
     assert calls(1) == calls(2) == [mu.MUON_ERR_INVALID_ARG] * 5
+
+
+def test_no_slots_leave_dx_of_any_rows():
+    """A rank that no token came to: rows of no slots have no address, and dx, whose rows they would name, its own number of
+    rows; nothing is written."""
+    w = m(1, 6, 8)
+    back = lambda slots, dx: call("muon_gated_backward", *(m(i if slots else 0, slots, 6) for i in (2, 3, 4)), w, 48, w, 48, 2, A * 5,  # noqa: E731
+                                  None, 0, *(m(i if slots else 0, slots, 6) for i in (6, 7)), dx)
+    assert back(0, m(8, 15, 8)) == back(0, m(0, 0, 8)) == mu.MUON_OK
+    assert back(12, m(8, 15, 8)) == mu.MUON_ERR_SHAPE
