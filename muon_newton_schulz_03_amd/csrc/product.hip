@@ -353,12 +353,13 @@ __device__ inline u32x4 scalar(const u32x4 &v) { return u32x4{scalar(v[0]), scal
 // 16 bytes a lane from the buffer straight to LDS (lane l's at lds + 16 l). In
 // assembly, because the compiler would wait for all of these loads before each
 // transposing LDS read; the waits that they need stand at the top of each step.
-// The wait states: one between m0 and the load, five from a vector instruction
-// that has written a scalar operand.
+// The LDS address goes in through m0, which the compiler so knows to have set; the
+// wait states: one from there to the load, five from a vector instruction that has
+// written a scalar operand.
 __device__ inline void to_lds(const u32x4 &r, uint32_t lds, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
-               : "s"(scalar(lds)), "v"(voff), "s"(r), "s"(scalar(soff))
+               : "{m0}"(scalar(lds)), "v"(voff), "s"(r), "s"(scalar(soff))
                : "memory");
 }
 
