@@ -1,6 +1,24 @@
-"""How exact a long sum has to be: shared by the tests on the CPU (that the bound
-sees lost precision) and on the GPU."""
+"""Products that stream from tile to tile in 256 x 256 tiles, or take those tiles
+through registers, and how exact a long sum has to be: shared by the tests on the
+CPU (that the plan takes these forms, that the bounds see lost precision) and on
+the GPU."""
 U = 2.0 ** -24
+FORWARD, GATED, BACKWARD, BOTH = range(4)  # BOTH: the gated block's dx, a sum over both products
+
+# kind, slots, groups, columns, length of the sum, type, whether rows lie in whole 16-byte chunks (else the tiles go through
+# registers). More tiles than CUs in each, so that a workgroup goes from one to the next; sums that end inside a step (64
+# values of bf16, 32 of float32) and inside a chunk, of one step and a part and of several; one group without lists, and
+# uneven groups.
+STREAMING = [
+    (kind, slots, groups, n // 2 if kind == GATED else n, k, "bf16", aligned)
+    for kind in range(4) for slots, groups, n, k, aligned in (
+        (20000, 1, 1032, 136, True), (8192, 1, 4096, 520, True), (20000, 24, 1032, 264, True), (20000, 40, 1032, 136, True),
+        (20000, 1, 1031, 517, False), (20000, 24, 1031, 199, False), (20000, 40, 1031, 131, False))
+] + [
+    (kind, slots, groups, n // 2 if kind == GATED and groups > 1 else n, k, "f32", aligned)
+    for kind in range(4) for slots, groups, n, k, aligned in (
+        (20000, 1, 4096, 264, True), (20000, 24, 1032, 136, True), (20000, 40, 1032, 72, True), (20000, 40, 1031, 67, False))
+]
 
 
 def tight(got, ref, terms, what):

@@ -1,12 +1,131 @@
-"""Long sums that workgroups share, against 64-bit sums on the GPU in norm, where
-lost precision shows."""
+"""The products' streaming form and long sums that workgroups share, against 64-bit
+sums on the GPU: value by value (as in test_gpu_ff_ops.py) and in norm, where lost precision shows.
+
+That the sizes take the forms meant here is tested on the CPU
+(test_product_plan_cpu.py)."""
 import pytest
 import torch
 
-from ff_forms import tight
-from test_gpu_ff_ops import BF, F32, LONG, gen, grouped64, mat, out_mat, stack
+from ff_forms import BACKWARD, BOTH, FORWARD, GATED, STREAMING, tight
+from test_gpu_ff_ops import BF, F32, HALF, LONG, MARK, U, gen, grouped64, mat, near, out_mat, randn, stack
 
 pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": BF, "f32": F32}
+
+
+def uneven(g, slots, groups):
+    """Offsets of groups of any length, some of one tile and less, an empty one, and slots behind the last."""
+    share = torch.rand(groups, generator=g, device="cuda") + 0.05
+    share[groups // 2] = 0
+    ends = (share.cumsum(0) / share.sum() * (slots - 77)).long()
+    return torch.cat([ends.new_zeros(1), ends])
+
+
+def case(g, slots, groups):
+    """(offsets, rows, topk): lists, or none for one group. A few entries name no row."""
+    if groups == 1:
+        return None, None, 1
+    rows = torch.randperm(slots, generator=g, device="cuda").to(torch.int32)
+    rows[::101] = -1
+    return uneven(g, slots, groups).to(torch.int32), rows, 4
+
+
+def both(got, ref, mag, dtype, terms, what):
+    near(got, ref, HALF[dtype] * ref.abs() + (2 * terms + 2) * U * mag, what)
+    tight(got, ref, terms, what)
+
+
+@pytest.mark.parametrize("kind,slots,groups,n,k,dtype,aligned", STREAMING)
+def test_streaming_products(gpu_lib, kind, slots, groups, n, k, dtype, aligned):
+    mu, g, dtype = gpu_lib, gen(slots + groups + n + k), TYPES[dtype]
+    offsets, rows, topk = case(g, slots, groups)
+    off = [0, slots] if offsets is None else offsets.tolist()
+    lists = dict(offsets=offsets, rows=rows)
+    own = torch.arange(slots, device="cuda")
+    used = own < off[-1]
+    named = used if rows is None else used & (rows >= 0)
+    to = own if rows is None else rows.long()
+    other = torch.ones(slots, dtype=torch.bool, device="cuda")
+    other[to[named]] = False  # rows of a scattered output that no slot names
+    if kind == GATED:
+        x, w, u = mat(randn(g, -(-slots // topk), k), dtype), stack(g, groups, n, k, dtype), stack(g, groups, n, k, dtype)
+        h, gate, up = (out_mat(slots, n, dtype) for _ in range(3))
+        mu.muon_gated_forward(x, w, u, h, gate, up, rows_per_token=topk, **lists)
+        token = own if rows is None else torch.where(rows < 0, -1, rows // topk).long()
+        rg, mg = grouped64(x, w, off, token, False)
+        ru, mu_ = grouped64(x, u, off, token, False)
+        both(gate[used], rg[used], mg[used], dtype, k, "gate")
+        both(up[used], ru[used], mu_[used], dtype, k, "up")
+        # the activation takes the float32 products; slopes lie within 1.2 of 0
+        e, eu = (2 * k + 2) * U * mg, (2 * k + 2) * U * mu_
+        v = rg * torch.sigmoid(rg)
+        near(h[used], (v * ru)[used], (HALF[dtype] * (v * ru).abs() + 1.2 * e * (ru.abs() + eu) + v.abs() * eu + 16 * U * (rg * ru).abs())[used], "h")
+        for t in (h, gate, up):
+            assert bool((t[~used] == MARK).all())
+        again = [out_mat(slots, n, dtype) for _ in range(3)]
+        mu.muon_gated_forward(x, w, u, *again, rows_per_token=topk, **lists)
+        assert all(torch.equal(a, b) for a, b in zip(again, (h, gate, up)))
+    elif kind == BOTH:
+        dh, gate, up = (mat(randn(g, slots, k), dtype) for _ in range(3))
+        w, u = stack(g, groups, k, n, dtype), stack(g, groups, k, n, dtype)
+        dgate, dup, dx = out_mat(slots, k, dtype), out_mat(slots, k, dtype), out_mat(slots, n, dtype)
+        mu.muon_gated_backward(dh, gate, up, w, u, dgate, dup, dx, **lists)
+        a, ma = grouped64(dgate, w, off, own, True)
+        b, mb = grouped64(dup, u, off, own, True)
+        both(dx[to[named]], (a + b)[named], (ma + mb)[named], dtype, 2 * k, "dx")
+        assert bool((dx[other] == MARK).all())
+        again = out_mat(slots, n, dtype)
+        mu.muon_gated_backward(dh, gate, up, w, u, dgate, dup, again, **lists)
+        assert torch.equal(again, dx)
+    else:
+        back = kind == BACKWARD
+        call = mu.muon_expert_backward if back else mu.muon_expert_forward
+        x, w = mat(randn(g, slots, k), dtype), stack(g, groups, *((k, n) if back else (n, k)), dtype)
+        y = out_mat(slots, n, dtype)
+        call(x, w, y, offsets)
+        ref, mag = grouped64(x, w, off, own, back)
+        both(y[used], ref[used], mag[used], dtype, k, "slot order")
+        assert bool((y[~used] == MARK).all())
+        if rows is not None:
+            z = out_mat(slots, n, dtype)
+            call(x, w, z, **lists, scatter=True)
+            assert torch.equal(z[to[named]], y[named]) and bool((z[other] == MARK).all())
+            # gathered and scattered; a row of x that no entry names is not read
+            z = out_mat(slots, n, dtype)
+            tokens = mat(randn(g, slots // topk, k), dtype)
+            token = torch.where(rows < 0, -1, rows // topk).long()
+            call(tokens, w, z, **lists, gather=topk, scatter=True)
+            ref, mag = grouped64(tokens, w, off, token, back)
+            both(z[to[named]], ref[named], mag[named], dtype, k, "gathered and scattered")
+            assert bool((z[other] == MARK).all())
+
+
+def test_streaming_products_behind_a_captured_graph(gpu_lib):
+    """Replays of the streaming forms on new inputs, eager ones between them, bit for bit."""
+    mu, g = gpu_lib, gen(5)
+    kind, slots, groups, n, k, dtype, _ = next(s for s in STREAMING if s[0] == BOTH and s[2] > 1)
+    assert dtype == "bf16"
+    offsets, rows, _ = case(g, slots, groups)
+    ins = [mat(randn(g, slots, k), BF) for _ in range(3)]
+    w, u = stack(g, groups, k, n, BF), stack(g, groups, k, n, BF)
+    outs = [[out_mat(slots, c, BF) for c in (k, k, n)] for _ in range(2)]
+    step = lambda o: mu.muon_gated_backward(*ins, w, u, *o, offsets=offsets, rows=rows)  # noqa: E731
+    step(outs[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(outs[0])
+    for _ in range(3):
+        for t in ins:
+            t.copy_(randn(g, slots, k))
+        for t in outs[0] + outs[1]:
+            t.fill_(MARK)
+        graph.replay()
+        step(outs[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+    mu.muon_set_stream(None)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
