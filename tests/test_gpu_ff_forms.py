@@ -1,13 +1,16 @@
-"""The products' streaming form and long sums that workgroups share, against 64-bit
-sums on the GPU: value by value (as in test_gpu_ff_ops.py) and in norm, where lost precision shows.
+"""The products' streaming form, long sums that workgroups share, and launches of
+more workgroups than a grid's first dimension holds, against 64-bit sums on the
+GPU: value by value (as in test_gpu_ff_ops.py) and in norm, where lost precision shows.
 
 That the sizes take the forms meant here is tested on the CPU
 (test_product_plan_cpu.py)."""
+import numpy as np
 import pytest
 import torch
 
 from ff_forms import BACKWARD, BOTH, FORWARD, GATED, STREAMING, tight
-from test_gpu_ff_ops import BF, F32, HALF, LONG, MARK, U, gen, grouped64, mat, near, out_mat, randn, stack
+from oracle import ff_oracle as F
+from test_gpu_ff_ops import BF, F32, HALF, KEY, LONG, MARK, U, gen, grouped64, key_of, mat, near, out_mat, randn, stack
 
 pytestmark = pytest.mark.gpu
 
@@ -156,3 +159,89 @@ def test_shared_sums_in_norm(gpu_lib, tokens, topk, experts, n, k, dtype):
     mu.muon_gated_backward(x, gate, up, w, u, dgate, dup, dx, offsets)
     # the gradients' values are no normal ones, but independent with mean near 0: both parts of the sum grow alike
     tight(dx, grouped64(dgate, w, off, own, True)[0] + grouped64(dup, u, off, own, True)[0], 2 * k, "dx")
+
+
+# ---------------------------------------------------------------------------
+# grids past their first dimension's bound of 2^20 workgroups, and the strides behind it
+# ---------------------------------------------------------------------------
+
+def test_rows_of_more_than_2_20_workgroups(gpu_lib):
+    """A workgroup takes one row of more than 512 columns: the rows behind 2^20 of them are a second turn's. Dropout, the sum
+    over experts and its backward pass, the gated block's gradients."""
+    mu, g = gpu_lib, gen(91)
+    rows, cols, p = (1 << 20) + 37, 520, 0.25
+    spans = [slice(0, 5), slice((1 << 20) - 3, (1 << 20) + 5), slice(rows - 5, rows)]
+    key, f = key_of(*KEY), {}
+    for s in spans:
+        f[s.start] = F.kept(s.start * cols, (s.stop - s.start) * cols, p, *KEY).reshape(-1, cols) / (1 - p)
+    x = torch.empty((rows, cols), dtype=BF, device="cuda").normal_(generator=g)
+    y, dx, dw = torch.full_like(x, MARK), torch.full_like(x, MARK), torch.full((rows, 1), MARK, device="cuda")
+    weights = torch.rand((rows, 1), generator=g, device="cuda") + 0.5
+    mu.muon_combine_forward(x, y, weights, p=p, key=key)
+    dy = torch.empty_like(x).normal_(generator=g)
+    mu.muon_combine_backward(dy, x, dx, dw, weights, p=p, key=key)
+    for s in spans:
+        X, W, D = x[s].double().cpu().numpy(), weights[s].double().cpu().numpy(), dy[s].double().cpu().numpy() * f[s.start]
+        for got, ref in ((y[s], X * W * f[s.start]), (dx[s], W * D)):
+            assert np.all(np.abs(got.double().cpu().numpy() - ref) <= (HALF[BF] + 4 * U) * np.abs(ref)), s
+        # sums of 65 runs of eight products
+        assert np.all(np.abs(dw[s].double().cpu().numpy()[:, 0] - (X * D).sum(1)) <= (8 + 16) * U * np.abs(X * D).sum(1)), s
+    z = torch.full_like(x, MARK)
+    mu.muon_dropout_forward(x, z, p, key, residual=dy)
+    for s in spans:
+        ref = dy[s].double().cpu().numpy() + x[s].double().cpu().numpy() * f[s.start]
+        tol = HALF[BF] * np.abs(ref) + 4 * U * (dy[s].double().abs().cpu().numpy() + np.abs(x[s].double().cpu().numpy() * f[s.start]))
+        assert np.all(np.abs(z[s].double().cpu().numpy() - ref) <= tol), s
+    assert not bool((y == MARK).all(1).any()) and not bool((dx == MARK).all(1).any()) and not bool((dw == MARK).any())
+    del x, y, z, dy, dx
+    # a workgroup a row from 1025 columns on
+    cols = 1032
+    dh, gate, up = (torch.empty((rows, cols), dtype=BF, device="cuda").normal_(generator=g) for _ in range(3))
+    dgate, dup = torch.full_like(dh, MARK), torch.full_like(dh, MARK)
+    mu.muon_gated_backward(dh, gate, up, None, None, dgate, dup)
+    for s in spans:
+        part = [torch.empty((s.stop - s.start, cols), dtype=BF, device="cuda") for _ in range(2)]
+        mu.muon_gated_backward(dh[s], gate[s], up[s], None, None, *part)
+        v, slope = F.act(gate[s].double().cpu().numpy(), "silu")
+        D, V = dh[s].double().cpu().numpy(), up[s].double().cpu().numpy()
+        assert torch.equal(part[0], dgate[s]) and torch.equal(part[1], dup[s])
+        tol = HALF[BF] * np.abs(D * V * slope) + 16 * U * np.abs(D * V) * (1 + gate[s].double().abs().cpu().numpy())
+        near(dgate[s], torch.from_numpy(D * V * slope).cuda(), torch.from_numpy(tol).cuda(), "dgate")
+    assert not bool((dgate == MARK).all(1).any()) and not bool((dup == MARK).all(1).any())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_columns_of_more_workgroups_than_a_row_has(gpu_lib, dtype):
+    """64 workgroups take 131072 columns of a row: those behind are a second turn's."""
+    mu, g, p = gpu_lib, gen(92), 0.1
+    rows, cols = 3, 131072 + 77
+    x, res, y = mat(randn(g, rows, cols), dtype), mat(randn(g, rows, cols), dtype), out_mat(rows, cols, dtype)
+    f = torch.from_numpy(F.dropped((rows, cols), p, *KEY)).cuda()
+    mu.muon_dropout_forward(x, y, p, key_of(*KEY), residual=res)
+    ref = res.double() + x.double() * f
+    near(y, ref, HALF[dtype] * ref.abs() + 4 * U * (res.double().abs() + (x.double() * f).abs()), "y")
+    dx, dw = out_mat(rows, cols, dtype), torch.empty((rows, 1), device="cuda")
+    mu.muon_combine_backward(x, res, dx, dw, torch.ones((rows, 1), device="cuda"), p=p, key=key_of(*KEY))
+    d = x.double() * f
+    near(dx, d, (HALF[dtype] + 4 * U) * d.abs(), "dx")
+    near(dw[:, 0], (res.double() * d).sum(1), (8 + cols / 2048 + 16) * U * (res.double() * d).abs().sum(1), "dweights")
+    gate, up, dgate, dup = mat(randn(g, rows, cols), dtype), mat(randn(g, rows, cols), dtype), out_mat(rows, cols, dtype), out_mat(rows, cols, dtype)
+    mu.muon_gated_backward(x, gate, up, None, None, dgate, dup)
+    s = torch.sigmoid(gate.double())
+    ref = x.double() * gate.double() * s
+    near(dup, ref, HALF[dtype] * ref.abs() + 16 * U * (x.double() * gate.double()).abs(), "dup")
+    ref = x.double() * up.double() * s * (1 + gate.double() * (1 - s))
+    near(dgate, ref, HALF[dtype] * ref.abs() + 16 * U * (x.double() * up.double()).abs() * (1 + gate.double().abs()), "dgate")
+
+
+def test_products_of_more_than_2_20_tiles(gpu_lib):
+    """65536 groups of a slot each, 17 or more tiles across: the launch's second dimension."""
+    mu, g = gpu_lib, gen(93)
+    groups, n, k = 65536, 4352, 8
+    w = torch.empty((groups, n, k), dtype=BF, device="cuda").normal_(0, k ** -0.5, generator=g)
+    x, y = mat(randn(g, groups, k), BF), torch.full((groups, n), MARK, dtype=BF, device="cuda")
+    mu.muon_expert_forward(x, w, y, torch.arange(groups + 1, dtype=torch.int32, device="cuda"))
+    for lo in range(0, groups, 4096):
+        terms = w[lo:lo + 4096].float() * x[lo:lo + 4096].float()[:, None, :]
+        ref, mag = terms.double().sum(2), terms.double().abs().sum(2)
+        near(y[lo:lo + 4096], ref, HALF[BF] * ref.abs() + (2 * k + 2) * U * mag, lo)
