@@ -661,16 +661,12 @@ __global__ __launch_bounds__(F::kThreads, F::kPerSimd) void product_kernel(const
       for (int q = 0; q < kW; ++q)  // a load's rows are of one of the gated block's products
         to_lds(kGated && ((lw * kW + q) * (64 / F::kChunks) & 32) ? wr2 : wr, st + F::kABytes + (lw * kW + q) * 1024, ow[q], sw);
     };
-    // s_waitcnt with vmcnt alone constrained: the loads of `n` steps may be under way
+    // s_waitcnt with vmcnt alone constrained: where `n` more steps follow, the next one's loads may be under way
     auto landed = [&](int n) __attribute__((always_inline)) {
       constexpr int kL = kX + kW;
-      static_assert(kL * (kAhead - 1) < 64 && kAhead <= 4 && kParts % 2 == 0);
+      static_assert(kAhead <= 2 && kL < 64 && kParts % 2 == 0);
       if (!loader) return;
-      if (n >= 3 && kAhead > 3)
-        __builtin_amdgcn_s_waitcnt((3 * kL & 15) | (3 * kL >> 4) << 14 | 0x0F70);
-      else if (n >= 2 && kAhead > 2)
-        __builtin_amdgcn_s_waitcnt((2 * kL & 15) | (2 * kL >> 4) << 14 | 0x0F70);
-      else if (n >= 1 && kAhead > 1)
+      if (n >= 1 && kAhead > 1)
         __builtin_amdgcn_s_waitcnt((kL & 15) | (kL >> 4) << 14 | 0x0F70);
       else
         __builtin_amdgcn_s_waitcnt(0x0F70);
@@ -991,7 +987,8 @@ hipError_t product(const ProductArgs &all, hipStream_t s) {
       case kSmall: lds ? tiled<T, Small, true>(a, s) : tiled<T, Small, false>(a, s); break;
       case kMid: lds ? tiled<T, Mid, true>(a, s) : tiled<T, Mid, false>(a, s); break;
       case kThin: lds ? tiled<T, Thin, true>(a, s) : tiled<T, Thin, false>(a, s); break;
-      default: lds ? tiled<T, Thin2, true>(a, s) : tiled<T, Thin2, false>(a, s);
+      default:  // kThin2, which bf16 does not take
+        if constexpr (sizeof(T) == 4) lds ? tiled<T, Thin2, true>(a, s) : tiled<T, Thin2, false>(a, s);
     }
   }
   if (all.splits == 1) return hipGetLastError();

@@ -1,12 +1,15 @@
 """Which tiles the products take (product_plan.cpp, which runs on the host), built
 with g++ under AddressSanitizer and UndefinedBehaviorSanitizer: the sizes of the
-GPU tests take the forms that those tests are for."""
+GPU tests take the forms that those tests are for, and every product kernel of the
+library is one that some call takes."""
 import os
+import re
 import shutil
 import subprocess
 
 import pytest
 
+import muon_newton_schulz_03_amd as mu
 from ff_forms import BACKWARD, BOTH, FORWARD, GATED, STREAMING
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -55,3 +58,19 @@ def test_forms_of_the_sizes_named_in_comments(plan):
              (0, GATED, 1, 2331, 12, 532, 1024): MID, (0, FORWARD, 1, 4096, 1, 2048, 4096): SMALL}
     got = plan([], sizes)
     assert {size: g[0] for size, g in zip(sizes, got) if g[2] == 0} == sizes
+
+
+def test_every_kernel_is_reached(plan):
+    """The product kernels that the library was compiled with are those that some size takes."""
+    if shutil.which("nm") is None:
+        pytest.skip("nm not installed")
+    names = subprocess.run(["nm", mu.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    forms = {(2, 4, 4, 1, 128, 1): LARGE, (2, 4, 4, 1, 128, 0): LARGE, (1, 4, 4, 1, 64, 0): WIDE, (2, 2, 1, 1, 128, 0): SMALL,
+             (2, 1, 1, 2, 64, 0): MID, (1, 1, 1, 4, 128, 0): THIN, (1, 1, 1, 4, 64, 0): THIN2}
+    built = set()
+    for t, wm, wn, i, kk, _, row, stream, back, gated, direct, part in re.findall(
+            r"stub__product_kernelI(DF16b|f)NS0_4FormILi(\d)ELi(\d)ELi(\d)ELi(\d)ELi(\d)ELi(\d+)ELb(\d)EEELb(\d)ELb(\d)ELb(\d)ELb(\d)E", names):
+        form = forms[tuple(map(int, (wm, wn, i, kk, row, stream)))]
+        built.add((int(t != "f"), 2 if back == "1" else int(gated), int(direct), form, int(part)))
+    assert built
+    assert built == set(plan(["all"], []))
