@@ -132,6 +132,42 @@ def test_streaming_products_behind_a_captured_graph(gpu_lib):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("slots,groups,n,k", [(107, 3, 40, 72), (300, 5, 136, 264), (20000, 40, 520, 136), (3, 1, 24, 8200)])
+def test_gated_operands_of_one_buffer_and_of_differing_pitches(gpu_lib, slots, groups, n, k, fused, dtype):
+    """Both weights as halves of one buffer and the slots' matrices as halves of wide rows, or a pitch of its own for each operand."""
+    mu, g = gpu_lib, gen(slots + n + fused)
+    offsets = None if groups == 1 else uneven(g, slots, groups).to(torch.int32)
+    off, own = [0, slots] if groups == 1 else offsets.tolist(), torch.arange(slots, device="cuda")
+    used = own < off[-1]
+    if fused:
+        w, u = stack(g, groups, 2 * n, k, dtype).split(n, 1)
+        halves = [out_mat(slots, 2 * n, dtype) for _ in range(2)]
+        (gate, up), (dgate, dup) = (t.split(n, 1) for t in halves)
+        x, dh, h, dx = mat(randn(g, slots, k), dtype), mat(randn(g, slots, n), dtype), out_mat(slots, n, dtype), out_mat(slots, k, dtype)
+    else:
+        w, u = stack(g, groups, n, k, dtype, 16), stack(g, groups, n, k, dtype, 3)
+        x, dh = mat(randn(g, slots, k), dtype, 5), mat(randn(g, slots, n), dtype, 8)
+        h, gate, up, dgate, dup, dx = (out_mat(slots, c, dtype, e) for c, e in ((n, 1), (n, 8), (n, 0), (n, 16), (n, 24), (k, 7)))
+    mu.muon_gated_forward(x, w, u, h, gate, up, offsets)
+    mu.muon_gated_backward(dh, gate, up, w, u, dgate, dup, dx, offsets)
+    rg, mg = grouped64(x, w, off, own, False)
+    ru, mu_ = grouped64(x, u, off, own, False)
+    both(gate[used], rg[used], mg[used], dtype, k, "gate")
+    both(up[used], ru[used], mu_[used], dtype, k, "up")
+    D, G, V = dh.double(), gate.double(), up.double()
+    s = torch.sigmoid(G)
+    rdg, rdu = D * V * s * (1 + G * (1 - s)), D * G * s
+    near(dgate[used], rdg[used], (HALF[dtype] * rdg.abs() + 16 * U * (D * V).abs() * (1 + G.abs()))[used], "dgate")
+    near(dup[used], rdu[used], (HALF[dtype] * rdu.abs() + 16 * U * (D * G).abs())[used], "dup")
+    a, ma = grouped64(dgate, w, off, own, True)
+    b, mb = grouped64(dup, u, off, own, True)
+    both(dx[used], (a + b)[used], (ma + mb)[used], dtype, 2 * n, "dx")
+    for t in (h, gate, up, dgate, dup, dx):
+        assert bool((t[~used] == MARK).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("tokens,topk,experts,n,k", LONG)
 def test_shared_sums_in_norm(gpu_lib, tokens, topk, experts, n, k, dtype):
     """Long sums whose parts several workgroups make, as exact as float32 sums: parts or operands of fewer bits are not."""
