@@ -557,9 +557,10 @@ muon_status muon_combine_forward(const muon_mat *x, int32_t topk, const float *w
  *   dx of slot t topk + j = weights[t, j] d[t],
  *   dweights[t, j] = sum over columns of x[t topk + j] d[t]
  * (the residual's gradient is dy itself).
- *   rows      NULL: dx lies as x does. Else as muon_route_forward wrote them:
- *             row s of dx belongs to slot rows[s]; a row of dx whose slot is
- *             -1, and a slot that is nowhere in rows, is not written.
+ *   rows      NULL: dx lies as x does. Else as muon_route_forward wrote them,
+ *             no slot twice: row s of dx belongs to slot rows[s]; a row of dx
+ *             whose slot is -1, and a slot that is nowhere in rows, is not written.
+ *             Nor, with or without rows, is that of a choice below 0.
  *   dweights  tokens x topk, overwritten, 0 where indices is below 0
  *             (NULL-able: not computed, x is then not read).
  * Workspace with rows: muon_combine_workspace_size.

@@ -10,8 +10,8 @@
 // keyed by a seed, an offset in the counter's upper half. What is dropped
 // counts for nothing, whatever its value.
 //
-// Memory bounds both: each row of x moves once, and dy once for all of a
-// token's slots. A thread takes eight columns of a token; the loads of all its
+// Memory bounds both: each row of x moves once, and dy once for eight of a
+// token's slots (with more of them again for the next eight, generator included). A thread takes eight columns of a token; the loads of all its
 // rows go out before the generator's words are worked out, and what does not
 // count is masked afterwards: a branch per row would have the loads wait for each
 // other. The last run of a row starts eight columns before its end, whatever the

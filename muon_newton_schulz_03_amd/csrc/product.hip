@@ -14,16 +14,19 @@
 // bf16 makes products of v_mfma_f32_32x32x16_bf16, float32 of
 // v_mfma_f32_32x32x2_f32 (float32 products and sums; the four values of a
 // fragment's 16 bytes are four products): the same bytes in LDS, the same reads.
-// A long sum runs in one float32 accumulator, a short one's outputs are rounded
-// once, from it.
+// A sum runs in one float32 accumulator, or in two or four where as many sets of
+// waves share it (64x64 and 32x64 tiles), and in up to sixteen parts of those where
+// workgroups do; they are added in order, in float32, and outputs are rounded once.
 //
-// What bounds it. Few slots a group: the weights, each read once from HBM (32
-// tokens, 8 of 128 experts 768x2048: 53-62 us, 5.5 TB/s; 64 tokens, gated, two
-// dense 18432x7168: 107-112 us, 4.8 TB/s).
-// Many: the socket's power, at which the shader clock falls to 1.5-2 GHz with the
-// matrix units busy half the time (16384 tokens, 8 of 128 experts 768x2048, gated:
-// 850-940 us, 930 TFLOP/s beside 3 TB/s of HBM; 4096 tokens, dense 18432x7168: 1700-1810
-// us, 1200-1270 TFLOP/s, busy 69%). There every byte that is not moved counts: whole 128-byte
+// What bounds it. Few slots a group: the weights, each read once (32 tokens, 8 of
+// 128 experts 2048x768: 60-66 us among other calls, 53 us and 290 MB at 5.5 TB/s when
+// the last call's weights, of which the cache before HBM keeps a part, are the same; 64
+// tokens, gated, two dense 18432x7168: 107-112 us, 4.8 TB/s).
+// Many: the socket's power, at which the shader clock falls to 1.5-2 GHz, for one
+// group (4096 tokens, dense 18432x7168: 1700-1810 us, 1200-1270 TFLOP/s, matrix units
+// busy 69%); for many experts also what their tiles fetch again and that they
+// are not full (16384 tokens, 8 of 128 experts 768x2048, gated: 850-896 us, 930 TFLOP/s,
+// busy 50%, 2.34 GB read for 0.87 GB of operands). There every byte that is not moved counts: whole 128-byte
 // lines of the operands in a stage took 7% off, tiles that take up the next one's
 // loads before they store 3-4%. LDS reads meet no bank conflicts (under 0.1%).
 // float32: the matrix units (4096 tokens, 2048x4096: 521 us, 132 TFLOP/s of 154).

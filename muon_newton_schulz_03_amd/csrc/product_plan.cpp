@@ -17,7 +17,9 @@ namespace {
 //   a tile     3           1.2             1.8             1.3            3 (float32: 1.5)
 // the first figure that of a single tile. A 256 x 256 tile skips 32-row blocks
 // without slots, down to half its time; through registers it takes
-// a tenth more. What it chose against the next best, us:
+// a tenth more (the others' times there are not told apart, and whether a sum is shared
+// out is asked as if all went straight to LDS: the workspace's size is known from
+// the sizes alone). What it chose against the next best, us:
 //   one token, 8 of 128 experts 768x2048, gated     32 x 64   14.7    (64 x 64: 19)
 //   64 tokens, 18432x7168, gated, nothing shared    64 x 128  133     (64 x 64: 149)
 //   80 tokens, 8 of 89, 418x135, gated              128 x 256 13.7    (64 x 128: 18, 32 x 64: 40)
@@ -100,7 +102,7 @@ ProductForm product_form(const ProductArgs &a, bool bf16, bool lds) {
 // tiles: 16 tokens, 7168x18432, float32, 146 -> 123; 5 tokens, 7168x5408, 50 -> 43. Of one group's tiles
 // that go round the CUs more than a whole number of times, those left over are
 // shared out, two launches of their own: 64 tokens, 18432x7168, gated, 288 tiles
-// of 64 x 64 (256 of them take 92), 133 -> 107-112 us; float32, 348 tokens, 3686x4512,
+// of 64 x 128 (256 of them take 92), 133 -> 107-112 us; float32, 348 tokens, 3686x4512,
 // backward, 158 -> 136; 1152 tokens, 4096x7168, gated, 1130 -> 1064.
 void product_plan(ProductArgs &a, bool bf16) {
   a.splits = 1;

@@ -396,8 +396,9 @@ def near(got, ref, tol, what):
     assert not bool(bad.any()), f"{what}: {int(bad.sum())} off, worst {float(((got.double() - ref).abs() / tol.clamp(min=1e-300)).max()):.3g} of the tolerance"
 
 
-# tokens, topk, experts, n, k: streams of several tiles a workgroup (with one group and with many), two row halves, tiles of
-# every size; the same with rows that start on no 16-byte boundary
+# tokens, topk, experts, n, k: tiles of every size, two row halves, one group and many; the same with rows that start on no
+# 16-byte boundary. Of 256 x 256 tiles that stream there is the gated forward pass of 5000 tokens; the other kinds' are in
+# test_gpu_ff_forms.py.
 SIZES = [(9000, 1, 1, 2304, 128), (5000, 4, 40, 640, 192), (4000, 2, 600, 264, 64), (900, 8, 128, 256, 64), (2300, 1, 1, 2048, 64),
          (700, 1, 1, 1024, 256), (513, 3, 16, 200, 512), (60, 4, 64, 512, 320), (2, 1, 1, 4096, 1024), (9, 2, 35, 72, 2048),
          (8000, 1, 1, 2303, 127), (5000, 4, 40, 639, 191), (2300, 1, 1, 2047, 63), (1000, 2, 30, 201, 333), (3, 2, 9, 515, 1031)]
@@ -451,6 +452,7 @@ def test_products_of_every_size(gpu_lib, tokens, topk, experts, n, k, dtype):
         assert bool((y[~used] == MARK).all())
 
 
+# Its 70000 rows take 128 x 256 tiles by the plan as it is; tiles that stream whose sums end inside a step: test_gpu_ff_forms.py.
 @pytest.mark.parametrize("k", [33, 40, 63, 64, 65, 72, 96, 120, 129, 200])
 def test_products_whose_sum_ends_anywhere_in_a_step(gpu_lib, k):
     """The operands lie in buffers of NaN: nothing behind a sum's end takes part. Tiles that stream (enough rows for them),
@@ -505,7 +507,8 @@ def test_lists_without_groups(gpu_lib, tokens, n, k, dtype):
     near(h, v * u, HALF[dtype] * (v * u).abs() + 1.2 * e * (u.abs() + eu) + v.abs() * eu + 16 * U * (r * u).abs(), "gated")
 
 
-# tokens, topk, experts, width, length of the sum: few outputs of long sums, which several workgroups share
+# tokens, topk, experts, width, length of the sum: few outputs of long sums, which several workgroups share. The bounds below
+# are the worst case of each value; test_gpu_ff_forms.py holds the same sizes to float32 sums in norm.
 LONG = [(1, 1, 1, 5, 8192), (64, 1, 1, 520, 8192), (100, 3, 4, 129, 4095), (40, 1, 3, 72, 6001), (33, 2, 9, 64, 12288),
         (12, 2, 5, 72, 8001), (16, 2, 3, 264, 9000)]
 

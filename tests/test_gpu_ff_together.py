@@ -299,6 +299,7 @@ def test_operands_past_32_bits(gpu_lib):
     near(y, r, HALF[BF] * r.abs() + 258 * U * m, "far groups")
 
 
+# 2^27 threads in 2^19 workgroups, 32 rows each: grids past 2^20 workgroups are in test_gpu_ff_forms.py.
 def test_more_slots_than_one_launch_counts(gpu_lib):
     """Rows past 2^32 threads' worth: the last ones are those of a call on them alone."""
     mu, g = gpu_lib, gen(81)
