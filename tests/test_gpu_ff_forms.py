@@ -281,3 +281,30 @@ def test_products_of_more_than_2_20_tiles(gpu_lib):
         terms = w[lo:lo + 4096].float() * x[lo:lo + 4096].float()[:, None, :]
         ref, mag = terms.double().sum(2), terms.double().abs().sum(2)
         near(y[lo:lo + 4096], ref, HALF[BF] * ref.abs() + (2 * k + 2) * U * mag, lo)
+
+
+def test_empty_tensors_through_the_binding(gpu_lib):
+    """A rank without experts, or one that no token came to: nothing is written, nothing is refused."""
+    mu, g = gpu_lib, gen(94)
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    x, y, h = mat(randn(g, 8, 16), F32), out_mat(8, 24, F32), out_mat(8, 24, F32)
+    w, none = stack(g, 2, 24, 16, F32), torch.empty((0, 24, 16), device="cuda")
+    mu.muon_expert_forward(x, none, y, i32(1))
+    mu.muon_gated_forward(x, none, none, h, offsets=i32(1), rows=i32(8))
+    dx, grads = out_mat(8, 16, F32), [out_mat(8, 24, F32) for _ in range(2)]
+    mu.muon_expert_backward(y, none, dx, i32(1))
+    mu.muon_gated_backward(y, y, h, none, none, *grads, dx, i32(1), i32(8))
+    ckpt = mu.Checkpoint.empty(8, 16)
+    mu.muon_ckpt_save(x, ckpt)
+    mu.muon_ckpt_weight_grad(y, ckpt, none, i32(1))
+    # no slots: two groups of none, rows of no slots, dx of other rows
+    void = [torch.empty((0, 24), device="cuda") for _ in range(5)]
+    mu.muon_gated_forward(x, w, w, void[0], void[1], void[2], i32(3), i32(0), 2)
+    mu.muon_gated_backward(*void[:3], w, w, *void[3:], dx, i32(3), i32(0))
+    mu.muon_expert_forward(x, w, y, i32(3), i32(0), gather=1, scatter=True)
+    mu.muon_expert_backward(void[0], w, dx, i32(3), i32(0), scatter=True)
+    for t in (y, h, dx, *grads):
+        assert bool((t == MARK).all())
+    for call, a, b in ((mu.muon_expert_forward, x, y), (mu.muon_expert_backward, y, dx)):
+        with pytest.raises(ValueError, match="rows: needed"):
+            call(a, w, b, i32(3), gather=1, scatter=True)
